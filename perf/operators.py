@@ -271,7 +271,7 @@ def run(s):
                          slot_weights=s.get("sums"), slot_weights_in=s.get("weights"), workspace=s["workspace"])
         return got + (s["sums"],) if case["weights"] else got
     kvc.evict(s["cache"], s["table"], s["lengths"], s["weights"], case["keep"], recent=case["recent"], births=s["births"],
-              lengths_out=s["lengths_out"], kept=s["kept"], weights_out=s["weights_out"], births_out=s["births_out"],
+              lengths_out=s["lengths_out"], kept=s["kept"], slot_weights_out=s["weights_out"], births_out=s["births_out"],
               workspace=s["workspace"])
     return s["cache"], s["lengths_out"], s["kept"], s["weights_out"], s["births_out"]
 
