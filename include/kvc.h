@@ -292,6 +292,121 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
                           int32_t out_dtype, void* stream);
 
 /*
+ * Attention of one new token per request over the packed slots of its pages.
+ * A slot's 512-vector k (decoded exactly, as kvc_dequantize does) is the key
+ * and the value of every head.  For request r, head h and its slots
+ * n < lengths[r], slot n lying in page page_table[r, n / 64] at n % 64:
+ *   s_n = scale * q[r, h] . k_n
+ *   L   = log(sum_n exp(s_n) + exp(sinks[h]))        (no sinks: without that term)
+ *   out[r, h] = sum_n exp(s_n - L) k_n,  lse[r, h] = L
+ *   slot_weights[r, n] = slot_weights_in[r, n] + sum_h exp(s_n - L_h)
+ * A row that sees no key (length 0 or every score -inf, and no sink) is zeros
+ * with lse -inf and adds nothing to the weights.  Scores, sums and results
+ * are formed in fp32; the softmax weights are rounded to bf16 for the product
+ * with the values, and out to bf16 at the end.
+ *
+ * q            bf16, head h of request r at q + r * q_req_stride + h *
+ *              q_head_stride (elements, multiples of 8), 16-byte aligned.
+ * num_heads    1 .. 128.
+ * kv_cache     uint8 [num_kv_pages, 37376], 16-byte aligned, read only.
+ * page_table   int32 [num_reqs, max_pages_per_req] at row stride
+ *              page_table_row_stride; only the entries below
+ *              ceil(lengths[r] / 64) are read.  Requests may share pages.
+ * lengths      int32 [num_reqs], 0 .. max_pages_per_req * 64.
+ * scale        finite.
+ * sinks        fp32 [num_heads] or NULL.
+ * out          bf16 [num_reqs, num_heads, 512], 16-byte aligned.
+ * lse          fp32 [num_reqs, num_heads] or NULL.
+ * slot_weights fp32 [num_reqs, max_slots] at its row stride, or NULL; entries
+ *              at and behind lengths[r] are left as they were.
+ * slot_weights_in  fp32 of the same shape at its row stride, or NULL for
+ *              zeros; may be slot_weights itself (accumulation in place).
+ * max_slots    columns of slot_weights (not read without it).
+ * workspace    kvc_attend_workspace_bytes(...) bytes, 16-byte aligned, of any
+ *              contents.  Calls that may overlap need one each, and so do
+ *              captured graphs whose replays may.
+ * flags        bits 0..15 force the number of CTAs that share the slots (0:
+ *              automatic); other bits must be zero.
+ *
+ * A length outside its range (or above max_slots), or a page outside the
+ * cache, records KVC_ERR_BAD_INDEX in the device error word and leaves that
+ * request's out, lse and slot_weights as they were; the other requests are
+ * computed.  The same inputs give the same bits on every call.  num_reqs at
+ * most 65535.  Allocates nothing.
+ */
+size_t kvc_attend_workspace_bytes(int64_t num_reqs, int32_t num_heads, int64_t max_pages_per_req,
+                                  int32_t with_slot_weights);
+kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride,
+                      int64_t num_reqs, int32_t num_heads,
+                      const uint8_t* kv_cache, int64_t num_kv_pages,
+                      const int32_t* page_table, int64_t max_pages_per_req,
+                      int64_t page_table_row_stride, const int32_t* lengths,
+                      float scale, const float* sinks, void* out, float* lse,
+                      const float* slot_weights_in, int64_t slot_weights_in_row_stride,
+                      float* slot_weights, int64_t slot_weights_row_stride, int64_t max_slots,
+                      void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+
+/*
+ * Join of attention parts whose softmax ran over disjoint sets of keys (the
+ * packed slots and the tokens not yet packed, or one cache with several
+ * owners):
+ *   L = log(sum_i exp(lses[i][row])),
+ *   out[row] = sum_i exp(lses[i][row] - L) outs[i][row],  lse[row] = L.
+ * A part with lse -inf held no key: its row is not read into the sum.  A row
+ * that no part holds is zeros with lse -inf.
+ *
+ * outs   host array of num_parts (1 .. 8) device pointers, each [num_rows,
+ *        512] of element type dtype (KVC_DTYPE_*), 16-byte aligned.
+ * lses   host array of device pointers, each fp32 [num_rows].
+ * out    [num_rows, 512] of the same type; may be one of outs.
+ * lse    fp32 [num_rows] or NULL; may be one of lses.
+ */
+kvc_status kvc_join(const void* const* outs, const float* const* lses, int32_t num_parts,
+                    int64_t num_rows, int32_t dtype, void* out, float* lse, void* stream);
+
+/*
+ * Evict the slots of each request that gathered the least attention.  Of the
+ * slots n < lengths[r], min(keep, lengths[r]) stay: first those of the
+ * `recent` newest births (births[r, n] > max birth - recent), then those of
+ * largest slot_weights[r, n]; the lowest index first among equals, NaN below
+ * every value.  With new = min(keep, lengths[r]), a slot n < new that stays
+ * keeps its place, and the i-th place below `new` that falls free takes the
+ * i-th slot that stays from behind it: the fewest slots move.  The order of
+ * slots is not preserved (attention does not depend on it); births tell
+ * their ages.
+ *
+ * kv_cache     uint8 [num_kv_pages, 37376]; the moved slots' 576 + 8 bytes
+ *              are written at their new places, all other bytes left alone.
+ *              No page may belong to two requests of the call.
+ * page_table, lengths   as for kvc_attend.
+ * slot_weights fp32 [num_reqs, max_slots] at its row stride.
+ * births       int32 of the same shape at its row stride, or NULL if recent
+ *              is 0: numbers that grow from slot to slot in the order they
+ *              were added (for instance the index of the window).
+ * keep         slots to keep, >= 0;  recent  0 .. keep.
+ * lengths_out  int32 [num_reqs], receives `new`; may be lengths itself.
+ * kept         int32 [num_reqs, keep] or NULL: the former place of the slot
+ *              now at each place, -1 from `new` on.
+ * slot_weights_out, births_out   optional [num_reqs, >= min(keep, max_slots)]
+ *              at their row strides: the arrays in the new order, left as
+ *              they were from `new` on; may be slot_weights and births.
+ * workspace    kvc_evict_workspace_bytes(...) bytes, as for kvc_attend.
+ *
+ * A bad length or page is treated as in kvc_attend: that request, its row of
+ * every output included, stays as it was.  num_reqs at most 65535.
+ */
+size_t kvc_evict_workspace_bytes(int64_t num_reqs, int64_t max_pages_per_req, int64_t keep);
+kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* page_table,
+                     int64_t num_reqs, int64_t max_pages_per_req,
+                     int64_t page_table_row_stride, const int32_t* lengths,
+                     const float* slot_weights, int64_t slot_weights_row_stride,
+                     int64_t max_slots, const int32_t* births, int64_t births_row_stride,
+                     int64_t keep, int64_t recent, int32_t* lengths_out, int32_t* kept,
+                     float* slot_weights_out, int64_t slot_weights_out_row_stride,
+                     int32_t* births_out, int64_t births_out_row_stride,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kvc_compress without a workspace argument, for callers that cannot
  * allocate device memory: plugins that are handed only their input and
  * output pointers, engines that reserve the whole device memory pool up front

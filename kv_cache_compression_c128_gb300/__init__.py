@@ -25,7 +25,7 @@ _INCLUDE = os.path.join(_ROOT, "include")
 _LIB_DIR = os.path.join(_HERE, "_lib")
 LIB_PATH = os.path.join(_LIB_DIR, "libkvc.so")
 _SOURCES = ["kvc_cluster.cu", "kvc_streamk.cu", "kvc_reader.cu", "kvc_api.cu", "kvc_static.cu",
-            "kvc_selftest.cu"]
+            "kvc_selftest.cu", "kvc_attend.cu", "kvc_join.cu", "kvc_evict.cu", "kvc_operators.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 KVC_OK = 0
@@ -156,6 +156,20 @@ def lib():
                 P, I32, I64, I64, I64, P, P, I64, P, I64, P, I64, I64, I64, I64, P, P, I64, P,
                 I64, P, I64, I32, I32, ctypes.c_float, P, P, ctypes.c_size_t, U32, P]
             L.kvc_compress_strided.restype = ctypes.c_int
+            L.kvc_attend_workspace_bytes.argtypes = [I64, I32, I64, I32]
+            L.kvc_attend_workspace_bytes.restype = ctypes.c_size_t
+            L.kvc_attend.argtypes = [
+                P, I64, I64, I64, I32, P, I64, P, I64, I64, P, ctypes.c_float, P, P, P, P, I64,
+                P, I64, I64, P, ctypes.c_size_t, U32, P]
+            L.kvc_attend.restype = ctypes.c_int
+            L.kvc_join.argtypes = [P, P, I32, I64, I32, P, P, P]
+            L.kvc_join.restype = ctypes.c_int
+            L.kvc_evict_workspace_bytes.argtypes = [I64, I64, I64]
+            L.kvc_evict_workspace_bytes.restype = ctypes.c_size_t
+            L.kvc_evict.argtypes = [
+                P, I64, P, I64, I64, I64, P, P, I64, I64, P, I64, I64, I64, P, P, P, I64, P, I64,
+                P, ctypes.c_size_t, P]
+            L.kvc_evict.restype = ctypes.c_int
             L.kvc_query_launch.argtypes = [I64, I32, U32, P, P, P, P]
             L.kvc_query_launch.restype = ctypes.c_int
             L.kvc_query_launch_ex.argtypes = [I64, I32, I32, U32, P, P, P, P]
@@ -355,6 +369,49 @@ def kvc_dequantize(kv_cache, num_kv_pages, slots, num_slots, out, out_dtype, str
     v = ctypes.c_void_p
     return int(lib().kvc_dequantize(v(kv_cache), num_kv_pages, v(slots), num_slots, v(out),
                                     int(out_dtype), v(stream)))
+
+
+def kvc_attend_workspace_bytes(num_reqs: int, num_heads: int, max_pages_per_req: int,
+                               with_slot_weights: bool = False) -> int:
+    return int(lib().kvc_attend_workspace_bytes(int(num_reqs), int(num_heads),
+                                                int(max_pages_per_req), int(with_slot_weights)))
+
+
+def kvc_attend(q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, num_kv_pages,
+               page_table, max_pages_per_req, page_table_row_stride, lengths, scale, sinks, out,
+               lse, slot_weights_in, slot_weights_in_row_stride, slot_weights,
+               slot_weights_row_stride, max_slots, workspace, workspace_bytes, flags,
+               stream) -> int:
+    """Attention over packed slots (raw integer pointers); returns the status."""
+    return lib().kvc_attend(
+        q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, num_kv_pages, page_table,
+        max_pages_per_req, page_table_row_stride, lengths, scale, sinks, out, lse,
+        slot_weights_in, slot_weights_in_row_stride, slot_weights, slot_weights_row_stride,
+        max_slots, workspace, workspace_bytes, flags, stream)
+
+
+def kvc_join(outs, lses, num_rows, dtype, out, lse, stream) -> int:
+    """Join of attention parts; outs and lses are sequences of integer device
+    pointers.  Returns the status."""
+    arr = ctypes.c_void_p * len(outs)
+    return lib().kvc_join(arr(*outs), arr(*lses), len(outs), num_rows, dtype, out, lse, stream)
+
+
+def kvc_evict_workspace_bytes(num_reqs: int, max_pages_per_req: int, keep: int) -> int:
+    return int(lib().kvc_evict_workspace_bytes(int(num_reqs), int(max_pages_per_req), int(keep)))
+
+
+def kvc_evict(kv_cache, num_kv_pages, page_table, num_reqs, max_pages_per_req,
+              page_table_row_stride, lengths, slot_weights, slot_weights_row_stride, max_slots,
+              births, births_row_stride, keep, recent, lengths_out, kept, slot_weights_out,
+              slot_weights_out_row_stride, births_out, births_out_row_stride, workspace,
+              workspace_bytes, stream) -> int:
+    """Eviction of packed slots (raw integer pointers); returns the status."""
+    return lib().kvc_evict(
+        kv_cache, num_kv_pages, page_table, num_reqs, max_pages_per_req, page_table_row_stride,
+        lengths, slot_weights, slot_weights_row_stride, max_slots, births, births_row_stride,
+        keep, recent, lengths_out, kept, slot_weights_out, slot_weights_out_row_stride,
+        births_out, births_out_row_stride, workspace, workspace_bytes, stream)
 
 
 # ---- torch-facing wrappers ----------------------------------------------------
@@ -576,3 +633,264 @@ def compress_layers(state_caches, token_to_req, positions, boundary_token_indice
     if st != KVC_OK:
         raise KvcError(st, name)
     return kv_caches
+
+
+# ---- operators on packed slots ------------------------------------------------
+
+def _operator_checks():
+    """torch and the (name, tensor, dtype, dim, device) check of the operators
+    below: columns contiguous, rows at any stride."""
+    import torch
+
+    def check(name, t, dtype, dim, dev):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.dim() != dim:
+            raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name} must have contiguous columns")
+
+    return torch, check
+
+
+class _on:
+    """Context of an operator call: its device current, and its stream too
+    while results and workspaces are allocated (memory of another stream's
+    pool could still be in use there)."""
+
+    def __init__(self, torch, dev, stream):
+        self.torch, self.stream, self.entered = torch, stream, []
+        if torch.cuda.current_device() != dev.index:
+            self.entered.append(torch.cuda.device(dev))
+        if stream is not None:
+            self.entered.append(torch.cuda.stream(stream))
+        self.dev = dev
+
+    def __enter__(self):
+        for c in self.entered:
+            c.__enter__()
+        s = self.stream if self.stream is not None else self.torch.cuda.current_stream(self.dev)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.entered):
+            c.__exit__(*exc)
+
+
+def _check_cache(check, torch, kv_cache, page_table, lengths):
+    dev = kv_cache.device
+    if dev.type != "cuda":
+        raise ValueError("kv_cache must be a CUDA tensor (there is no CPU path)")
+    check("kv_cache", kv_cache, torch.uint8, 2, dev)
+    if kv_cache.shape[1] != KV_PAGE_BYTES or not kv_cache.is_contiguous():
+        raise ValueError(f"kv_cache must be contiguous [num_pages, {KV_PAGE_BYTES}] uint8")
+    check("page_table", page_table, torch.int32, 2, dev)
+    check("lengths", lengths, torch.int32, 1, dev)
+    if lengths.shape[0] != page_table.shape[0]:
+        raise ValueError("page_table and lengths must have one row per request")
+    return dev
+
+
+def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None, lse=None,
+           slot_weights=None, slot_weights_in=None, flags: int = 0, stream=None, workspace=None):
+    """Attention of one new token per request over its packed slots.
+
+    q bf16 [R, H, 512] (any request and head strides that are multiples of 8
+    elements, columns contiguous; H up to 128); kv_cache uint8 [pages, 37376];
+    page_table int32 [R, max_pages] (any row stride), 64 slots to a page;
+    lengths int32 [R], slots of each request.  A slot's decoded vector is the
+    key and the value of every head; `scale` defaults to 512 ** -0.5; optional
+    sinks fp32 [H] join the softmax as a score without a value.
+
+    Returns (out bf16 [R, H, 512], lse fp32 [R, H]).  With slot_weights (fp32
+    [R, S]), entry [r, n] of every slot also receives slot_weights_in[r, n]
+    (zero without it; may be the same tensor) plus the slot's softmax weight
+    summed over the heads: what `evict` goes by.  A request whose length or
+    pages are out of range keeps its rows as they were and raises the device
+    error word (kvc_get_device_error).
+    """
+    torch, check = _operator_checks()
+    dev = _check_cache(check, torch, kv_cache, page_table, lengths)
+    check("q", q, torch.bfloat16, 3, dev)
+    R, H, D = q.shape
+    if D != HEAD_DIM or not 1 <= H <= 128:
+        raise ValueError("q must be [num_reqs, 1..128 heads, 512]")
+    if page_table.shape[0] != R:
+        raise ValueError("q and page_table must have one row per request")
+    if sinks is not None:
+        check("sinks", sinks, torch.float32, 1, dev)
+        if sinks.shape[0] != H:
+            raise ValueError("sinks must have one entry per head")
+    S = 0
+    if slot_weights is not None:
+        check("slot_weights", slot_weights, torch.float32, 2, dev)
+        S = slot_weights.shape[1]
+        if slot_weights.shape[0] != R:
+            raise ValueError("slot_weights must have one row per request")
+    if slot_weights_in is not None:
+        check("slot_weights_in", slot_weights_in, torch.float32, 2, dev)
+        if slot_weights is None or slot_weights_in.shape != slot_weights.shape:
+            raise ValueError("slot_weights_in needs slot_weights of the same shape")
+    with _on(torch, dev, stream) as sp:
+        if out is None:
+            out = torch.empty((R, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        else:
+            check("out", out, torch.bfloat16, 3, dev)
+            if out.shape != q.shape or not out.is_contiguous():
+                raise ValueError("out must be contiguous [num_reqs, num_heads, 512]")
+        if lse is None:
+            lse = torch.empty((R, H), dtype=torch.float32, device=dev)
+        else:
+            check("lse", lse, torch.float32, 2, dev)
+            if lse.shape != q.shape[:2] or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous [num_reqs, num_heads]")
+        if R == 0 or page_table.shape[1] == 0:
+            if R != 0:
+                raise ValueError("page_table must have at least one column")
+            return out, lse
+        if workspace is None:
+            workspace = torch.empty(
+                kvc_attend_workspace_bytes(R, H, page_table.shape[1], slot_weights is not None),
+                dtype=torch.uint8, device=dev)
+        else:
+            check("workspace", workspace, torch.uint8, 1, dev)
+        st = kvc_attend(
+            q.data_ptr(), q.stride(0), q.stride(1), R, H, kv_cache.data_ptr(), kv_cache.shape[0],
+            page_table.data_ptr(), page_table.shape[1], page_table.stride(0), lengths.data_ptr(),
+            HEAD_DIM ** -0.5 if scale is None else scale,
+            None if sinks is None else sinks.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            None if slot_weights_in is None else slot_weights_in.data_ptr(),
+            0 if slot_weights_in is None else slot_weights_in.stride(0),
+            None if slot_weights is None else slot_weights.data_ptr(),
+            0 if slot_weights is None else slot_weights.stride(0), S, workspace.data_ptr(),
+            workspace.numel(), flags, sp)
+    if st != KVC_OK:
+        raise KvcError(st, "kvc_attend")
+    return out, lse
+
+
+def join(outs, lses, *, out=None, lse=None, stream=None):
+    """Join attention parts whose softmax ran over disjoint keys.
+
+    outs: 1 to 8 contiguous [..., 512] tensors, all bf16 or all fp32, of one
+    shape; lses: as many contiguous fp32 tensors of that shape without the 512
+    (-inf: the part held no key for the row).  Returns (out, lse); `out` may
+    be one of outs and `lse` one of lses.
+    """
+    torch, check = _operator_checks()
+    if not 1 <= len(outs) <= 8 or len(lses) != len(outs):
+        raise ValueError("outs and lses need one entry per part, 1 to 8 parts")
+    first = outs[0]
+    dev, dtype, shape = first.device, first.dtype, first.shape
+    if dev.type != "cuda":
+        raise ValueError("outs must be CUDA tensors (there is no CPU path)")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("outs must have dtype torch.float32 or torch.bfloat16")
+    if len(shape) < 1 or shape[-1] != HEAD_DIM:
+        raise ValueError("outs must be [..., 512]")
+
+    def same(name, t, dt, sh):
+        check(name, t, dt, len(sh), dev) if len(sh) else None
+        if t.shape != sh or t.dtype != dt or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {tuple(sh)} {dt} on {dev}")
+
+    for i in range(len(outs)):
+        same(f"outs[{i}]", outs[i], dtype, shape)
+        same(f"lses[{i}]", lses[i], torch.float32, shape[:-1])
+    with _on(torch, dev, stream) as sp:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            same("out", out, dtype, shape)
+        if lse is None:
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        else:
+            same("lse", lse, torch.float32, shape[:-1])
+        st = kvc_join([t.data_ptr() for t in outs], [t.data_ptr() for t in lses], lse.numel(),
+                      KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32,
+                      out.data_ptr(), lse.data_ptr(), sp)
+    if st != KVC_OK:
+        raise KvcError(st, "kvc_join")
+    return out, lse
+
+
+def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0, births=None,
+          lengths_out=None, kept=None, slot_weights_out=None, births_out=None, stream=None,
+          workspace=None):
+    """Evict, in place, the slots that gathered the least attention.
+
+    Of the first lengths[r] slots of request r, min(keep, lengths[r]) stay:
+    the `recent` newest by birth number (births int32 [R, S], needed if recent
+    > 0), then those of largest slot_weights[r, n] (fp32 [R, S]), the lowest
+    index first among equals, NaN last.  Slots that stay below the new length
+    keep their places; the i-th place that falls free takes the i-th slot that
+    stays from behind.  The slots' bytes move within kv_cache; no page may
+    belong to two requests.
+
+    Returns (lengths_out int32 [R], kept int32 [R, keep]): the new lengths,
+    and the former place of the slot at each place (-1 behind the new length).
+    slot_weights_out and births_out, if given, receive those arrays in the new
+    order (entries behind the new length are left as they were).  lengths_out,
+    slot_weights_out and births_out may be the inputs themselves.
+    """
+    torch, check = _operator_checks()
+    dev = _check_cache(check, torch, kv_cache, page_table, lengths)
+    R, keep, recent = lengths.shape[0], int(keep), int(recent)
+    if keep < 0 or not 0 <= recent <= keep:
+        raise ValueError("keep must be >= 0 and recent between 0 and keep")
+    check("slot_weights", slot_weights, torch.float32, 2, dev)
+    S = slot_weights.shape[1]
+    if slot_weights.shape[0] != R:
+        raise ValueError("slot_weights must have one row per request")
+    if births is not None:
+        check("births", births, torch.int32, 2, dev)
+        if births.shape != slot_weights.shape:
+            raise ValueError("births must have the shape of slot_weights")
+    elif recent > 0 or births_out is not None:
+        raise ValueError("recent and births_out need births")
+    for name, t, dt in (("slot_weights_out", slot_weights_out, torch.float32),
+                        ("births_out", births_out, torch.int32)):
+        if t is not None:
+            check(name, t, dt, 2, dev)
+            if t.shape[0] != R or t.shape[1] < min(keep, S):
+                raise ValueError(f"{name} must be [num_reqs, at least min(keep, slots)]")
+    with _on(torch, dev, stream) as sp:
+        if lengths_out is None:
+            lengths_out = torch.empty_like(lengths)
+        else:
+            check("lengths_out", lengths_out, torch.int32, 1, dev)
+            if lengths_out.shape[0] != R:
+                raise ValueError("lengths_out must have one entry per request")
+        if kept is None:
+            kept = torch.empty((R, keep), dtype=torch.int32, device=dev)
+        else:
+            check("kept", kept, torch.int32, 2, dev)
+            if kept.shape != (R, keep) or not kept.is_contiguous():
+                raise ValueError("kept must be contiguous [num_reqs, keep]")
+        if R == 0 or page_table.shape[1] == 0:
+            if R != 0:
+                raise ValueError("page_table must have at least one column")
+            return lengths_out, kept
+        if workspace is None:
+            workspace = torch.empty(kvc_evict_workspace_bytes(R, page_table.shape[1], keep),
+                                    dtype=torch.uint8, device=dev)
+        else:
+            check("workspace", workspace, torch.uint8, 1, dev)
+        st = kvc_evict(
+            kv_cache.data_ptr(), kv_cache.shape[0], page_table.data_ptr(), R, page_table.shape[1],
+            page_table.stride(0), lengths.data_ptr(), slot_weights.data_ptr(),
+            slot_weights.stride(0), S, None if births is None else births.data_ptr(),
+            0 if births is None else births.stride(0), keep, recent, lengths_out.data_ptr(),
+            kept.data_ptr() if keep else None,
+            None if slot_weights_out is None else slot_weights_out.data_ptr(),
+            0 if slot_weights_out is None else slot_weights_out.stride(0),
+            None if births_out is None else births_out.data_ptr(),
+            0 if births_out is None else births_out.stride(0), workspace.data_ptr(),
+            workspace.numel(), sp)
+    if st != KVC_OK:
+        raise KvcError(st, "kvc_evict")
+    return lengths_out, kept

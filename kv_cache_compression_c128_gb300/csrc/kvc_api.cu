@@ -13,6 +13,7 @@
 
 #include "../../include/kvc.h"
 #include "kvc_internal.h"
+#include "kvc_operators.h"
 
 namespace {
 
@@ -210,6 +211,19 @@ bool pick_route(const DeviceInfo& d, int64_t N, int64_t K, bool streamk_ok, doub
 }
 
 }  // namespace
+
+namespace kvc {
+
+kvc_status operator_device(int* sms, uint32_t** error_word) {
+  DeviceInfo d;
+  const kvc_status st = device_info(&d);
+  if (st != KVC_OK) return st;
+  *sms = d.sms;
+  *error_word = d.error_word;
+  return KVC_OK;
+}
+
+}  // namespace kvc
 
 extern "C" {
 

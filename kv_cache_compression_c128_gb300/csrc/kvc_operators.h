@@ -1,0 +1,81 @@
+// Internal interface between the C entry points of the operators on packed
+// slots (kvc_operators.cu: attend, join, evict) and their kernels.  Not part
+// of the ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+constexpr int kMaxHeads = 128;
+constexpr int kMaxParts = 8;
+
+struct AttendParams {
+  const uint16_t* q;  // bf16, head h of request r at r * q_req_stride + h * q_head_stride
+  int64_t q_req_stride, q_head_stride;
+  int64_t num_reqs;
+  int num_heads;
+  const uint8_t* kv_cache;
+  int64_t num_pages;
+  const int32_t* page_table;
+  int64_t max_pages, page_table_row_stride;
+  const int32_t* lengths;
+  int64_t max_slots;  // a longer request is a bad index
+  float scale;
+  const float* sinks;  // [num_heads] or null
+  uint16_t* out;       // bf16 [num_reqs, num_heads, 512]
+  float* lse;          // [num_reqs, num_heads]
+  const float* weights_in;  // null: zeros
+  float* weights_out;       // null: not wanted
+  int64_t weights_in_row_stride, weights_out_row_stride;
+  uint32_t* error;
+};
+
+struct JoinParams {
+  const void* outs[kMaxParts];
+  const float* lses[kMaxParts];
+  int num_parts;
+  int64_t num_rows;
+  int bf16;
+  void* out;
+  float* lse;  // null: not wanted
+};
+
+struct EvictParams {
+  uint8_t* kv_cache;
+  int64_t num_pages;
+  const int32_t* page_table;
+  int64_t num_reqs, page_table_row_stride;
+  const int32_t* lengths;
+  int64_t max_slots;  // a longer request is a bad index
+  const float* weights;
+  int64_t weights_row_stride;
+  const int32_t* births;  // null: none
+  int64_t births_row_stride;
+  int64_t keep, recent;
+  int32_t* lengths_out;
+  int32_t* kept;  // [num_reqs, keep] or null
+  float* weights_out;
+  int64_t weights_out_row_stride;
+  int32_t* births_out;
+  int64_t births_out_row_stride;
+  int32_t* counts;  // workspace: moves of each request
+  int32_t* moves;   // workspace: per request, move_stride holes and move_stride movers
+  int64_t move_stride;
+  uint32_t* error;
+};
+
+cudaError_t launch_attend(const AttendParams& p, cudaStream_t stream);
+cudaError_t launch_join(const JoinParams& p, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+
+// The current device's set-up (kvc_api.cu): its SM count and the address of
+// its error word.
+kvc_status operator_device(int* sms, uint32_t** error_word);
+
+}  // namespace kvc
