@@ -214,12 +214,13 @@ bool pick_route(const DeviceInfo& d, int64_t N, int64_t K, bool streamk_ok, doub
 
 namespace kvc {
 
-kvc_status operator_device(int* sms, uint32_t** error_word) {
+kvc_status operator_device(int* sms, uint32_t** error_word, long long* wait_limit) {
   DeviceInfo d;
   const kvc_status st = device_info(&d);
   if (st != KVC_OK) return st;
   *sms = d.sms;
   *error_word = d.error_word;
+  *wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   return KVC_OK;
 }
 

@@ -8,130 +8,921 @@
 //   weights_out[r, n] = weights_in[r, n] + sum_h exp(s_n - L_h).
 // A row that sees no key (no slots, or every score -inf, and no sink) is
 // zeros with lse -inf.
+//
+// One page (64 slots) at a time, with the slots and dims on the rows of the
+// tensor core's tiles and the heads on their columns, so that the time of a
+// page falls with the number of heads (padded to N = 16, 32 or 64; more heads
+// make several groups):
+//   S[slot, head]  = K[64 x 512] Q^T              (M 64,  N heads, K 512)
+//   O[dim, head]  += K^T[128 dims x 64] P, 4 times (M 128, N heads, K 64)
+// K is decoded to bf16 (exact) once, into shared memory with the 128-byte
+// swizzle; the same bytes serve the first product with the dims innermost and
+// the second one transposed.  S (2 buffers) and O are fp32 in tensor memory.
+// P = 2^(s - m) goes to shared memory in bf16: its rounding is of the size of
+// the output's own, and the sum l that divides is taken before it.  m is a
+// column's reference, not its running maximum: any m serves as long as 2^(s - m)
+// stays in range, so O is rescaled only where a score exceeds m by 2^32.
+//
+// Warps of a CTA: 0..3 softmax and epilogue, 4..11 decode, 12 issues the
+// products.  The pages of all (request, head group) units are laid end to end
+// and cut into equal shares, one per CTA; a unit that a cut divides leaves its
+// parts (m, l, O) in the workspace, and a second kernel joins them in the order
+// of the shares, so the same lengths give the same bits.  That kernel also
+// forms the slots' weights, from the scores that the first one left behind.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
 #include "kvc_decode.cuh"
+#include "kvc_device.cuh"
 #include "kvc_internal.h"
 #include "kvc_operators.h"
 
 namespace kvc {
 namespace {
 
-constexpr uint32_t kErrBadIndexAttend = 4;
-constexpr int kRowThreads = kHeadDim / 4;
+using dev::kErrBadIndex;
+using dev::kErrTimeout;
+using dev::kLog2e;
+using dev::smem_addr;
 
-// Four dims d0 .. d0 + 3 of slot n of a request's pages.
-__device__ __forceinline__ void read4(const AttendParams& p, const int32_t* table, int n, int d0,
-                                      float v[4]) {
-  const uint8_t* page = p.kv_cache + table[n / kSlotsPerPage] * kPageBytes;
-  const int off = n % kSlotsPerPage;
-  if (d0 < kNopeDim) {
-    const uint32_t codes = *reinterpret_cast<const uint32_t*>(page + off * kTokenStride + d0);
-    decode4(codes, half_scale(page[kScaleBase + off * kScaleDim + d0 / kGroup]), v);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(page + off * kTokenStride + kNopeDim +
-                                                    2 * (d0 - kNopeDim));
-    v[0] = __uint_as_float(w.x << 16);
-    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(w.y << 16);
-    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+constexpr int kSoftmaxWarps = 4, kDecodeWarps = 8;
+constexpr int kSoftmaxThreads = kSoftmaxWarps * 32, kDecodeThreads = kDecodeWarps * 32;
+constexpr int kIssueWarp = kSoftmaxWarps + kDecodeWarps;
+constexpr int kAttendThreads = (kIssueWarp + 1) * 32;
+constexpr int kKeyBlock = kSlotsPerPage * 128;          // 64 slots x 64 dims, bf16
+constexpr int kKeyStage = 8 * kKeyBlock;                // a decoded page
+constexpr float kRescaleAbove = 32.f;                   // log2
+constexpr int kJoinThreads = 128;
+constexpr int kWeightSlots = 64;                        // slots per CTA of its weights part
+
+struct Barriers {
+  unsigned long long kv_full[2], kv_empty[2], s_full[2], p_full[2], q_empty, o_full, drain;
+};
+
+template <int N>
+struct AttendShared {
+  alignas(1024) uint8_t keys[2][kKeyStage];
+  alignas(1024) uint8_t q[N * 1024];
+  alignas(1024) uint8_t p[2][kSlotsPerPage * 2 * N];
+  float red[kSoftmaxWarps][N];
+  float ref[N], factor[N];
+  Barriers bar;
+  long long scan[kAttendThreads / 32];
+  long long total;
+  int start_req;
+  long long start_off;
+  uint32_t tmem;
+  int bad[4];
+  volatile int abort;
+};
+
+// ---- tensor core and tensor memory ---------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Arrives on `bar` once every product issued so far by this thread is done.
+__device__ __forceinline__ void tc_commit(unsigned long long* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+// Shared-memory operand: start and the two strides in bytes, swizzle 2 (128
+// bytes), 4 (64) or 6 (32).  Rows innermost (dims of a slot for the first
+// product): `sbo` between groups of 8 rows.  Columns innermost (the second
+// product): `lbo` between swizzle rows' widths along the columns, `sbo`
+// between groups of 8 along the summed axis.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) |
+         (static_cast<uint64_t>(swizzle) << 61);
+}
+
+// fp32 accumulator, bf16 operands; `transposed`: both with their columns innermost.
+__host__ __device__ constexpr uint32_t instruction(int m, int n, bool transposed) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (transposed ? (1u << 15) | (1u << 16) : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+#define KVC_R4(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
+#define KVC_R16(v, i) KVC_R4(v, i), KVC_R4(v, i + 4), KVC_R4(v, i + 8), KVC_R4(v, i + 12)
+
+// 16 lanes x 16 columns: thread t gets columns 2 (t % 4) + {0, 1} of each 8,
+// of lane t / 4 (values 0, 1) and t / 4 + 8 (values 2, 3).
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : KVC_R4(v, 0), KVC_R4(v, 4)
+               : "r"(addr));
+}
+
+// 32 lanes x 16 columns: thread t gets all columns of lane t.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : KVC_R16(v, 0)
+      : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st_32x16(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Barrier over the softmax warps; `or` of a predicate.
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("bar.sync 2, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 3, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "n"(kSoftmaxThreads)
+      : "memory");
+  return r != 0;
+}
+
+// ---- the walk over a CTA's share -------------------------------------------------
+
+// Pages of a request; none if its length is out of range.
+__device__ __forceinline__ int pages_of(const AttendParams& p, int64_t length) {
+  if (length <= 0 || length > p.max_slots) return 0;
+  return static_cast<int>((length + kSlotsPerPage - 1) / kSlotsPerPage);
+}
+
+// Where a CTA is in its share: page `page` of `pages` of unit (req, group).
+struct Walk {
+  int req, group, page, pages, length;
+  long long left;  // pages of the share from here on
+
+  __device__ void begin(const AttendParams& p, int r, long long off, long long count) {
+    req = r;
+    left = count;
+    if (count <= 0) return;
+    length = p.lengths[r];
+    pages = pages_of(p, length);
+    group = static_cast<int>(off / pages);
+    page = static_cast<int>(off % pages);
+  }
+  __device__ int segment() const {
+    return static_cast<int>(min(static_cast<long long>(pages - page), left));
+  }
+  // On by `n` pages, at most to the unit's end.
+  __device__ void advance(const AttendParams& p, int n) {
+    left -= n;
+    page += n;
+    if (left <= 0 || page < pages) return;
+    page = 0;
+    if (++group < p.groups) return;
+    group = 0;
+    do {
+      length = p.lengths[++req];
+      pages = pages_of(p, length);
+    } while (pages == 0);
+  }
+};
+
+// Start of CTA c's share of `total` pages among `ctas`.
+__device__ __forceinline__ long long share_start(long long total, int c, int ctas) {
+  return total * c / ctas;
+}
+
+// The CTA whose share holds page `at`.
+__device__ __forceinline__ int share_of(long long total, long long at, int ctas) {
+  int c = static_cast<int>(((at + 1) * ctas - 1) / total);
+  while (c > 0 && share_start(total, c, ctas) > at) --c;
+  while (c + 1 < ctas && share_start(total, c + 1, ctas) <= at) ++c;
+  return c;
+}
+
+// ---- decode -------------------------------------------------------------------------
+
+// What one decode thread holds of a page: thread t has slot t / 4; of each of
+// its 7 groups the codes 16 (t % 4) .. + 15, and 16-byte pieces t % 4 and
+// t % 4 + 4 of its RoPE words.  Four threads read 64 bytes in a row.
+struct RawPage {
+  uint4 codes[7], rope[2];
+  uint2 scale;
+};
+
+struct PageRef {
+  int req, group;
+  int id;      // the page, as the table has it
+  int valid;   // slots of it that count
+  bool first;  // of its segment
+};
+
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void load_page(const AttendParams& p, const PageRef& ref, int t, RawPage* raw) {
+  const int slot = t >> 2, c = t & 3;
+  if (slot < ref.valid && static_cast<uint32_t>(ref.id) < p.num_pages) {
+    const uint8_t* page = p.kv_cache + ref.id * kPageBytes;
+    const uint8_t* row = page + slot * kTokenStride + 16 * c;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) raw->codes[i] = load16(row + 64 * i);
+    raw->rope[0] = load16(row + kNopeDim);
+    raw->rope[1] = load16(row + kNopeDim + 64);
+    raw->scale = __ldg(reinterpret_cast<const uint2*>(page + kScaleBase + slot * kScaleDim));
+  } else {  // code 0 in every place
+#pragma unroll
+    for (int i = 0; i < 7; ++i) raw->codes[i] = make_uint4(0, 0, 0, 0);
+    raw->rope[0] = raw->rope[1] = make_uint4(0, 0, 0, 0);
+    raw->scale = make_uint2(0, 0);
   }
 }
 
-// Whether the request's length and pages are in range; the whole block calls.
-__device__ bool request_ok(const AttendParams& p, const int32_t* table, int64_t length) {
-  bool ok = length >= 0 && length <= p.max_slots;
-  if (ok)
-    for (int64_t i = threadIdx.x; i * kSlotsPerPage < length; i += blockDim.x)
-      ok = ok && static_cast<uint32_t>(table[i]) < p.num_pages;
-  ok = __syncthreads_and(ok);
-  if (!ok && threadIdx.x == 0) atomicCAS(p.error, 0u, kErrBadIndexAttend);
-  return ok;
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
-__global__ void __launch_bounds__(kRowThreads) kvc_attend_rows_kernel(AttendParams p) {
-  __shared__ float part[2][4];
-  const int h = blockIdx.x, t = threadIdx.x;
-  const int64_t r = blockIdx.y;
-  const int32_t* table = p.page_table + r * p.page_table_row_stride;
-  const int64_t length = p.lengths[r];
-  if (!request_ok(p, table, length)) return;
-  const uint16_t* q = p.q + r * p.q_req_stride + h * p.q_head_stride + 4 * t;
-  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < 4; ++i) qv[i] = __uint_as_float(static_cast<uint32_t>(q[i]) << 16);
-  float top = -INFINITY, total = 0.f;
-  if (p.sinks != nullptr) {
-    top = p.sinks[h];
-    total = top == -INFINITY ? 0.f : 1.f;
-  }
-  for (int n = 0; n < length; ++n) {
-    float v[4], dot = 0.f;
-    read4(p, table, n, 4 * t, v);
-    for (int i = 0; i < 4; ++i) dot += qv[i] * v[i];
-    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-    if ((t & 31) == 0) part[n & 1][t >> 5] = dot;
-    __syncthreads();
-    const float* w = part[n & 1];
-    const float s = (w[0] + w[1] + w[2] + w[3]) * p.scale;
-    const float next = fmaxf(top, s);
-    if (next == -INFINITY && !isnan(s)) continue;
-    const float keep = expf(top - next), e = expf(s - next);
-    total = total * keep + e;
-    for (int i = 0; i < 4; ++i) acc[i] = acc[i] * keep + e * v[i];
-    top = next;
-  }
-  const float f = total == 0.f ? 0.f : 1.f / total;
-  const int64_t row = r * p.num_heads + h;
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(acc[i] * f);
-    p.out[row * kHeadDim + 4 * t + i] = *reinterpret_cast<const uint16_t*>(&b);
-  }
-  if (t == 0) p.lse[row] = total == 0.f ? -INFINITY : top + logf(total);
+// 4 codes times 2^(b - 127) as two words of bf16, exactly.  u = code + 128 in
+// the low bits of a bf16 is u 2^-133 (subnormal below 128, the first binade
+// above: one linear scale); times 2^127 it is u 2^-6, and one fused
+// multiply-add by 2^(b - 121) less 128 2^(b - 127) leaves code 2^(b - 127),
+// 8 bits that are exact down to bf16's last subnormal.  b <= 247, so that
+// both constants are bf16 values: `up` = (b + 6) << 7, `less` = -((b + 7) << 7)
+// as bits, in both halves.
+__device__ __forceinline__ void decode4_bf16(uint32_t word, uint32_t up, uint32_t less, uint32_t* lo,
+                                             uint32_t* hi) {
+  const uint32_t u = word ^ 0x80808080u;
+  *lo = fma_bf16x2(mul_bf16x2(__byte_perm(u, 0, 0x4140), 0x7F007F00u), up, less);
+  *hi = fma_bf16x2(mul_bf16x2(__byte_perm(u, 0, 0x4342), 0x7F007F00u), up, less);
 }
 
-__global__ void __launch_bounds__(kRowThreads) kvc_attend_weights_kernel(AttendParams p) {
-  __shared__ float part[4];
-  const int t = threadIdx.x;
-  const int64_t r = blockIdx.y;
-  const int32_t* table = p.page_table + r * p.page_table_row_stride;
-  const int64_t length = p.lengths[r];
-  if (!request_ok(p, table, length)) return;
-  for (int n = blockIdx.x; n < length; n += gridDim.x) {
-    float v[4], sum = 0.f;
-    read4(p, table, n, 4 * t, v);
-    for (int h = 0; h < p.num_heads; ++h) {
-      const uint16_t* q = p.q + r * p.q_req_stride + h * p.q_head_stride + 4 * t;
-      float dot = 0.f;
-      for (int i = 0; i < 4; ++i) dot += __uint_as_float(static_cast<uint32_t>(q[i]) << 16) * v[i];
-      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
-      __syncthreads();
-      if ((t & 31) == 0) part[t >> 5] = dot;
-      __syncthreads();
-      const float s = (part[0] + part[1] + part[2] + part[3]) * p.scale;
-      const float lse = p.lse[r * p.num_heads + h];
-      if (lse != -INFINITY) sum += expf(s - lse);
+__device__ __forceinline__ void store_page(const RawPage& raw, uint8_t* keys, int t) {
+  const int slot = t >> 2, c = t & 3, x = slot & 7;
+  uint8_t* const row = keys + slot * 128;
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint32_t b = ((i < 4 ? raw.scale.x : raw.scale.y) >> (8 * (i & 3))) & 0xFFu;
+    const uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
+    uint32_t v[8];
+    if (b <= 247u) {
+      const uint32_t up = (b + 6u) * 0x00800080u, less = (b + 7u) * 0x00800080u | 0x80008000u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) decode4_bf16(words[j], up, less, &v[2 * j], &v[2 * j + 1]);
+    } else {  // values of 2^121 and above
+      const float hs = half_scale(b);
+      for (int j = 0; j < 4; ++j) {
+        float f[4];
+        decode4(words[j], hs, f);
+        v[2 * j] = bf16_pair(f[0], f[1]);
+        v[2 * j + 1] = bf16_pair(f[2], f[3]);
+      }
     }
-    if (t == 0)
-      p.weights_out[r * p.weights_out_row_stride + n] =
-          (p.weights_in == nullptr ? 0.f : p.weights_in[r * p.weights_in_row_stride + n]) + sum;
+    uint8_t* const block = row + i * kKeyBlock;
+    *reinterpret_cast<uint4*>(block + (((2 * c) ^ x) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(block + (((2 * c + 1) ^ x) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
   }
+  uint8_t* const block = row + 7 * kKeyBlock;
+  *reinterpret_cast<uint4*>(block + ((c ^ x) << 4)) = raw.rope[0];
+  *reinterpret_cast<uint4*>(block + (((c + 4) ^ x) << 4)) = raw.rope[1];
+}
+
+// ---- the kernel -----------------------------------------------------------------------
+
+template <int N>
+__host__ __device__ constexpr uint32_t tmem_columns() { return N == 64 ? 512 : N == 32 ? 256 : 128; }
+
+template <int N>
+__device__ __forceinline__ int heads_of(const AttendParams& p, int group) {
+  return min(p.group_heads, p.num_heads - group * p.group_heads);
+}
+
+// Decode warps: every page of the share to shared memory, and each segment's q.
+template <int N>
+__device__ void decode_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+  const int t = threadIdx.x - kSoftmaxThreads, lane = t & 31;
+  auto next_ref = [&]() {  // the walk's page, and one page on
+    PageRef ref{0, 0, 0, 0, false};
+    if (w.left <= 0) return ref;
+    ref.req = w.req;
+    ref.group = w.group;
+    ref.id = __ldg(p.page_table + w.req * p.page_table_row_stride + w.page);
+    ref.valid = min(kSlotsPerPage, w.length - w.page * kSlotsPerPage);
+    ref.first = w.page == 0;
+    w.advance(p, 1);
+    return ref;
+  };
+  const long long count = w.left;
+  PageRef now = next_ref();
+  now.first = true;
+  RawPage raw, raw_next;
+  load_page(p, now, t, &raw);
+  PageRef next = next_ref();
+  int segment = -1;
+  for (long long i = 0; i < count; ++i) {
+    load_page(p, next, t, &raw_next);
+    const PageRef after = next_ref();
+    bool ok = true;
+    if (now.first) {
+      ++segment;
+      if (segment > 0) ok = dev::mbar_wait_bounded(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit);
+      const int heads = heads_of<N>(p, now.group);
+      const uint16_t* q = p.q + now.req * p.q_req_stride + now.group * p.group_heads * p.q_head_stride;
+#pragma unroll 8
+      for (int j = t; j < N * 64; j += kDecodeThreads) {
+        const int h = j >> 6, c = j & 63;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (h < heads) v = *reinterpret_cast<const uint4*>(q + h * p.q_head_stride + 8 * c);
+        *reinterpret_cast<uint4*>(s.q + (c >> 3) * (N * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4)) = v;
+      }
+    }
+    const int stage = i & 1;
+    if (i >= 2)
+      ok = ok && dev::mbar_wait_bounded(&s.bar.kv_empty[stage], ((i >> 1) - 1) & 1, p.wait_limit);
+    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+      s.abort = 1;
+      return;
+    }
+    if (now.valid > 0 && static_cast<uint32_t>(now.id) >= p.num_pages) {
+      s.bad[segment & 3] = 1;
+      if (t == 0) atomicCAS(p.error, 0u, kErrBadIndex);
+    }
+    store_page(raw, s.keys[stage], t);
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(&s.bar.kv_full[stage]);
+    raw = raw_next;
+    now = next;
+    next = after;
+  }
+}
+
+// One thread: the products of every page, the next page's first product ahead
+// of the present one's second.
+template <int N>
+__device__ void issue_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+  constexpr uint32_t kFirst = instruction(64, N, false), kSecond = instruction(128, N, true);
+  constexpr uint32_t kSwizzleP = N == 64 ? 2 : N == 32 ? 4 : 6;
+  const uint32_t tmem = s.tmem, q = smem_addr(s.q);
+  const long long count = w.left;
+  Walk ahead = w;  // of the first products
+  int ahead_left = ahead.segment(), left = w.segment();
+  bool fresh = true;
+  auto first = [&](long long i) {
+    const int stage = i & 1;
+    if (!dev::mbar_wait_bounded(&s.bar.kv_full[stage], (i >> 1) & 1, p.wait_limit) || s.abort) return false;
+    tc_fence_after();
+    const uint32_t keys = smem_addr(s.keys[stage]);
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tc_mma(tmem + 4 * N + stage * N, operand(keys + b * kKeyBlock + 32 * k, 16, 1024, 2),
+               operand(q + b * (N * 128) + 32 * k, 16, 1024, 2), kFirst, b + k > 0);
+    tc_commit(&s.bar.s_full[stage]);
+    if (--ahead_left == 0) {
+      tc_commit(&s.bar.q_empty);
+      ahead.advance(p, ahead.segment());
+      if (ahead.left > 0) ahead_left = ahead.segment();
+    }
+    return true;
+  };
+  bool ok = first(0);
+  for (long long i = 0; ok && i < count; ++i) {
+    if (i + 1 < count && !first(i + 1)) { ok = false; break; }
+    const int stage = i & 1;
+    ok = dev::mbar_wait_bounded(&s.bar.p_full[stage], (i >> 1) & 1, p.wait_limit) && !s.abort;
+    if (!ok) break;
+    tc_fence_after();
+    const uint32_t keys = smem_addr(s.keys[stage]), probs = smem_addr(s.p[stage]);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tc_mma(tmem + c * N, operand(keys + 2 * c * kKeyBlock + 2048 * k, kKeyBlock, 1024, 2),
+               operand(probs + k * 32 * N, 16, 16 * N, kSwizzleP), kSecond, !fresh || k > 0);
+    fresh = false;
+    tc_commit(&s.bar.kv_empty[stage]);
+    if (--left == 0) {
+      tc_commit(&s.bar.o_full);
+      w.advance(p, w.segment());
+      if (w.left > 0) left = w.segment();
+      fresh = true;
+    }
+  }
+  if (!ok) s.abort = 1;
+  // no product may run on when the CTA's memory is given back
+  tc_commit(&s.bar.drain);
+  dev::mbar_wait_drain(&s.bar.drain, 0);
+}
+
+// Softmax warps.  Warp w has slots 16 w .. 16 w + 15 of a page: thread t the
+// slots t / 4 and t / 4 + 8 of them, and columns 2 (t % 4) + {0, 1} of each 8.
+template <int N>
+__device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, int cta, int ctas) {
+  constexpr int kCols = N / 4;  // columns of a thread
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const uint32_t tmem = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const float c = p.scale * kLog2e;
+  const int row = warp * 16 + (lane >> 2);
+  long long i = 0;
+  long long at = share_start(s.total, cta, ctas);
+  for (int segment = 0; w.left > 0; ++segment) {
+    const int n = w.segment();
+    float ref[kCols], sum[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) ref[j] = -FLT_MAX, sum[j] = 0.f;
+    for (int pg = 0; pg < n; ++pg, ++i) {
+      const int stage = i & 1;
+      bool ok = dev::mbar_wait_bounded(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) s.abort = 1;
+      tc_fence_after();
+      uint32_t v[2 * kCols];
+#pragma unroll
+      for (int j = 0; j < N / 16; ++j) tmem_ld_16x16(tmem + 4 * N + stage * N + 16 * j, v + 8 * j);
+      tmem_wait_ld();
+      const int valid = w.length - (w.page + pg) * kSlotsPerPage;
+      const bool in0 = row < valid, in1 = row + 8 < valid;
+      if (p.scores != nullptr) {
+        float* dst = p.scores + ((w.req * p.max_pages + w.page + pg) * kSlotsPerPage + row) * p.score_cols +
+                     w.group * N + 2 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+          if (in0)
+            *reinterpret_cast<float2*>(dst + 8 * j) =
+                make_float2(__uint_as_float(v[4 * j]) * c, __uint_as_float(v[4 * j + 1]) * c);
+          if (in1)
+            *reinterpret_cast<float2*>(dst + 8 * p.score_cols + 8 * j) =
+                make_float2(__uint_as_float(v[4 * j + 2]) * c, __uint_as_float(v[4 * j + 3]) * c);
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 2 * kCols; ++j) {
+        const float x = ((j & 2) ? in1 : in0) ? __uint_as_float(v[j]) * c : -INFINITY;
+        v[j] = __float_as_uint(x);
+        top = fmaxf(top, x - ref[(j >> 2) * 2 + (j & 1)]);
+      }
+      if (softmax_any(top > kRescaleAbove || !ok)) {
+        if (softmax_any(s.abort)) return;
+        // the columns' maxima over the page
+        float m[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          m[j] = fmaxf(__uint_as_float(v[4 * (j >> 1) + (j & 1)]),
+                       __uint_as_float(v[4 * (j >> 1) + 2 + (j & 1)]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], d));
+          if (lane < 4) s.red[warp][8 * (j >> 1) + 2 * lane + (j & 1)] = m[j];
+        }
+        softmax_sync();
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const int col = 8 * (j >> 1) + 2 * (lane & 3) + (j & 1);
+          const float next = fmaxf(fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
+                                         fmaxf(s.red[2][col], s.red[3][col])), ref[j]);
+          const float f = exp2_fast(ref[j] - next);
+          sum[j] *= f;
+          ref[j] = next;
+          if (warp == 0 && lane < 4) s.factor[col] = f;
+        }
+        softmax_sync();
+        if (pg > 0) {  // bring what is summed up so far to the new reference
+          bool done = dev::mbar_wait_bounded(&s.bar.kv_empty[stage ^ 1], ((i - 1) >> 1) & 1, p.wait_limit);
+          if (softmax_any(!done)) {
+            s.abort = 1;
+            return;
+          }
+          tc_fence_after();
+          for (int b = 0; b < 4 * N; b += 16) {
+            uint32_t o[16];
+            tmem_ld_32x16(tmem + b, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * s.factor[(b + j) & (N - 1)]);
+            tmem_st_32x16(tmem + b, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      uint8_t* const probs = s.p[stage];
+#pragma unroll
+      for (int j = 0; j < N / 8; ++j) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float a = exp2_fast(__uint_as_float(v[4 * j + 2 * half]) - ref[2 * j]);
+          const float b = exp2_fast(__uint_as_float(v[4 * j + 2 * half + 1]) - ref[2 * j + 1]);
+          sum[2 * j] += a;
+          sum[2 * j + 1] += b;
+          const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
+          const uint32_t off = (row + 8 * half) * (2 * N) + 16 * j + 4 * (lane & 3);
+          constexpr uint32_t kMask = N / 8 - 1;  // 16-byte pieces of a row
+          *reinterpret_cast<__nv_bfloat162*>(probs + (off ^ (((off >> 7) & kMask) << 4))) = ab;
+        }
+      }
+      fence_async_shared();
+      tc_fence_before();
+      dev::mbar_arrive(&s.bar.p_full[stage]);
+    }
+    // the segment's end: columns' sums, then the rows of O
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], d);
+      const int col = 8 * (j >> 1) + 2 * lane + (j & 1);
+      if (lane < 4) s.red[warp][col] = sum[j];
+      if (warp == 0 && lane < 4) s.ref[col] = ref[j];
+    }
+    softmax_sync();
+    const bool whole = n == w.pages, bad = s.bad[segment & 3] != 0;
+    const int part = 2 * cta + (segment > 0);
+    const int heads = heads_of<N>(p, w.group);
+    const int64_t row0 = static_cast<int64_t>(w.req) * p.num_heads + w.group * p.group_heads;
+    if (t < heads) {
+      const float l = s.red[0][t] + s.red[1][t] + s.red[2][t] + s.red[3][t], m = s.ref[t];
+      float f = 1.f;
+      if (whole) {
+        float top = m, total = l;
+        f = 1.f;
+        if (p.sinks != nullptr) {
+          const float sink = p.sinks[w.group * p.group_heads + t] * kLog2e;
+          top = fmaxf(m, sink);
+          f = exp2_fast(m - top);
+          total = l * f + exp2_fast(sink - top);
+        }
+        if (!bad) p.lse[row0 + t] = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
+        f = total == 0.f ? 0.f : f / total;
+      } else {
+        p.part_stats[part * N + t] = make_float2(m, l);
+      }
+      s.factor[t] = f;
+    }
+    if (t == 0) {
+      if (w.page == 0) {  // the unit's first part: where its parts lie
+        const int last = share_of(s.total, at + w.pages - 1, ctas);
+        p.unit_parts[static_cast<int64_t>(w.req) * p.groups + w.group] =
+            whole ? make_int2(-1, bad) : make_int2(part, last);
+      }
+      if (!whole) {
+        p.part_bad[part] = bad;
+        if (w.page + n == w.pages) {  // the unit's last part: this share's joins it
+          const int first = share_of(s.total, at - w.page, ctas);
+          const bool at_start = share_start(s.total, first, ctas) == at - w.page;
+          p.joins[cta] = make_int4(w.req, w.group, 2 * first + !at_start, cta);
+        }
+      }
+    }
+    bool ok = dev::mbar_wait_bounded(&s.bar.o_full, segment & 1, p.wait_limit);
+    if (softmax_any(!ok)) {  // also makes s.factor visible
+      s.abort = 1;
+      return;
+    }
+    if (t == 0) s.bad[segment & 3] = 0;
+    tc_fence_after();
+    if (!whole || !bad) {
+      for (int chunk = 0; chunk < 4; ++chunk) {
+        const int d = chunk * 128 + warp * 32 + lane;
+        for (int b = 0; b < heads; b += 16) {
+          uint32_t o[16];
+          tmem_ld_32x16(tmem + chunk * N + b, o);
+          tmem_wait_ld();
+          if (whole) {
+            uint16_t* const out = p.out + (row0 + b) * kHeadDim;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              // lanes 2 i and 2 i + 1 trade: one stores both dims of head j, the other of j + 1
+              const float a = __uint_as_float(o[j]) * s.factor[b + j];
+              const float e = __uint_as_float(o[j + 1]) * s.factor[b + j + 1];
+              const bool odd = lane & 1;
+              const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : e, 1);
+              const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, e) : __floats2bfloat162_rn(a, got);
+              if (b + j + odd < heads)
+                *reinterpret_cast<__nv_bfloat162*>(out + (j + odd) * kHeadDim + (d & ~1)) = v;
+            }
+          } else {
+            float* const dst = p.parts + (static_cast<int64_t>(part) * N + b) * kHeadDim + d;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (b + j < heads) dst[j * kHeadDim] = __uint_as_float(o[j]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    softmax_sync();  // s.red, s.factor and O are free again
+    at += n;
+    w.advance(p, n);
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __grid_constant__ AttendParams p) {
+  extern __shared__ uint8_t raw_shared[];
+  AttendShared<N>& s = *reinterpret_cast<AttendShared<N>*>(
+      raw_shared + ((1024 - (smem_addr(raw_shared) & 1023)) & 1023));
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int cta = blockIdx.x;
+  if (warp == kIssueWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
+  if (t == 0) {
+    for (int i = 0; i < 2; ++i) {
+      dev::mbar_init(&s.bar.kv_full[i], kDecodeWarps);
+      dev::mbar_init(&s.bar.kv_empty[i], 1);
+      dev::mbar_init(&s.bar.s_full[i], 1);
+      dev::mbar_init(&s.bar.p_full[i], kSoftmaxThreads);
+    }
+    dev::mbar_init(&s.bar.q_empty, 1);
+    dev::mbar_init(&s.bar.o_full, 1);
+    dev::mbar_init(&s.bar.drain, 1);
+    dev::fence_mbar_init();
+    s.abort = 0;
+    for (int i = 0; i < 4; ++i) s.bad[i] = 0;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // pages before each thread's run of requests
+  const int run = static_cast<int>((p.num_reqs + kAttendThreads - 1) / kAttendThreads);
+  const int lo = min(static_cast<int>(p.num_reqs), t * run), hi = min(static_cast<int>(p.num_reqs), lo + run);
+  long long mine = 0;
+  bool bad_length = false;
+  for (int r = lo; r < hi; ++r) {
+    const int64_t length = p.lengths[r];
+    mine += pages_of(p, length);
+    bad_length = bad_length || length < 0 || length > p.max_slots;
+  }
+  if (bad_length && cta == 0) atomicCAS(p.error, 0u, kErrBadIndex);
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) s.scan[warp] = inc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long before = inc - mine, total = 0;
+  for (int i = 0; i < kAttendThreads / 32; ++i) {
+    if (i < warp) before += s.scan[i];
+    total += s.scan[i];
+  }
+  total *= p.groups;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1LL)));
+  const long long start = cta < ctas ? share_start(total, cta, ctas) : 0;
+  const long long count = cta < ctas ? share_start(total, cta + 1, ctas) - start : 0;
+  if (t == 0) {
+    s.total = total;
+    p.joins[cta] = make_int4(-1, 0, 0, 0);
+  }
+  if (count > 0 && start >= before * p.groups && start < (before + mine) * p.groups) {
+    long long off = start - before * p.groups;
+    int r = lo;
+    for (;; ++r) {
+      const long long here = static_cast<long long>(pages_of(p, p.lengths[r])) * p.groups;
+      if (off < here) break;
+      off -= here;
+    }
+    s.start_req = r;
+    s.start_off = off;
+  }
+  __syncthreads();
+  if (count > 0) {
+    Walk w;
+    w.begin(p, s.start_req, s.start_off, count);
+    if (warp < kSoftmaxWarps) {
+      softmax_role<N>(p, s, w, cta, ctas);
+    } else if (warp < kIssueWarp) {
+      decode_role<N>(p, s, w);
+    } else if (lane == 0) {
+      issue_role<N>(p, s, w);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (t == 0) {
+    if (s.abort) atomicCAS(p.error, 0u, kErrTimeout);
+  }
+  if (warp == kIssueWarp) tmem_free(s.tmem, tmem_columns<N>());
+}
+
+// ---- joining kernel -----------------------------------------------------------------
+
+// Log-sum-exp of one head of a unit from its parts' (m, l) and its sink: the
+// reference and the total above it.
+__device__ __forceinline__ float2 unit_total(const AttendParams& p, int n, int first, int last, int col,
+                                             int head) {
+  float top = p.sinks == nullptr ? -INFINITY : p.sinks[head] * kLog2e;
+  const float sink = top;
+  for (int part = first;; part = (part | 1) + 1) {
+    top = fmaxf(top, p.part_stats[part * n + col].x);
+    if (part >> 1 == last) break;
+  }
+  float total = p.sinks == nullptr ? 0.f : exp2_fast(sink - top);
+  for (int part = first;; part = (part | 1) + 1) {
+    const float2 ml = p.part_stats[part * n + col];
+    total += ml.y * exp2_fast(ml.x - top);
+    if (part >> 1 == last) break;
+  }
+  return make_float2(top, total);
+}
+
+// CTAs 0 .. ctas * heads - 1: one head of the unit that share c completes (if
+// it was divided).  Then, per request: zeros for one without slots, and its
+// slots' weights.
+__global__ void __launch_bounds__(kJoinThreads) kvc_attend_join_kernel(const __grid_constant__ AttendParams p,
+                                                                        int n, int ctas, int chunks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x;
+  const int join_ctas = ctas * p.group_heads;
+  if (blockIdx.x < join_ctas) {
+    const int4 join = p.joins[blockIdx.x / p.group_heads];
+    const int col = blockIdx.x % p.group_heads;
+    const int head = join.y * p.group_heads + col;
+    if (join.x < 0 || head >= p.num_heads) return;
+    for (int part = join.z;; part = (part | 1) + 1) {
+      if (p.part_bad[part]) return;
+      if (part >> 1 == join.w) break;
+    }
+    const float2 mt = unit_total(p, n, join.z, join.w, col, head);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int part = join.z;; part = (part | 1) + 1) {
+      const float f = exp2_fast(p.part_stats[part * n + col].x - mt.x);
+      const float4 o = reinterpret_cast<const float4*>(p.parts + (static_cast<int64_t>(part) * n + col) * kHeadDim)[t];
+      acc.x += f * o.x;
+      acc.y += f * o.y;
+      acc.z += f * o.z;
+      acc.w += f * o.w;
+      if (part >> 1 == join.w) break;
+    }
+    const float f = mt.y == 0.f ? 0.f : 1.f / mt.y;
+    const int64_t row = static_cast<int64_t>(join.x) * p.num_heads + head;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    reinterpret_cast<uint2*>(p.out + row * kHeadDim)[t] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    if (t == 0) p.lse[row] = mt.y == 0.f ? -INFINITY : (mt.x + log2f(mt.y)) / kLog2e;
+    return;
+  }
+  const int item = blockIdx.x - join_ctas;
+  const int r = item / chunks, chunk = item % chunks;
+  const int64_t length = p.lengths[r];
+  if (length < 0 || length > p.max_slots) return;
+  if (length == 0) {
+    if (chunk != 0) return;
+    const int64_t row0 = static_cast<int64_t>(r) * p.num_heads;
+    uint4* out = reinterpret_cast<uint4*>(p.out + row0 * kHeadDim);
+    for (int i = t; i < p.num_heads * (kHeadDim / 8); i += kJoinThreads) out[i] = make_uint4(0, 0, 0, 0);
+    for (int h = t; h < p.num_heads; h += kJoinThreads) p.lse[row0 + h] = p.sinks == nullptr ? -INFINITY : p.sinks[h];
+    return;
+  }
+  if (p.weights_out == nullptr) return;
+  // the heads' log2-sum-exp, by column of the scores; +inf where there is no head or no key
+  __shared__ float total[2 * 64];
+  __shared__ int skip;
+  if (t == 0) skip = 0;
+  __syncthreads();
+  for (int col = t; col < p.score_cols; col += kJoinThreads) {
+    const int group = col / n, c = col % n, head = group * p.group_heads + c;
+    float v = INFINITY;
+    if (c < p.group_heads && head < p.num_heads) {
+      const int2 parts = p.unit_parts[static_cast<int64_t>(r) * p.groups + group];
+      if (parts.x < 0) {
+        if (parts.y) skip = 1;
+        v = p.lse[static_cast<int64_t>(r) * p.num_heads + head] * kLog2e;
+      } else {
+        for (int part = parts.x;; part = (part | 1) + 1) {
+          if (p.part_bad[part]) skip = 1;
+          if (part >> 1 == parts.y) break;
+        }
+        const float2 mt = unit_total(p, n, parts.x, parts.y, c, head);
+        v = mt.y == 0.f ? -INFINITY : mt.x + log2f(mt.y);
+      }
+      if (v == -INFINITY) v = INFINITY;
+    }
+    total[col] = v;
+  }
+  __syncthreads();
+  if (skip) return;
+  const int lane = t & 31, warp = t >> 5;
+  const int width = p.score_cols < 32 ? static_cast<int>(p.score_cols) : 32, sub = lane / width, of = 32 / width;
+  for (int i = warp * of + sub; i < kWeightSlots; i += (kJoinThreads / 32) * of) {
+    const int64_t slot = static_cast<int64_t>(chunk) * kWeightSlots + i;
+    float sum = 0.f;
+    if (slot < length) {
+      const float* scores = p.scores + (r * p.max_pages * kSlotsPerPage + slot) * p.score_cols;
+      for (int col = lane % width; col < p.score_cols; col += width)
+        if (total[col] != INFINITY) sum += exp2_fast(scores[col] - total[col]);
+    }
+    for (int d = width / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (slot < length && lane % width == 0)
+      p.weights_out[r * p.weights_out_row_stride + slot] =
+          (p.weights_in == nullptr ? 0.f : p.weights_in[r * p.weights_in_row_stride + slot]) + sum;
+  }
+}
+
+template <int N>
+cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
+  const size_t smem = sizeof(AttendShared<N>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kvc_attend_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kAttendThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N>, p);
+  if (e != cudaSuccess) return e;
+  const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kWeightSlots - 1) / kWeightSlots;
+  const int64_t grid = static_cast<int64_t>(ctas) * p.group_heads + p.num_reqs * (chunks > 0 ? chunks : 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kvc_attend_join_kernel, p, N, ctas, static_cast<int>(chunks > 0 ? chunks : 1));
 }
 
 }  // namespace
 
-cudaError_t launch_attend(const AttendParams& p, cudaStream_t stream) {
-  const unsigned reqs = static_cast<unsigned>(p.num_reqs);
-  kvc_attend_rows_kernel<<<dim3(p.num_heads, reqs), kRowThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.weights_out == nullptr) return e;
-  const unsigned wide = static_cast<unsigned>(p.max_slots < 1024 ? p.max_slots : 1024);
-  kvc_attend_weights_kernel<<<dim3(wide, reqs), kRowThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+AttendShape attend_shape(int num_heads) {
+  AttendShape s;
+  s.groups = (num_heads + 63) / 64;
+  s.group_heads = (num_heads + s.groups - 1) / s.groups;
+  s.columns = s.group_heads <= 16 ? 16 : s.group_heads <= 32 ? 32 : 64;
+  return s;
+}
+
+cudaError_t launch_attend(const AttendParams& p, int columns, int ctas, cudaStream_t stream) {
+  switch (columns) {
+    case 16: return launch_n<16>(p, ctas, stream);
+    case 32: return launch_n<32>(p, ctas, stream);
+    default: return launch_n<64>(p, ctas, stream);
+  }
 }
 
 }  // namespace kvc

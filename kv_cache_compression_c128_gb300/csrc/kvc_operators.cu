@@ -29,15 +29,44 @@ bool pages_ok(const void* kv_cache, int64_t num_kv_pages, const int32_t* page_ta
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Byte offsets in an attention's workspace.
+struct AttendWorkspace {
+  size_t parts, stats, bad, units, joins, lse, scores, total;
+};
+
+AttendWorkspace attend_workspace(int64_t num_reqs, int num_heads, int64_t max_pages, bool scores) {
+  const kvc::AttendShape shape = kvc::attend_shape(num_heads);
+  const size_t columns = 2 * static_cast<size_t>(kvc::kAttendCtas) * shape.columns;
+  AttendWorkspace w;
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += round16(bytes);
+    return here;
+  };
+  w.parts = take(columns * kvc::kHeadDim * sizeof(float));
+  w.stats = take(columns * sizeof(float2));
+  w.bad = take(2 * kvc::kAttendCtas * sizeof(int32_t));
+  w.units = take(num_reqs * shape.groups * sizeof(int2));
+  w.joins = take(kvc::kAttendCtas * sizeof(int4));
+  w.lse = take(num_reqs * num_heads * sizeof(float));
+  w.scores = take(scores ? static_cast<size_t>(num_reqs) * max_pages * kvc::kSlotsPerPage * shape.groups *
+                               shape.columns * sizeof(float)
+                         : 0);
+  w.total = at;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t kvc_attend_workspace_bytes(int64_t num_reqs, int32_t num_heads, int64_t max_pages_per_req,
                                   int32_t with_slot_weights) {
-  (void)with_slot_weights;
-  if (num_reqs < 0 || num_heads < 1 || num_heads > kvc::kMaxHeads || max_pages_per_req < 0) return 0;
-  return round16(sizeof(float) * num_reqs * num_heads) + 16;
+  if (num_reqs < 0 || num_reqs > kMaxRequests || num_heads < 1 || num_heads > kvc::kMaxHeads ||
+      max_pages_per_req < 0 || max_pages_per_req > kMaxSlots / kvc::kSlotsPerPage)
+    return 0;
+  return attend_workspace(num_reqs, num_heads, max_pages_per_req, with_slot_weights != 0).total;
 }
 
 kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride, int64_t num_reqs,
@@ -49,7 +78,7 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
                       int64_t slot_weights_row_stride, int64_t max_slots, void* workspace,
                       size_t workspace_bytes, uint32_t flags, void* stream) {
   if (num_reqs < 0 || num_heads < 1 || num_heads > kvc::kMaxHeads || !std::isfinite(scale) ||
-      flags != 0)
+      (flags & ~KVC_FLAG_GRID_MASK) != 0)
     return KVC_ERR_INVALID_ARG;
   if (num_reqs == 0) return KVC_OK;
   if (!pages_ok(kv_cache, num_kv_pages, page_table, num_reqs, max_pages_per_req,
@@ -70,7 +99,7 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
     return KVC_ERR_INVALID_ARG;
   int sms = 0;
   kvc::AttendParams p = {};
-  const kvc_status st = kvc::operator_device(&sms, &p.error);
+  const kvc_status st = kvc::operator_device(&sms, &p.error, &p.wait_limit);
   if (st != KVC_OK) return st;
   p.q = static_cast<const uint16_t*>(q);
   p.q_req_stride = q_req_stride;
@@ -88,12 +117,29 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
   p.scale = scale;
   p.sinks = sinks;
   p.out = static_cast<uint16_t*>(out);
-  p.lse = lse != nullptr ? lse : static_cast<float*>(workspace);
+  const AttendWorkspace at = attend_workspace(num_reqs, num_heads, max_pages_per_req, slot_weights != nullptr);
+  uint8_t* const base = static_cast<uint8_t*>(workspace);
+  p.lse = lse != nullptr ? lse : reinterpret_cast<float*>(base + at.lse);
+  p.parts = reinterpret_cast<float*>(base + at.parts);
+  p.part_stats = reinterpret_cast<float2*>(base + at.stats);
+  p.part_bad = reinterpret_cast<int32_t*>(base + at.bad);
+  p.unit_parts = reinterpret_cast<int2*>(base + at.units);
+  p.joins = reinterpret_cast<int4*>(base + at.joins);
   p.weights_in = slot_weights_in;
   p.weights_out = slot_weights;
   p.weights_in_row_stride = slot_weights_in_row_stride;
   p.weights_out_row_stride = slot_weights_row_stride;
-  const cudaError_t e = kvc::launch_attend(p, static_cast<cudaStream_t>(stream));
+  const kvc::AttendShape shape = kvc::attend_shape(num_heads);
+  p.groups = shape.groups;
+  p.group_heads = shape.group_heads;
+  p.score_cols = static_cast<int64_t>(shape.groups) * shape.columns;
+  if (slot_weights != nullptr) p.scores = reinterpret_cast<float*>(base + at.scores);
+  // one CTA per SM, fewer where the table cannot name a page for each
+  int64_t ctas = sms < kvc::kAttendCtas ? sms : kvc::kAttendCtas;
+  if (num_reqs * max_pages_per_req * shape.groups < ctas) ctas = num_reqs * max_pages_per_req * shape.groups;
+  if ((flags & KVC_FLAG_GRID_MASK) != 0 && (flags & KVC_FLAG_GRID_MASK) < ctas) ctas = flags & KVC_FLAG_GRID_MASK;
+  const cudaError_t e =
+      kvc::launch_attend(p, shape.columns, static_cast<int>(ctas), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 
@@ -155,8 +201,9 @@ kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* pag
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need)
     return KVC_ERR_INVALID_ARG;
   int sms = 0;
+  long long wait_limit = 0;
   kvc::EvictParams p = {};
-  const kvc_status st = kvc::operator_device(&sms, &p.error);
+  const kvc_status st = kvc::operator_device(&sms, &p.error, &wait_limit);
   if (st != KVC_OK) return st;
   const int64_t slots = max_pages_per_req * kvc::kSlotsPerPage;
   const int64_t behind = slots > keep ? slots - keep : 0;

@@ -33,8 +33,28 @@ struct AttendParams {
   const float* weights_in;  // null: zeros
   float* weights_out;       // null: not wanted
   int64_t weights_in_row_stride, weights_out_row_stride;
+  int groups, group_heads;  // head groups of a request (AttendShape)
+  // workspace
+  float* scores;         // [num_reqs, max_pages * 64, score_cols] log2 scores, or null
+  int64_t score_cols;    // groups * columns
+  float* parts;          // [2 * ctas][columns][512]: what divided units summed up
+  float2* part_stats;    // [2 * ctas][columns]: their reference (log2) and sum
+  int32_t* part_bad;     // [2 * ctas]: a page was outside the cache
+  int2* unit_parts;      // [num_reqs * groups]: first part and last CTA; (-1, bad) if whole
+  int4* joins;           // [ctas]: (request, group, first part, last CTA) to join, or (-1, ...)
+  long long wait_limit;
   uint32_t* error;
 };
+
+// How the heads of a request are laid out: `groups` runs of `group_heads`
+// (the last may be shorter), each padded to `columns` of a product.
+struct AttendShape {
+  int groups, group_heads, columns;
+};
+AttendShape attend_shape(int num_heads);
+
+// CTAs at most (GB300 has 152 SMs); the workspace holds two parts for each.
+constexpr int kAttendCtas = 152;
 
 struct JoinParams {
   const void* outs[kMaxParts];
@@ -70,12 +90,12 @@ struct EvictParams {
   uint32_t* error;
 };
 
-cudaError_t launch_attend(const AttendParams& p, cudaStream_t stream);
+cudaError_t launch_attend(const AttendParams& p, int columns, int ctas, cudaStream_t stream);
 cudaError_t launch_join(const JoinParams& p, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 
-// The current device's set-up (kvc_api.cu): its SM count and the address of
-// its error word.
-kvc_status operator_device(int* sms, uint32_t** error_word);
+// The current device's set-up (kvc_api.cu): its SM count, the address of its
+// error word, and the limit on a kernel's pipeline waits.
+kvc_status operator_device(int* sms, uint32_t** error_word, long long* wait_limit);
 
 }  // namespace kvc
