@@ -306,7 +306,9 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
  * with the values, and out to bf16 at the end.
  *
  * q            bf16, head h of request r at q + r * q_req_stride + h *
- *              q_head_stride (elements, multiples of 8), 16-byte aligned.
+ *              q_head_stride (elements, multiples of 8; a request stride of 0
+ *              gives all requests the same queries, the head stride is not
+ *              0), 16-byte aligned.
  * num_heads    1 .. 128.
  * kv_cache     uint8 [num_kv_pages, 37376], 16-byte aligned, read only.
  * page_table   int32 [num_reqs, max_pages_per_req] at row stride

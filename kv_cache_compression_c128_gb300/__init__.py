@@ -736,6 +736,8 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
         if slot_weights is None or slot_weights_in.shape != slot_weights.shape:
             raise ValueError("slot_weights_in needs slot_weights of the same shape")
     with _on(torch, dev, stream) as sp:
+        if H > 1 and q.stride(1) == 0:  # one query for all heads
+            q = q.contiguous()
         if out is None:
             out = torch.empty((R, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
         else:

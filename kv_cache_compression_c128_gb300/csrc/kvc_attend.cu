@@ -24,7 +24,14 @@
 // stays in range, so O is rescaled only where a score exceeds m by 2^32.
 //
 // Warps of a CTA: 0..3 softmax and epilogue, 4..11 decode, 12 issues the
-// products.  The pages of all (request, head group) units are laid end to end
+// products, 13 copies the codes, 14 the queries.  The codes of a page come by
+// TMA in 7 pieces of 64 slots x 64 bytes through a ring of kPieces: 24 KB (N 64)
+// or 56 KB stay on their way whatever the decode does.  (Plain loads of the
+// same bytes kept some 14 KB on the way, for the cache that they pass through
+// is what shared memory leaves of it, and took 193 us where this takes TIME_TMA
+// on 64 requests x 8192 slots x 64 heads.)  The RoPE
+// words come through the registers of one warp.
+// The pages of all (request, head group) units are laid end to end
 // and cut into equal shares, one per CTA; a unit that a cut divides leaves its
 // parts (m, l, O) in the workspace, and a second kernel joins them in the order
 // of the shares, so the same lengths give the same bits.  That kernel also
@@ -36,6 +43,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kvc_decode.cuh"
 #include "kvc_device.cuh"
@@ -51,33 +59,73 @@ using dev::kLog2e;
 using dev::smem_addr;
 
 constexpr int kSoftmaxWarps = 4, kDecodeWarps = 8;
-constexpr int kSoftmaxThreads = kSoftmaxWarps * 32, kDecodeThreads = kDecodeWarps * 32;
-constexpr int kIssueWarp = kSoftmaxWarps + kDecodeWarps;
-constexpr int kAttendThreads = (kIssueWarp + 1) * 32;
+constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
+constexpr int kIssueWarp = kSoftmaxWarps + kDecodeWarps, kCopyWarp = kIssueWarp + 1, kQueryWarp = kIssueWarp + 2;
+constexpr int kAttendThreads = (kIssueWarp + 4) * 32;  // the last warp only fills up a group of four
+// Registers of a thread by group of warps: 512 x 128 at launch, shared out
+// anew so that no role spills (the cache that a spill would sit in is shared
+// memory here).  128 x 160 + 256 x 112 + 128 x 128 = 512 x 128.
+constexpr int kSoftmaxRegs = 160, kDecodeRegs = 112;
 constexpr int kKeyBlock = kSlotsPerPage * 128;          // 64 slots x 64 dims, bf16
 constexpr int kKeyStage = 8 * kKeyBlock;                // a decoded page
+constexpr int kGroups = 7;                              // of 64 codes with one scale
+constexpr int kPieceBytes = kSlotsPerPage * kGroup;     // a page's codes of one group
+constexpr int kScaleBytes = kSlotsPerPage * kScaleDim;
+// Pages described at a time.  The products of page i wait for its RoPE words,
+// the decode of page i + 2 then for theirs, and the copies run less than two
+// pages ahead of the decode: a page's place is taken again by page i + 5 at the
+// earliest.
+constexpr int kInfos = 6;
 constexpr float kRescaleAbove = 32.f;                   // log2
 constexpr int kJoinThreads = 128;
 constexpr int kWeightSlots = 64;                        // slots per CTA of its weights part
 
+// Pieces in the ring: what 227 KB leave at N = 64; two pages' worth otherwise.
+template <int N>
+__host__ __device__ constexpr int pieces() { return N == 64 ? 6 : 14; }
+// Warps that decode: piece n goes to warp n % decoders() from place n %
+// pieces() of the ring, so that a place has one reader, in order.
+template <int N>
+__host__ __device__ constexpr int decoders() { return N == 64 ? 6 : 7; }
+// Pages whose scales are kept.  The copy of page i's waits for the ring's place
+// of its first piece, so all pieces of page i - kScales are read if
+// 7 kScales - kPieces >= 6.
+template <int N>
+__host__ __device__ constexpr int scale_slots() { return N == 64 ? 2 : 3; }
+
+template <int N>
 struct Barriers {
-  unsigned long long kv_full[2], kv_empty[2], s_full[2], p_full[2], q_empty, o_full, drain;
+  // of a stage's 8 blocks of 64 dims, and of its 4 chunks of 128
+  unsigned long long block_full[2][8], chunk_empty[2][4];
+  unsigned long long s_full[2];
+  unsigned long long p_full, q_full, q_empty, o_full, drain;
+  unsigned long long piece_full[pieces<N>()], piece_empty[pieces<N>()], info_full[kInfos];
+};
+
+// A page on its way: slots that count, its id (clamped), whether it ends its segment.
+struct PageInfo {
+  int id;
+  int16_t valid, last;
 };
 
 template <int N>
 struct AttendShared {
   alignas(1024) uint8_t keys[2][kKeyStage];
   alignas(1024) uint8_t q[N * 1024];
-  alignas(1024) uint8_t p[2][kSlotsPerPage * 2 * N];
-  float red[kSoftmaxWarps][N];
+  alignas(1024) uint8_t p[kSlotsPerPage * 2 * N];
+  alignas(1024) uint8_t codes[pieces<N>()][kPieceBytes];
+  alignas(16) uint8_t scales[scale_slots<N>()][kScaleBytes];
+  union {
+    float red[kSoftmaxWarps][N];
+    long long scan[kAttendThreads / 32];
+  };
   float ref[N], factor[N];
-  Barriers bar;
-  long long scan[kAttendThreads / 32];
-  long long total;
+  Barriers<N> bar;
+  PageInfo info[kInfos];
+  uint8_t bad[8];  // of the last segments: a page was outside the cache
+  long long total, start_off;
   int start_req;
-  long long start_off;
   uint32_t tmem;
-  int bad[4];
   volatile int abort;
 };
 
@@ -111,24 +159,35 @@ __device__ __forceinline__ void tc_commit(unsigned long long* bar) {
                : "memory");
 }
 
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool accumulate) {
+// Shared-memory operands are described by 64 bits: the start in the low word,
+// the strides and the swizzle (2: 128 bytes, 4: 64, 6: 32).  Rows innermost
+// (the first product): `sbo` bytes between groups of 8 rows.  Columns
+// innermost (the second product): `lbo` between swizzle rows' widths along the
+// columns, `sbo` between groups of 8 along the summed axis.
+__host__ __device__ constexpr uint32_t operand_lo(uint32_t addr, uint32_t lbo) {
+  return (addr >> 4) | (lbo >> 4) << 16;  // shared addresses lie below 2^18
+}
+__host__ __device__ constexpr uint32_t operand_hi(uint32_t sbo, uint32_t swizzle) {
+  return (sbo >> 4) | (1u << 14) | (swizzle << 29);
+}
+
+template <uint32_t kHiA, uint32_t kHiB, uint32_t kInstruction>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %6, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(static_cast<uint32_t>(accumulate)), "n"(kHiA), "n"(kHiB), "r"(kInstruction)
       : "memory");
 }
 
-// Shared-memory operand: start and the two strides in bytes, swizzle 2 (128
-// bytes), 4 (64) or 6 (32).  Rows innermost (dims of a slot for the first
-// product): `sbo` between groups of 8 rows.  Columns innermost (the second
-// product): `lbo` between swizzle rows' widths along the columns, `sbo`
-// between groups of 8 along the summed axis.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) |
-         (static_cast<uint64_t>(swizzle) << 61);
+// One thread of a converged warp, the same one at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // fp32 accumulator, bf16 operands; `transposed`: both with their columns innermost.
@@ -177,6 +236,29 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// dev::mbar_wait_bounded in line (a call would have its registers counted
+// against every role), and with the clock read only if the phase is not
+// complete at once: read at every wait it took 270 cycles of the issuing
+// thread each, 9 times a page.
+__device__ __forceinline__ bool wait_for(unsigned long long* bar, uint32_t parity, long long limit) {
+  const bool poll = limit < dev::kPollBelowCycles;
+  if (!poll && dev::mbar_try_wait(bar, parity)) return true;
+  const long long start = clock64();
+  do {
+    if (poll ? dev::mbar_test_wait(bar, parity) : dev::mbar_try_wait(bar, parity)) return true;
+  } while (clock64() - start <= limit);
+  return false;
 }
 
 // Barrier over the softmax warps; `or` of a predicate.
@@ -249,20 +331,23 @@ __device__ __forceinline__ int share_of(long long total, long long at, int ctas)
 
 // ---- decode -------------------------------------------------------------------------
 
-// What one decode thread holds of a page: thread t has slot t / 4; of each of
-// its 7 groups the codes 16 (t % 4) .. + 15, and 16-byte pieces t % 4 and
-// t % 4 + 4 of its RoPE words.  Four threads read 64 bytes in a row.
-struct RawPage {
-  uint4 codes[7], rope[2];
-  uint2 scale;
-};
+// One tensor copy global -> shared of the box at (x, y, z), completing on `bar`.
+__device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                         unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
 
-struct PageRef {
-  int req, group;
-  int id;      // the page, as the table has it
-  int valid;   // slots of it that count
-  bool first;  // of its segment
-};
+__device__ __forceinline__ void copy_bytes(void* dst, const void* src, uint32_t bytes, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
@@ -270,24 +355,6 @@ __device__ __forceinline__ uint4 load16(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-
-__device__ __forceinline__ void load_page(const AttendParams& p, const PageRef& ref, int t, RawPage* raw) {
-  const int slot = t >> 2, c = t & 3;
-  if (slot < ref.valid && static_cast<uint32_t>(ref.id) < p.num_pages) {
-    const uint8_t* page = p.kv_cache + ref.id * kPageBytes;
-    const uint8_t* row = page + slot * kTokenStride + 16 * c;
-#pragma unroll
-    for (int i = 0; i < 7; ++i) raw->codes[i] = load16(row + 64 * i);
-    raw->rope[0] = load16(row + kNopeDim);
-    raw->rope[1] = load16(row + kNopeDim + 64);
-    raw->scale = __ldg(reinterpret_cast<const uint2*>(page + kScaleBase + slot * kScaleDim));
-  } else {  // code 0 in every place
-#pragma unroll
-    for (int i = 0; i < 7; ++i) raw->codes[i] = make_uint4(0, 0, 0, 0);
-    raw->rope[0] = raw->rope[1] = make_uint4(0, 0, 0, 0);
-    raw->scale = make_uint2(0, 0);
-  }
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -315,37 +382,7 @@ __device__ __forceinline__ void decode4_bf16(uint32_t word, uint32_t up, uint32_
   *hi = fma_bf16x2(mul_bf16x2(__byte_perm(u, 0, 0x4342), 0x7F007F00u), up, less);
 }
 
-__device__ __forceinline__ void store_page(const RawPage& raw, uint8_t* keys, int t) {
-  const int slot = t >> 2, c = t & 3, x = slot & 7;
-  uint8_t* const row = keys + slot * 128;
-#pragma unroll
-  for (int i = 0; i < 7; ++i) {
-    const uint32_t b = ((i < 4 ? raw.scale.x : raw.scale.y) >> (8 * (i & 3))) & 0xFFu;
-    const uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
-    uint32_t v[8];
-    if (b <= 247u) {
-      const uint32_t up = (b + 6u) * 0x00800080u, less = (b + 7u) * 0x00800080u | 0x80008000u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) decode4_bf16(words[j], up, less, &v[2 * j], &v[2 * j + 1]);
-    } else {  // values of 2^121 and above
-      const float hs = half_scale(b);
-      for (int j = 0; j < 4; ++j) {
-        float f[4];
-        decode4(words[j], hs, f);
-        v[2 * j] = bf16_pair(f[0], f[1]);
-        v[2 * j + 1] = bf16_pair(f[2], f[3]);
-      }
-    }
-    uint8_t* const block = row + i * kKeyBlock;
-    *reinterpret_cast<uint4*>(block + (((2 * c) ^ x) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<uint4*>(block + (((2 * c + 1) ^ x) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-  uint8_t* const block = row + 7 * kKeyBlock;
-  *reinterpret_cast<uint4*>(block + ((c ^ x) << 4)) = raw.rope[0];
-  *reinterpret_cast<uint4*>(block + (((c + 4) ^ x) << 4)) = raw.rope[1];
-}
-
-// ---- the kernel -----------------------------------------------------------------------
+// ---- the roles ------------------------------------------------------------------------
 
 template <int N>
 __host__ __device__ constexpr uint32_t tmem_columns() { return N == 64 ? 512 : N == 32 ? 256 : 128; }
@@ -355,121 +392,238 @@ __device__ __forceinline__ int heads_of(const AttendParams& p, int group) {
   return min(p.group_heads, p.num_heads - group * p.group_heads);
 }
 
-// Decode warps: every page of the share to shared memory, and each segment's q.
+// Copies the codes and scales of every page of the share.
 template <int N>
-__device__ void decode_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
-  const int t = threadIdx.x - kSoftmaxThreads, lane = t & 31;
-  auto next_ref = [&]() {  // the walk's page, and one page on
-    PageRef ref{0, 0, 0, 0, false};
-    if (w.left <= 0) return ref;
-    ref.req = w.req;
-    ref.group = w.group;
-    ref.id = __ldg(p.page_table + w.req * p.page_table_row_stride + w.page);
-    ref.valid = min(kSlotsPerPage, w.length - w.page * kSlotsPerPage);
-    ref.first = w.page == 0;
-    w.advance(p, 1);
-    return ref;
-  };
-  const long long count = w.left;
-  PageRef now = next_ref();
-  now.first = true;
-  RawPage raw, raw_next;
-  load_page(p, now, t, &raw);
-  PageRef next = next_ref();
-  int segment = -1;
-  for (long long i = 0; i < count; ++i) {
-    load_page(p, next, t, &raw_next);
-    const PageRef after = next_ref();
-    bool ok = true;
-    if (now.first) {
-      ++segment;
-      if (segment > 0) ok = dev::mbar_wait_bounded(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit);
-      const int heads = heads_of<N>(p, now.group);
-      const uint16_t* q = p.q + now.req * p.q_req_stride + now.group * p.group_heads * p.q_head_stride;
-#pragma unroll 8
-      for (int j = t; j < N * 64; j += kDecodeThreads) {
-        const int h = j >> 6, c = j & 63;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (h < heads) v = *reinterpret_cast<const uint4*>(q + h * p.q_head_stride + 8 * c);
-        *reinterpret_cast<uint4*>(s.q + (c >> 3) * (N * 128) + h * 128 + (((c & 7) ^ (h & 7)) << 4)) = v;
+__device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+  constexpr int kPieces = pieces<N>(), kScales = scale_slots<N>();
+  const int lane = threadIdx.x & 31;
+  long long i = 0, n = 0, infos = 0;  // pages, and (lane 0) pieces and infos on their way so far
+  bool ok = true;
+  for (int segment = 0; ok && w.left > 0; ++segment) {
+    const int count = w.segment();
+    const int32_t* table = p.page_table + w.req * p.page_table_row_stride + w.page;
+    int ids = 0;  // of 32 pages, one a lane
+    for (int pg = 0; ok && pg < count; ++pg, ++i) {
+      if ((pg & 31) == 0) ids = pg + lane < count ? __ldg(table + pg + lane) : 0;
+      const int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
+      const bool there = static_cast<uint32_t>(id) < p.num_pages;
+      if (lane == 0) {
+        if (!there) {
+          s.bad[segment & 7] = 1;
+          atomicCAS(p.error, 0u, kErrBadIndex);
+        }
+        const int valid = there ? min(kSlotsPerPage, w.length - (w.page + pg) * kSlotsPerPage) : 0;
+        const PageInfo info{there ? id : 0, static_cast<int16_t>(valid), static_cast<int16_t>(pg + 1 == count)};
+        for (int g = 0; g < kGroups; ++g, ++n) {
+          const int slot = static_cast<int>(n % kPieces);
+          if (n >= kPieces && !wait_for(&s.bar.piece_empty[slot], (n / kPieces - 1) & 1, p.wait_limit)) {
+            ok = false;
+            break;
+          }
+          if (g == 0) {
+            s.info[i % kInfos] = info;
+            dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], kScaleBytes);
+            copy_bytes(s.scales[i % kScales], p.kv_cache + info.id * kPageBytes + kScaleBase, kScaleBytes,
+                       &s.bar.info_full[i % kInfos]);
+            ++infos;
+          }
+          dev::mbar_arrive_expect_tx(&s.bar.piece_full[slot], kPieceBytes);
+          copy_box(s.codes[slot], &p.code_map, g * kGroup, 0, info.id, &s.bar.piece_full[slot]);
+        }
+        ok = ok && !s.abort;
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);
     }
-    const int stage = i & 1;
-    if (i >= 2)
-      ok = ok && dev::mbar_wait_bounded(&s.bar.kv_empty[stage], ((i >> 1) - 1) & 1, p.wait_limit);
+    w.advance(p, count);
+  }
+  if (!ok) s.abort = 1;
+  if (lane == 0) {  // no copy may land in memory that the CTA has given back
+    for (long long m = n > kPieces ? n - kPieces : 0; m < n; ++m)
+      wait_for(&s.bar.piece_full[m % kPieces], (m / kPieces) & 1, kDefaultWaitLimitCycles);
+    for (long long j = infos > kInfos ? infos - kInfos : 0; j < infos; ++j)
+      wait_for(&s.bar.info_full[j % kInfos], (j / kInfos) & 1, kDefaultWaitLimitCycles);
+  }
+  __syncwarp();
+}
+
+// Copies each segment's queries, in the layout of the products' operand.
+template <int N>
+__device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+  for (int segment = 0; w.left > 0; ++segment) {
+    bool ok = segment == 0 || wait_for(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit);
     if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
       s.abort = 1;
       return;
     }
-    if (now.valid > 0 && static_cast<uint32_t>(now.id) >= p.num_pages) {
-      s.bad[segment & 3] = 1;
-      if (t == 0) atomicCAS(p.error, 0u, kErrBadIndex);
+    if (elect_one()) {
+      dev::mbar_arrive_expect_tx(&s.bar.q_full, N * 1024);
+      for (int b = 0; b < 8; ++b)
+        copy_box(s.q + b * (N * 128), &p.q_map, 64 * b, w.group * p.group_heads, p.q_shared ? 0 : w.req, &s.bar.q_full);
     }
-    store_page(raw, s.keys[stage], t);
+    __syncwarp();
+    wait_for(&s.bar.q_full, segment & 1, kDefaultWaitLimitCycles);
+    w.advance(p, w.segment());
+  }
+}
+
+// Decodes the pieces of warp `v`: 64 slots x 64 codes of one scale group, 8
+// times 8 slots, lane l slot l / 4 of the 8 and codes 16 (l % 4) .. + 15.
+template <int N>
+__device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int v, long long count) {
+  constexpr int kPieces = pieces<N>(), kScales = scale_slots<N>();
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  for (long long n = v; n < count * kGroups; n += decoders<N>()) {
+    const long long i = n / kGroups;
+    const int g = static_cast<int>(n % kGroups), stage = i & 1, slot = static_cast<int>(n % kPieces);
+    bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
+    const int valid = s.info[i % kInfos].valid;
+    uint32_t scale[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
+    ok = ok && wait_for(&s.bar.piece_full[slot], (n / kPieces) & 1, p.wait_limit);
+    uint4 raw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[slot] + (lane + 32 * j) * 16);
+    if (valid < kSlotsPerPage) {  // code 0 in every place of the slots that do not count
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r + 8 * j >= valid) raw[j] = make_uint4(0, 0, 0, 0), scale[j] = 0;
+    }
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(&s.bar.piece_empty[slot]);
+    // decoded before its place is free, so that only the stores are left then
+    uint4 lo[8], hi[8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = max(most, scale[j]);
+    if (__all_sync(0xFFFFFFFFu, most <= 247u)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t up = scale[j] * 0x00800080u + 0x03000300u, less = scale[j] * 0x00800080u + 0x83808380u;
+        decode4_bf16(raw[j].x, up, less, &lo[j].x, &lo[j].y);
+        decode4_bf16(raw[j].y, up, less, &lo[j].z, &lo[j].w);
+        decode4_bf16(raw[j].z, up, less, &hi[j].x, &hi[j].y);
+        decode4_bf16(raw[j].w, up, less, &hi[j].z, &hi[j].w);
+      }
+    } else {  // values of 2^121 and above
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hs = half_scale(scale[j]);
+        float f[16];
+        decode4(raw[j].x, hs, f);
+        decode4(raw[j].y, hs, f + 4);
+        decode4(raw[j].z, hs, f + 8);
+        decode4(raw[j].w, hs, f + 12);
+        lo[j] = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+        hi[j] = make_uint4(bf16_pair(f[8], f[9]), bf16_pair(f[10], f[11]), bf16_pair(f[12], f[13]),
+                           bf16_pair(f[14], f[15]));
+      }
+    }
+    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit);
+    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+      s.abort = 1;
+      return;
+    }
+    uint8_t* const block = s.keys[stage] + g * kKeyBlock + r * 128;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      *reinterpret_cast<uint4*>(block + 1024 * j + (((2 * c) ^ r) << 4)) = lo[j];
+      *reinterpret_cast<uint4*>(block + 1024 * j + (((2 * c + 1) ^ r) << 4)) = hi[j];
+    }
     fence_async_shared();
     __syncwarp();
-    if (lane == 0) dev::mbar_arrive(&s.bar.kv_full[stage]);
-    raw = raw_next;
-    now = next;
-    next = after;
+    if (lane == 0) dev::mbar_arrive(&s.bar.block_full[stage][g]);
+  }
+}
+
+// The RoPE words of every page, read ahead into registers (8 KB, which plain
+// loads can keep on their way) and stored once their place is free: lane l has
+// piece l % 8 of rows l / 8 + 4 j.
+template <int N>
+__device__ void rope_role(const AttendParams& p, AttendShared<N>& s, long long count) {
+  const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7;
+  for (long long i = 0; i < count; ++i) {
+    const int stage = i & 1;
+    bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
+    const PageInfo info = s.info[i % kInfos];
+    const uint8_t* src = p.kv_cache + info.id * kPageBytes + r * kTokenStride + kNopeDim + 16 * c;
+    uint4 v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)  // slots that do not count may hold anything, NaN too
+      v[j] = r + 4 * j < info.valid ? load16(src + 4 * j * kTokenStride) : make_uint4(0, 0, 0, 0);
+    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][3], ((i >> 1) - 1) & 1, p.wait_limit);
+    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+      s.abort = 1;
+      return;
+    }
+    uint8_t* const block = s.keys[stage] + kGroups * kKeyBlock + r * 128;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      *reinterpret_cast<uint4*>(block + 512 * j + ((c ^ (r + 4 * (j & 1))) << 4)) = v[j];
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(&s.bar.block_full[stage][kGroups]);
   }
 }
 
 // One thread: the products of every page, the next page's first product ahead
 // of the present one's second.
 template <int N>
-__device__ void issue_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+__device__ void issue_role(const AttendParams& p, AttendShared<N>& s, long long count) {
   constexpr uint32_t kFirst = instruction(64, N, false), kSecond = instruction(128, N, true);
-  constexpr uint32_t kSwizzleP = N == 64 ? 2 : N == 32 ? 4 : 6;
-  const uint32_t tmem = s.tmem, q = smem_addr(s.q);
-  const long long count = w.left;
-  Walk ahead = w;  // of the first products
-  int ahead_left = ahead.segment(), left = w.segment();
-  bool fresh = true;
+  constexpr uint32_t kRows = operand_hi(1024, 2);
+  constexpr uint32_t kProbs = operand_hi(16 * N, N == 64 ? 2 : N == 32 ? 4 : 6);
+  const uint32_t tmem = s.tmem, q = operand_lo(smem_addr(s.q), 16);
+  int segment = -1;
+  bool last = false, next_last = true;  // of its segment: the present page, the next
   auto first = [&](long long i) {
     const int stage = i & 1;
-    if (!dev::mbar_wait_bounded(&s.bar.kv_full[stage], (i >> 1) & 1, p.wait_limit) || s.abort) return false;
-    tc_fence_after();
-    const uint32_t keys = smem_addr(s.keys[stage]);
-    for (int b = 0; b < 8; ++b)
+    const uint32_t parity = (i >> 1) & 1;
+    last = next_last;
+    if (last && !wait_for(&s.bar.q_full, ++segment & 1, p.wait_limit)) return false;
+    const uint32_t keys = operand_lo(smem_addr(s.keys[stage]), 16);
+#pragma unroll 1  // short loops: straight code of every page came too slowly to the one thread
+    for (int b = 0; b < 8; ++b) {
+      if (!wait_for(&s.bar.block_full[stage][b], parity, p.wait_limit)) return false;
+      tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        tc_mma(tmem + 4 * N + stage * N, operand(keys + b * kKeyBlock + 32 * k, 16, 1024, 2),
-               operand(q + b * (N * 128) + 32 * k, 16, 1024, 2), kFirst, b + k > 0);
-    tc_commit(&s.bar.s_full[stage]);
-    if (--ahead_left == 0) {
-      tc_commit(&s.bar.q_empty);
-      ahead.advance(p, ahead.segment());
-      if (ahead.left > 0) ahead_left = ahead.segment();
+        tc_mma<kRows, kRows, kFirst>(tmem + 4 * N + stage * N, keys + (b * kKeyBlock + 32 * k) / 16,
+                                     q + (b * (N * 128) + 32 * k) / 16, b + k > 0);
     }
-    return true;
+    next_last = s.info[i % kInfos].last;
+    tc_commit(&s.bar.s_full[stage]);
+    if (next_last) tc_commit(&s.bar.q_empty);
+    return !s.abort;
   };
-  bool ok = first(0);
+  bool ok = first(0), fresh = true;
   for (long long i = 0; ok && i < count; ++i) {
-    if (i + 1 < count && !first(i + 1)) { ok = false; break; }
     const int stage = i & 1;
-    ok = dev::mbar_wait_bounded(&s.bar.p_full[stage], (i >> 1) & 1, p.wait_limit) && !s.abort;
+    if (i + 1 < count) {
+      ok = first(i + 1);
+    } else {
+      last = true;
+    }
+    ok = ok && wait_for(&s.bar.p_full, i & 1, p.wait_limit);
     if (!ok) break;
     tc_fence_after();
-    const uint32_t keys = smem_addr(s.keys[stage]), probs = smem_addr(s.p[stage]);
-    for (int c = 0; c < 4; ++c)
+    const uint32_t keys = operand_lo(smem_addr(s.keys[stage]), kKeyBlock);
+    const uint32_t probs = operand_lo(smem_addr(s.p), 16);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        tc_mma(tmem + c * N, operand(keys + 2 * c * kKeyBlock + 2048 * k, kKeyBlock, 1024, 2),
-               operand(probs + k * 32 * N, 16, 16 * N, kSwizzleP), kSecond, !fresh || k > 0);
-    fresh = false;
-    tc_commit(&s.bar.kv_empty[stage]);
-    if (--left == 0) {
-      tc_commit(&s.bar.o_full);
-      w.advance(p, w.segment());
-      if (w.left > 0) left = w.segment();
-      fresh = true;
+        tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
+                                       probs + k * 32 * N / 16, !fresh || k > 0);
+      tc_commit(&s.bar.chunk_empty[stage][c]);  // the decode of page i + 2 follows chunk by chunk
     }
+    if (last) tc_commit(&s.bar.o_full);
+    fresh = last;
   }
   if (!ok) s.abort = 1;
   // no product may run on when the CTA's memory is given back
   tc_commit(&s.bar.drain);
-  dev::mbar_wait_drain(&s.bar.drain, 0);
+  wait_for(&s.bar.drain, 0, kDefaultWaitLimitCycles);
 }
 
 // Softmax warps.  Warp w has slots 16 w .. 16 w + 15 of a page: thread t the
@@ -479,10 +633,12 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
   constexpr int kCols = N / 4;  // columns of a thread
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t tmem = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  const float c = p.scale * kLog2e;
+  const float c = p.scale == 0.f ? 1.f : p.scale * kLog2e;  // scores of scale 0 are zeros
+  const uint32_t behind = c < 0.f ? 0x7F800000u : 0xFF800000u;  // times c: -inf
   const int row = warp * 16 + (lane >> 2);
   long long i = 0;
   long long at = share_start(s.total, cta, ctas);
+  bool ok = true;  // once false, the next vote ends the role
   for (int segment = 0; w.left > 0; ++segment) {
     const int n = w.segment();
     float ref[kCols], sum[kCols];
@@ -490,9 +646,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
     for (int j = 0; j < kCols; ++j) ref[j] = -FLT_MAX, sum[j] = 0.f;
     for (int pg = 0; pg < n; ++pg, ++i) {
       const int stage = i & 1;
-      bool ok = dev::mbar_wait_bounded(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) s.abort = 1;
+      ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit));
       tc_fence_after();
       uint32_t v[2 * kCols];
 #pragma unroll
@@ -500,6 +654,15 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       tmem_wait_ld();
       const int valid = w.length - (w.page + pg) * kSlotsPerPage;
       const bool in0 = row < valid, in1 = row + 8 < valid;
+      if (p.scale == 0.f) {
+#pragma unroll
+        for (int j = 0; j < 2 * kCols; ++j) v[j] = 0;
+      }
+      if (valid < kSlotsPerPage) {  // slots behind the request's last one
+#pragma unroll
+        for (int j = 0; j < 2 * kCols; ++j)
+          if (!((j & 2) ? in1 : in0)) v[j] = behind;
+      }
       if (p.scores != nullptr) {
         float* dst = p.scores + ((w.req * p.max_pages + w.page + pg) * kSlotsPerPage + row) * p.score_cols +
                      w.group * N + 2 * (lane & 3);
@@ -515,22 +678,21 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       }
       float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 2 * kCols; ++j) {
-        const float x = ((j & 2) ? in1 : in0) ? __uint_as_float(v[j]) * c : -INFINITY;
-        v[j] = __float_as_uint(x);
-        top = fmaxf(top, x - ref[(j >> 2) * 2 + (j & 1)]);
-      }
+      for (int j = 0; j < 2 * kCols; ++j)
+        top = fmaxf(top, fmaf(__uint_as_float(v[j]), c, -ref[(j >> 2) * 2 + (j & 1)]));
       if (softmax_any(top > kRescaleAbove || !ok)) {
-        if (softmax_any(s.abort)) return;
+        if (softmax_any(!ok)) {
+          s.abort = 1;
+          return;
+        }
         // the columns' maxima over the page
-        float m[kCols];
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
-          m[j] = fmaxf(__uint_as_float(v[4 * (j >> 1) + (j & 1)]),
-                       __uint_as_float(v[4 * (j >> 1) + 2 + (j & 1)]));
+          float m = fmaxf(__uint_as_float(v[4 * (j >> 1) + (j & 1)]) * c,
+                          __uint_as_float(v[4 * (j >> 1) + 2 + (j & 1)]) * c);
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], d));
-          if (lane < 4) s.red[warp][8 * (j >> 1) + 2 * lane + (j & 1)] = m[j];
+          for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+          if (lane < 4) s.red[warp][8 * (j >> 1) + 2 * lane + (j & 1)] = m;
         }
         softmax_sync();
 #pragma unroll
@@ -545,12 +707,9 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
         }
         softmax_sync();
         if (pg > 0) {  // bring what is summed up so far to the new reference
-          bool done = dev::mbar_wait_bounded(&s.bar.kv_empty[stage ^ 1], ((i - 1) >> 1) & 1, p.wait_limit);
-          if (softmax_any(!done)) {
-            s.abort = 1;
-            return;
-          }
+          ok = __all_sync(0xFFFFFFFFu, wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
           tc_fence_after();
+#pragma unroll 1
           for (int b = 0; b < 4 * N; b += 16) {
             uint32_t o[16];
             tmem_ld_32x16(tmem + b, o);
@@ -563,13 +722,15 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
           tmem_wait_st();
         }
       }
-      uint8_t* const probs = s.p[stage];
+      if (i > 0)  // the products of the page before have read its P
+        ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
+      uint8_t* const probs = s.p;
 #pragma unroll
       for (int j = 0; j < N / 8; ++j) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const float a = exp2_fast(__uint_as_float(v[4 * j + 2 * half]) - ref[2 * j]);
-          const float b = exp2_fast(__uint_as_float(v[4 * j + 2 * half + 1]) - ref[2 * j + 1]);
+          const float a = exp2_fast(fmaf(__uint_as_float(v[4 * j + 2 * half]), c, -ref[2 * j]));
+          const float b = exp2_fast(fmaf(__uint_as_float(v[4 * j + 2 * half + 1]), c, -ref[2 * j + 1]));
           sum[2 * j] += a;
           sum[2 * j + 1] += b;
           const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
@@ -580,7 +741,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       }
       fence_async_shared();
       tc_fence_before();
-      dev::mbar_arrive(&s.bar.p_full[stage]);
+      dev::mbar_arrive(&s.bar.p_full);
     }
     // the segment's end: columns' sums, then the rows of O
 #pragma unroll
@@ -592,7 +753,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       if (warp == 0 && lane < 4) s.ref[col] = ref[j];
     }
     softmax_sync();
-    const bool whole = n == w.pages, bad = s.bad[segment & 3] != 0;
+    const bool whole = n == w.pages, bad = s.bad[segment & 7] != 0;
     const int part = 2 * cta + (segment > 0);
     const int heads = heads_of<N>(p, w.group);
     const int64_t row0 = static_cast<int64_t>(w.req) * p.num_heads + w.group * p.group_heads;
@@ -630,12 +791,12 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
         }
       }
     }
-    bool ok = dev::mbar_wait_bounded(&s.bar.o_full, segment & 1, p.wait_limit);
+    ok = ok && wait_for(&s.bar.o_full, segment & 1, p.wait_limit);
     if (softmax_any(!ok)) {  // also makes s.factor visible
       s.abort = 1;
       return;
     }
-    if (t == 0) s.bad[segment & 3] = 0;
+    if (t == 0) s.bad[segment & 7] = 0;
     tc_fence_after();
     if (!whole || !bad) {
       for (int chunk = 0; chunk < 4; ++chunk) {
@@ -675,25 +836,30 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
 
 template <int N>
 __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __grid_constant__ AttendParams p) {
-  extern __shared__ uint8_t raw_shared[];
-  AttendShared<N>& s = *reinterpret_cast<AttendShared<N>*>(
-      raw_shared + ((1024 - (smem_addr(raw_shared) & 1023)) & 1023));
+  extern __shared__ __align__(1024) uint8_t raw_shared[];
+  AttendShared<N>& s = *reinterpret_cast<AttendShared<N>*>(raw_shared);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int cta = blockIdx.x;
   if (warp == kIssueWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
   if (t == 0) {
     for (int i = 0; i < 2; ++i) {
-      dev::mbar_init(&s.bar.kv_full[i], kDecodeWarps);
-      dev::mbar_init(&s.bar.kv_empty[i], 1);
+      for (int j = 0; j < 8; ++j) dev::mbar_init(&s.bar.block_full[i][j], 1);
+      for (int j = 0; j < 4; ++j) dev::mbar_init(&s.bar.chunk_empty[i][j], 1);
       dev::mbar_init(&s.bar.s_full[i], 1);
-      dev::mbar_init(&s.bar.p_full[i], kSoftmaxThreads);
     }
+    dev::mbar_init(&s.bar.p_full, kSoftmaxThreads);
+    dev::mbar_init(&s.bar.q_full, 1);
     dev::mbar_init(&s.bar.q_empty, 1);
     dev::mbar_init(&s.bar.o_full, 1);
     dev::mbar_init(&s.bar.drain, 1);
+    for (int i = 0; i < pieces<N>(); ++i) {
+      dev::mbar_init(&s.bar.piece_full[i], 1);
+      dev::mbar_init(&s.bar.piece_empty[i], 1);
+    }
+    for (int i = 0; i < kInfos; ++i) dev::mbar_init(&s.bar.info_full[i], 1);
     dev::fence_mbar_init();
     s.abort = 0;
-    for (int i = 0; i < 4; ++i) s.bad[i] = 0;
+    for (int i = 0; i < 8; ++i) s.bad[i] = 0;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -747,11 +913,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     Walk w;
     w.begin(p, s.start_req, s.start_off, count);
     if (warp < kSoftmaxWarps) {
+      more_registers<kSoftmaxRegs>();
       softmax_role<N>(p, s, w, cta, ctas);
     } else if (warp < kIssueWarp) {
-      decode_role<N>(p, s, w);
-    } else if (lane == 0) {
-      issue_role<N>(p, s, w);
+      fewer_registers<kDecodeRegs>();
+      if (warp - kSoftmaxWarps < decoders<N>()) {
+        decode_role<N>(p, s, warp - kSoftmaxWarps, count);
+      } else if (warp == kIssueWarp - 1) {
+        rope_role<N>(p, s, count);
+      }
+    } else if (warp == kIssueWarp) {
+      if (elect_one()) issue_role<N>(p, s, count);
+    } else if (warp == kCopyWarp) {
+      copy_role<N>(p, s, w);
+    } else if (warp == kQueryWarp) {
+      query_role<N>(p, s, w);
     }
   }
   __syncwarp();
@@ -883,7 +1059,8 @@ __global__ void __launch_bounds__(kJoinThreads) kvc_attend_join_kernel(const __g
 
 template <int N>
 cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
-  const size_t smem = sizeof(AttendShared<N>) + 1024;
+  constexpr size_t smem = sizeof(AttendShared<N>);
+  static_assert(smem <= 232448, "227 KB a CTA");
   cudaError_t e = cudaFuncSetAttribute(kvc_attend_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;

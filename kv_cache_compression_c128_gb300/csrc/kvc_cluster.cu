@@ -992,6 +992,17 @@ EncodeTiledFn encode_tiled() {
 
 }  // namespace
 
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                       CUtensorMapSwizzle swizzle) {
+  const EncodeTiledFn fn = encode_tiled();
+  const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+  return fn != nullptr &&
+         fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, unit,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The TMA tensor map of one layer's state when its rows are apart: the 4-D
 // view (256 elements, 4 row segments, block_size rows, num_blocks blocks)
 // with strides (256 elements, row stride, block stride) in bytes, and a box

@@ -123,6 +123,12 @@ cudaError_t launch_cluster(const Params& p, int clusters, cudaStream_t stream);
 bool encode_rows_map(CUtensorMap* map, const void* base, bool f32, int64_t block_size,
                      int64_t num_blocks, int64_t row_bytes, int64_t block_bytes);
 
+// A TMA tensor map of `rank` dimensions, innermost first (host; false when the
+// driver refuses it).  strides: bytes between entries of dimensions 1 ...
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                       CUtensorMapSwizzle swizzle);
+
 // reader direction (kvc_reader.cu)
 cudaError_t launch_dequantize(const uint8_t* kv, int64_t num_pages, const int64_t* slots,
                               int64_t num_slots, void* out, int out_bf16, uint32_t* err,

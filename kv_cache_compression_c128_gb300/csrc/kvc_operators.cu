@@ -86,6 +86,7 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
     return KVC_ERR_INVALID_ARG;
   if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16) ||
       q_req_stride % 8 != 0 || q_head_stride % 8 != 0 || q_req_stride < 0 || q_head_stride < 0 ||
+      (q_head_stride == 0 && num_heads > 1) ||
       !aligned(sinks, 4) || !aligned(lse, 4))
     return KVC_ERR_INVALID_ARG;
   if (slot_weights == nullptr && slot_weights_in != nullptr) return KVC_ERR_INVALID_ARG;
@@ -101,9 +102,26 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
   kvc::AttendParams p = {};
   const kvc_status st = kvc::operator_device(&sms, &p.error, &p.wait_limit);
   if (st != KVC_OK) return st;
-  p.q = static_cast<const uint16_t*>(q);
-  p.q_req_stride = q_req_stride;
-  p.q_head_stride = q_head_stride;
+  const kvc::AttendShape shape = kvc::attend_shape(num_heads);
+  {
+    // a dimension of one entry has no stride, and one of stride 0 has one entry
+    p.q_shared = q_req_stride == 0;
+    const cuuint64_t head_bytes = num_heads == 1 ? 1024 : 2 * static_cast<cuuint64_t>(q_head_stride);
+    const cuuint64_t reqs = p.q_shared ? 1 : num_reqs;
+    const cuuint64_t req_bytes = reqs == 1 ? head_bytes * num_heads : 2 * static_cast<cuuint64_t>(q_req_stride);
+    const cuuint64_t q_dims[3] = {kvc::kHeadDim, static_cast<cuuint64_t>(num_heads), reqs};
+    const cuuint64_t q_strides[2] = {head_bytes, req_bytes};
+    const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(shape.columns), 1};
+    const cuuint64_t page_dims[3] = {kvc::kTokenStride, kvc::kSlotsPerPage, static_cast<cuuint64_t>(num_kv_pages)};
+    const cuuint64_t page_strides[2] = {kvc::kTokenStride, kvc::kPageBytes};
+    const cuuint32_t code_box[3] = {kvc::kGroup, kvc::kSlotsPerPage, 1};
+    if (!kvc::encode_tensor_map(&p.q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, q_dims, q_strides, q_box,
+                                CU_TENSOR_MAP_SWIZZLE_128B))
+      return KVC_ERR_UNSUPPORTED;
+    if (!kvc::encode_tensor_map(&p.code_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, kv_cache, page_dims, page_strides,
+                                code_box, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return KVC_ERR_CUDA;
+  }
   p.num_reqs = num_reqs;
   p.num_heads = num_heads;
   p.kv_cache = kv_cache;
@@ -129,7 +147,6 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
   p.weights_out = slot_weights;
   p.weights_in_row_stride = slot_weights_in_row_stride;
   p.weights_out_row_stride = slot_weights_row_stride;
-  const kvc::AttendShape shape = kvc::attend_shape(num_heads);
   p.groups = shape.groups;
   p.group_heads = shape.group_heads;
   p.score_cols = static_cast<int64_t>(shape.groups) * shape.columns;

@@ -6,6 +6,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kvc_internal.h"
@@ -16,8 +17,9 @@ constexpr int kMaxHeads = 128;
 constexpr int kMaxParts = 8;
 
 struct AttendParams {
-  const uint16_t* q;  // bf16, head h of request r at r * q_req_stride + h * q_head_stride
-  int64_t q_req_stride, q_head_stride;
+  CUtensorMap q_map;     // bf16 [num_reqs][num_heads][512], boxes of `columns` heads x 64 dims
+  CUtensorMap code_map;  // bytes [num_pages][64][576], boxes of 64 slots x 64 bytes
+  int q_shared;          // every request has the queries of request 0
   int64_t num_reqs;
   int num_heads;
   const uint8_t* kv_cache;

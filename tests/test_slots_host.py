@@ -25,7 +25,7 @@ _ATTEND = dict(q=0x10000, q_req_stride=64 * 512, q_head_stride=512, num_reqs=4, 
 
 
 @pytest.mark.parametrize("change", [
-    dict(q=0), dict(q=0x10008), dict(q_req_stride=4), dict(q_head_stride=513), dict(q_head_stride=-512), dict(num_reqs=-1),
+    dict(q=0), dict(q=0x10008), dict(q_req_stride=4), dict(q_head_stride=513), dict(q_head_stride=-512), dict(q_head_stride=0), dict(num_reqs=-1),
     dict(num_reqs=65536), dict(num_heads=0), dict(num_heads=129), dict(kv_cache=0), dict(kv_cache=0x20004),
     dict(num_kv_pages=0), dict(num_kv_pages=1 << 31), dict(page_table=0), dict(page_table=0x30002),
     dict(max_pages_per_req=0), dict(max_pages_per_req=1 << 40), dict(page_table_row_stride=-1), dict(lengths=0),
