@@ -23,8 +23,8 @@
 // column's reference, not its running maximum: any m serves as long as 2^(s - m)
 // stays in range, so O is rescaled only where a score exceeds m by 2^32.
 //
-// Warps of a CTA: 0..3 softmax and epilogue, 4..11 decode, 12 issues the
-// products, 13 copies the codes, 14 the queries.  The codes of a page come by
+// Warps of a CTA: 0..3 softmax and epilogue, one issues the products, one copies
+// the codes, one the queries, seven decode, one brings the RoPE words.  The codes of a page come by
 // TMA in 7 pieces of 64 slots x 64 bytes through a ring of kPieces: 24 KB (N 64)
 // or 56 KB stay on their way whatever the decode does.  (Plain loads of the
 // same bytes kept some 14 KB on the way, for the cache that they pass through
@@ -58,14 +58,17 @@ using dev::kErrTimeout;
 using dev::kLog2e;
 using dev::smem_addr;
 
-constexpr int kSoftmaxWarps = 4, kDecodeWarps = 8;
+constexpr int kSoftmaxWarps = 4;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kIssueWarp = kSoftmaxWarps + kDecodeWarps, kCopyWarp = kIssueWarp + 1, kQueryWarp = kIssueWarp + 2;
-constexpr int kAttendThreads = (kIssueWarp + 4) * 32;  // the last warp only fills up a group of four
-// Registers of a thread by group of warps: 512 x 128 at launch, shared out
-// anew so that no role spills (the cache that a spill would sit in is shared
-// memory here).  128 x 160 + 256 x 112 + 128 x 128 = 512 x 128.
-constexpr int kSoftmaxRegs = 160, kDecodeRegs = 112;
+// Every fourth warp shares a scheduler and its instruction cache: the products'
+// issuer sits with the two copying warps, apart from the decode, whose long
+// loop body would push its short one out.
+constexpr int kIssueWarp = 7, kCopyWarp = 11, kQueryWarp = 15;
+constexpr int kAttendThreads = 16 * 32;
+// Registers of a thread by group of four warps: 512 x 128 at launch, shared
+// out anew so that no role spills (the cache that a spill would sit in is
+// shared memory here).  128 x 168 + 384 x 112 <= 512 x 128.
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 112;
 constexpr int kKeyBlock = kSlotsPerPage * 128;          // 64 slots x 64 dims, bf16
 constexpr int kKeyStage = 8 * kKeyBlock;                // a decoded page
 constexpr int kGroups = 7;                              // of 64 codes with one scale
@@ -75,37 +78,41 @@ constexpr int kScaleBytes = kSlotsPerPage * kScaleDim;
 // the decode of page i + 2 then for theirs, and the copies run less than two
 // pages ahead of the decode: a page's place is taken again by page i + 5 at the
 // earliest.
-constexpr int kInfos = 6;
+constexpr int kInfos = 8;
 constexpr float kRescaleAbove = 32.f;                   // log2
 constexpr int kJoinThreads = 128;
 constexpr int kWeightSlots = 64;                        // slots per CTA of its weights part
 
-// Pieces in the ring: what 227 KB leave at N = 64; two pages' worth otherwise.
+// Groups of a page whose codes come through the ring, one warp and one or two
+// places each.  At N = 64 the 227 KB leave 6 places; with 7 groups in turn on
+// them the seventh piece of a page waited for a warp that was held up by the
+// first one, and every product with it (147 us on the case above; TIME_OWN so).
+// The seventh group is read ahead by its warp then, as the RoPE words are.
 template <int N>
-__host__ __device__ constexpr int pieces() { return N == 64 ? 6 : 14; }
-// Warps that decode: piece n goes to warp n % decoders() from place n %
-// pieces() of the ring, so that a place has one reader, in order.
+__host__ __device__ constexpr int ring_groups() { return N == 64 ? 6 : 7; }
+// Pages that the ring holds, and pages whose scales are kept for its groups:
+// the copy of page i's scales waits for the place of its first piece, so that
+// all pieces of page i - 1 - depth() are read, and their scales before them.
 template <int N>
-__host__ __device__ constexpr int decoders() { return N == 64 ? 6 : 7; }
-// Pages whose scales are kept.  The copy of page i's waits for the ring's place
-// of its first piece, so all pieces of page i - kScales are read if
-// 7 kScales - kPieces >= 6.
+__host__ __device__ constexpr int depth() { return N == 64 ? 1 : 2; }
 template <int N>
-__host__ __device__ constexpr int scale_slots() { return N == 64 ? 2 : 3; }
+__host__ __device__ constexpr int scale_slots() { return N == 64 ? 2 : 4; }
 
-template <int N>
-struct Barriers {
-  // of a stage's 8 blocks of 64 dims, and of its 4 chunks of 128
-  unsigned long long block_full[2][8], chunk_empty[2][4];
-  unsigned long long s_full[2];
-  unsigned long long p_full, q_full, q_empty, o_full, drain;
-  unsigned long long piece_full[pieces<N>()], piece_empty[pieces<N>()], info_full[kInfos];
-};
-
-// A page on its way: slots that count, its id (clamped), whether it ends its segment.
+// A page on its way: its id (clamped), slots that count, whether it ends its segment.
 struct PageInfo {
   int id;
   int16_t valid, last;
+};
+
+template <int N>
+struct Barriers {
+  // Of a stage's halves of 256 dims, and of its chunks of 128.  A wait of the
+  // issuer costs some 250 cycles even if nothing is to be waited for, since
+  // the products' operands keep shared memory busy: two a page, not eight.
+  unsigned long long half_full[2][2], chunk_empty[2][4];
+  unsigned long long s_full[2];
+  unsigned long long p_full, q_full, q_empty, o_full, drain;
+  unsigned long long piece_full[depth<N>()][ring_groups<N>()], piece_empty[depth<N>()][ring_groups<N>()], info_full[kInfos];
 };
 
 template <int N>
@@ -113,18 +120,17 @@ struct AttendShared {
   alignas(1024) uint8_t keys[2][kKeyStage];
   alignas(1024) uint8_t q[N * 1024];
   alignas(1024) uint8_t p[kSlotsPerPage * 2 * N];
-  alignas(1024) uint8_t codes[pieces<N>()][kPieceBytes];
+  alignas(1024) uint8_t codes[depth<N>()][ring_groups<N>()][kPieceBytes];
   alignas(16) uint8_t scales[scale_slots<N>()][kScaleBytes];
   union {
     float red[kSoftmaxWarps][N];
-    long long scan[kAttendThreads / 32];
+    int scan[kAttendThreads / 32];
   };
   float ref[N], factor[N];
   Barriers<N> bar;
   PageInfo info[kInfos];
   uint8_t bad[8];  // of the last segments: a page was outside the cache
-  long long total, start_off;
-  int start_req;
+  int total, start_req, start_off;
   uint32_t tmem;
   volatile int abort;
 };
@@ -287,19 +293,19 @@ __device__ __forceinline__ int pages_of(const AttendParams& p, int64_t length) {
 // Where a CTA is in its share: page `page` of `pages` of unit (req, group).
 struct Walk {
   int req, group, page, pages, length;
-  long long left;  // pages of the share from here on
+  int left;  // pages of the share from here on
 
-  __device__ void begin(const AttendParams& p, int r, long long off, long long count) {
+  __device__ void begin(const AttendParams& p, int r, int off, int count) {
     req = r;
     left = count;
     if (count <= 0) return;
     length = p.lengths[r];
     pages = pages_of(p, length);
-    group = static_cast<int>(off / pages);
-    page = static_cast<int>(off % pages);
+    group = off / pages;
+    page = off % pages;
   }
   __device__ int segment() const {
-    return static_cast<int>(min(static_cast<long long>(pages - page), left));
+    return min(pages - page, left);
   }
   // On by `n` pages, at most to the unit's end.
   __device__ void advance(const AttendParams& p, int n) {
@@ -317,13 +323,13 @@ struct Walk {
 };
 
 // Start of CTA c's share of `total` pages among `ctas`.
-__device__ __forceinline__ long long share_start(long long total, int c, int ctas) {
-  return total * c / ctas;
+__device__ __forceinline__ int share_start(int total, int c, int ctas) {
+  return static_cast<int>(static_cast<long long>(total) * c / ctas);
 }
 
 // The CTA whose share holds page `at`.
-__device__ __forceinline__ int share_of(long long total, long long at, int ctas) {
-  int c = static_cast<int>(((at + 1) * ctas - 1) / total);
+__device__ __forceinline__ int share_of(int total, int at, int ctas) {
+  int c = static_cast<int>((static_cast<long long>(at + 1) * ctas - 1) / total);
   while (c > 0 && share_start(total, c, ctas) > at) --c;
   while (c + 1 < ctas && share_start(total, c + 1, ctas) <= at) ++c;
   return c;
@@ -395,18 +401,21 @@ __device__ __forceinline__ int heads_of(const AttendParams& p, int group) {
 // Copies the codes and scales of every page of the share.
 template <int N>
 __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
-  constexpr int kPieces = pieces<N>(), kScales = scale_slots<N>();
+  constexpr int kDepth = depth<N>(), kScales = scale_slots<N>(), kRing = ring_groups<N>();
   const int lane = threadIdx.x & 31;
-  long long i = 0, n = 0, infos = 0;  // pages, and (lane 0) pieces and infos on their way so far
+  int i = 0, g = 0;  // pages begun; of the last one, the pieces asked for (lane 0)
   bool ok = true;
+#pragma unroll 1
   for (int segment = 0; ok && w.left > 0; ++segment) {
     const int count = w.segment();
     const int32_t* table = p.page_table + w.req * p.page_table_row_stride + w.page;
     int ids = 0;  // of 32 pages, one a lane
-    for (int pg = 0; ok && pg < count; ++pg, ++i) {
+#pragma unroll 1
+    for (int pg = 0; ok && pg < count; ++pg) {
       if ((pg & 31) == 0) ids = pg + lane < count ? __ldg(table + pg + lane) : 0;
       const int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
       const bool there = static_cast<uint32_t>(id) < p.num_pages;
+      const int place = i % kDepth, turn = i / kDepth;
       if (lane == 0) {
         if (!there) {
           s.bad[segment & 7] = 1;
@@ -414,9 +423,9 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
         }
         const int valid = there ? min(kSlotsPerPage, w.length - (w.page + pg) * kSlotsPerPage) : 0;
         const PageInfo info{there ? id : 0, static_cast<int16_t>(valid), static_cast<int16_t>(pg + 1 == count)};
-        for (int g = 0; g < kGroups; ++g, ++n) {
-          const int slot = static_cast<int>(n % kPieces);
-          if (n >= kPieces && !wait_for(&s.bar.piece_empty[slot], (n / kPieces - 1) & 1, p.wait_limit)) {
+#pragma unroll 1
+        for (g = 0; g < kRing; ++g) {
+          if (turn > 0 && !wait_for(&s.bar.piece_empty[place][g], (turn - 1) & 1, p.wait_limit)) {
             ok = false;
             break;
           }
@@ -425,22 +434,29 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
             dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], kScaleBytes);
             copy_bytes(s.scales[i % kScales], p.kv_cache + info.id * kPageBytes + kScaleBase, kScaleBytes,
                        &s.bar.info_full[i % kInfos]);
-            ++infos;
           }
-          dev::mbar_arrive_expect_tx(&s.bar.piece_full[slot], kPieceBytes);
-          copy_box(s.codes[slot], &p.code_map, g * kGroup, 0, info.id, &s.bar.piece_full[slot]);
+          dev::mbar_arrive_expect_tx(&s.bar.piece_full[place][g], kPieceBytes);
+          copy_box(s.codes[place][g], &p.code_map, g * kGroup, 0, info.id, &s.bar.piece_full[place][g]);
         }
         ok = ok && !s.abort;
       }
+      ++i;
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
     w.advance(p, count);
   }
   if (!ok) s.abort = 1;
   if (lane == 0) {  // no copy may land in memory that the CTA has given back
-    for (long long m = n > kPieces ? n - kPieces : 0; m < n; ++m)
-      wait_for(&s.bar.piece_full[m % kPieces], (m / kPieces) & 1, kDefaultWaitLimitCycles);
-    for (long long j = infos > kInfos ? infos - kInfos : 0; j < infos; ++j)
+    const int whole = i > 0 && g < kRing ? i - 1 : i;  // pages asked for in full; g pieces of page `whole` besides
+#pragma unroll 1
+    for (int k = 0; k < kDepth * kRing; ++k) {
+      const int place = k / kRing, piece = k % kRing;
+      const int times = (whole + kDepth - 1 - place) / kDepth + (whole < i && whole % kDepth == place && piece < g);
+      if (times > 0) wait_for(&s.bar.piece_full[place][piece], (times - 1) & 1, kDefaultWaitLimitCycles);
+    }
+    const int infos = whole + (whole < i && g > 0);
+#pragma unroll 1
+    for (int j = max(0, infos - kInfos); j < infos; ++j)
       wait_for(&s.bar.info_full[j % kInfos], (j / kInfos) & 1, kDefaultWaitLimitCycles);
   }
   __syncwarp();
@@ -449,6 +465,7 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
 // Copies each segment's queries, in the layout of the products' operand.
 template <int N>
 __device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+#pragma unroll 1
   for (int segment = 0; w.left > 0; ++segment) {
     bool ok = segment == 0 || wait_for(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit);
     if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
@@ -457,6 +474,7 @@ __device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
     }
     if (elect_one()) {
       dev::mbar_arrive_expect_tx(&s.bar.q_full, N * 1024);
+#pragma unroll 1
       for (int b = 0; b < 8; ++b)
         copy_box(s.q + b * (N * 128), &p.q_map, 64 * b, w.group * p.group_heads, p.q_shared ? 0 : w.req, &s.bar.q_full);
     }
@@ -466,37 +484,47 @@ __device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
   }
 }
 
-// Decodes the pieces of warp `v`: 64 slots x 64 codes of one scale group, 8
-// times 8 slots, lane l slot l / 4 of the 8 and codes 16 (l % 4) .. + 15.
+// Decodes group g of every page: 64 slots x 64 codes, 8 times 8 slots, lane l
+// slot l / 4 of the 8 and codes 16 (l % 4) .. + 15.
 template <int N>
-__device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int v, long long count) {
-  constexpr int kPieces = pieces<N>(), kScales = scale_slots<N>();
+__device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, int count) {
+  constexpr int kDepth = depth<N>(), kScales = scale_slots<N>(), kRing = ring_groups<N>();
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  for (long long n = v; n < count * kGroups; n += decoders<N>()) {
-    const long long i = n / kGroups;
-    const int g = static_cast<int>(n % kGroups), stage = i & 1, slot = static_cast<int>(n % kPieces);
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const int stage = i & 1;
     bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
     const int valid = s.info[i % kInfos].valid;
     uint32_t scale[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
-    ok = ok && wait_for(&s.bar.piece_full[slot], (n / kPieces) & 1, p.wait_limit);
     uint4 raw[8];
+    if (g < kRing) {
+      const int place = i % kDepth;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[slot] + (lane + 32 * j) * 16);
-    if (valid < kSlotsPerPage) {  // code 0 in every place of the slots that do not count
+      for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
+      ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[place][g] + (lane + 32 * j) * 16);
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
+    } else {
+      const uint8_t* page = p.kv_cache + s.info[i % kInfos].id * kPageBytes;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        raw[j] = load16(page + (r + 8 * j) * kTokenStride + g * kGroup + 16 * c);
+        scale[j] = __ldg(page + kScaleBase + (r + 8 * j) * kScaleDim + g);
+      }
+    }
+    if (__builtin_expect(valid < kSlotsPerPage, 0)) {  // code 0 in every place of the slots that do not count
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (r + 8 * j >= valid) raw[j] = make_uint4(0, 0, 0, 0), scale[j] = 0;
     }
-    __syncwarp();
-    if (lane == 0) dev::mbar_arrive(&s.bar.piece_empty[slot]);
     // decoded before its place is free, so that only the stores are left then
     uint4 lo[8], hi[8];
     uint32_t most = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = max(most, scale[j]);
-    if (__all_sync(0xFFFFFFFFu, most <= 247u)) {
+    if (__builtin_expect(__all_sync(0xFFFFFFFFu, most <= 247u), 1)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t up = scale[j] * 0x00800080u + 0x03000300u, less = scale[j] * 0x00800080u + 0x83808380u;
@@ -532,7 +560,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int v, lo
     }
     fence_async_shared();
     __syncwarp();
-    if (lane == 0) dev::mbar_arrive(&s.bar.block_full[stage][g]);
+    if (lane == 0) dev::mbar_arrive(&s.bar.half_full[stage][g >> 2]);
   }
 }
 
@@ -540,9 +568,10 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int v, lo
 // loads can keep on their way) and stored once their place is free: lane l has
 // piece l % 8 of rows l / 8 + 4 j.
 template <int N>
-__device__ void rope_role(const AttendParams& p, AttendShared<N>& s, long long count) {
+__device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) {
   const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7;
-  for (long long i = 0; i < count; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
     const int stage = i & 1;
     bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
     const PageInfo info = s.info[i % kInfos];
@@ -562,67 +591,91 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N>& s, long long c
       *reinterpret_cast<uint4*>(block + 512 * j + ((c ^ (r + 4 * (j & 1))) << 4)) = v[j];
     fence_async_shared();
     __syncwarp();
-    if (lane == 0) dev::mbar_arrive(&s.bar.block_full[stage][kGroups]);
+    if (lane == 0) dev::mbar_arrive(&s.bar.half_full[stage][1]);
   }
 }
 
-// One thread: the products of every page, the next page's first product ahead
-// of the present one's second.
+// The products of every page: whatever can be issued next, a half of the
+// following page's first product before the present page's second.  The whole
+// warp walks, one elected thread issues.  One short loop: the two questions
+// travel together and behind products already queued, and every role's code has
+// to stay in the instruction cache beside the others'.
 template <int N>
-__device__ void issue_role(const AttendParams& p, AttendShared<N>& s, long long count) {
+__device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count) {
   constexpr uint32_t kFirst = instruction(64, N, false), kSecond = instruction(128, N, true);
   constexpr uint32_t kRows = operand_hi(1024, 2);
   constexpr uint32_t kProbs = operand_hi(16 * N, N == 64 ? 2 : N == 32 ? 4 : 6);
-  const uint32_t tmem = s.tmem, q = operand_lo(smem_addr(s.q), 16);
-  int segment = -1;
-  bool last = false, next_last = true;  // of its segment: the present page, the next
-  auto first = [&](long long i) {
-    const int stage = i & 1;
-    const uint32_t parity = (i >> 1) & 1;
-    last = next_last;
-    if (last && !wait_for(&s.bar.q_full, ++segment & 1, p.wait_limit)) return false;
-    const uint32_t keys = operand_lo(smem_addr(s.keys[stage]), 16);
-#pragma unroll 1  // short loops: straight code of every page came too slowly to the one thread
-    for (int b = 0; b < 8; ++b) {
-      if (!wait_for(&s.bar.block_full[stage][b], parity, p.wait_limit)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma<kRows, kRows, kFirst>(tmem + 4 * N + stage * N, keys + (b * kKeyBlock + 32 * k) / 16,
-                                     q + (b * (N * 128) + 32 * k) / 16, b + k > 0);
-    }
-    next_last = s.info[i % kInfos].last;
-    tc_commit(&s.bar.s_full[stage]);
-    if (next_last) tc_commit(&s.bar.q_empty);
-    return !s.abort;
-  };
-  bool ok = first(0), fresh = true;
-  for (long long i = 0; ok && i < count; ++i) {
-    const int stage = i & 1;
-    if (i + 1 < count) {
-      ok = first(i + 1);
-    } else {
-      last = true;
-    }
-    ok = ok && wait_for(&s.bar.p_full, i & 1, p.wait_limit);
-    if (!ok) break;
-    tc_fence_after();
-    const uint32_t keys = operand_lo(smem_addr(s.keys[stage]), kKeyBlock);
-    const uint32_t probs = operand_lo(smem_addr(s.p), 16);
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s.tmem, 0);
+  const uint32_t q = operand_lo(smem_addr(s.q), 16), all_keys = smem_addr(s.keys);
+  const uint32_t probs = operand_lo(smem_addr(s.p), 16);
+  int halves = 0, done = 0;      // halves of first products and whole second products issued
+  int segment = 0;               // segments begun
+  bool begins = true;            // the next half begins a segment
+  bool ends[2] = {true, false};  // the page of each stage ends its segment
+  bool fresh = true;             // the next second product is its segment's first
+  bool ok = true;
+  long long since = clock64();
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+  while (done < count) {
+    const int i = halves >> 1, half = halves & 1, stage = i & 1;
+    bool first = i < count && dev::mbar_test_wait(&s.bar.half_full[stage][half], (i >> 1) & 1);
+    if (begins) first = first && dev::mbar_test_wait(&s.bar.q_full, segment & 1);
+    const bool second = done < i && dev::mbar_test_wait(&s.bar.p_full, done & 1);
+    if (__all_sync(0xFFFFFFFFu, first)) {
+      tc_fence_after();
+      const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + half * (4 * kKeyBlock), 16);
+      const uint32_t queries = q + half * (4 * N * 128 / 16), into = tmem + 4 * N + stage * N;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
-                                       probs + k * 32 * N / 16, !fresh || k > 0);
-      tc_commit(&s.bar.chunk_empty[stage][c]);  // the decode of page i + 2 follows chunk by chunk
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma<kRows, kRows, kFirst>(into, keys + (b * kKeyBlock + 32 * k) / 16,
+                                         queries + (b * (N * 128) + 32 * k) / 16, half + b + k > 0);
+      }
+      segment += begins;
+      begins = false;
+      if (half == 1) {
+        begins = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
+        ends[0] = stage == 0 ? begins : ends[0];
+        ends[1] = stage == 1 ? begins : ends[1];
+        if (elect_one()) {
+          tc_commit(&s.bar.s_full[stage]);
+          if (begins) tc_commit(&s.bar.q_empty);
+        }
+      }
+      ++halves;
+    } else if (__all_sync(0xFFFFFFFFu, second)) {
+      tc_fence_after();
+      const int of = done & 1;
+      const bool last = of == 0 ? ends[0] : ends[1];
+      const uint32_t keys = operand_lo(all_keys + of * kKeyStage, kKeyBlock);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
+                                           probs + k * 32 * N / 16, !fresh || k > 0);
+          tc_commit(&s.bar.chunk_empty[of][c]);  // the decode of page i + 2 follows chunk by chunk
+        }
+      }
+      if (last && elect_one()) tc_commit(&s.bar.o_full);
+      fresh = last;
+      ++done;
+    } else {
+      if (__any_sync(0xFFFFFFFFu, clock64() - since > p.wait_limit || s.abort)) {
+        ok = false;
+        break;
+      }
+      continue;
     }
-    if (last) tc_commit(&s.bar.o_full);
-    fresh = last;
+    since = clock64();
   }
   if (!ok) s.abort = 1;
   // no product may run on when the CTA's memory is given back
-  tc_commit(&s.bar.drain);
+  if (elect_one()) tc_commit(&s.bar.drain);
+  __syncwarp();
   wait_for(&s.bar.drain, 0, kDefaultWaitLimitCycles);
 }
 
@@ -636,14 +689,15 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
   const float c = p.scale == 0.f ? 1.f : p.scale * kLog2e;  // scores of scale 0 are zeros
   const uint32_t behind = c < 0.f ? 0x7F800000u : 0xFF800000u;  // times c: -inf
   const int row = warp * 16 + (lane >> 2);
-  long long i = 0;
-  long long at = share_start(s.total, cta, ctas);
+  int i = 0, at = share_start(s.total, cta, ctas);
   bool ok = true;  // once false, the next vote ends the role
+#pragma unroll 1
   for (int segment = 0; w.left > 0; ++segment) {
     const int n = w.segment();
     float ref[kCols], sum[kCols];
 #pragma unroll
     for (int j = 0; j < kCols; ++j) ref[j] = -FLT_MAX, sum[j] = 0.f;
+#pragma unroll 1
     for (int pg = 0; pg < n; ++pg, ++i) {
       const int stage = i & 1;
       ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit));
@@ -654,16 +708,16 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       tmem_wait_ld();
       const int valid = w.length - (w.page + pg) * kSlotsPerPage;
       const bool in0 = row < valid, in1 = row + 8 < valid;
-      if (p.scale == 0.f) {
+      if (__builtin_expect(p.scale == 0.f, 0)) {
 #pragma unroll
         for (int j = 0; j < 2 * kCols; ++j) v[j] = 0;
       }
-      if (valid < kSlotsPerPage) {  // slots behind the request's last one
+      if (__builtin_expect(valid < kSlotsPerPage, 0)) {  // slots behind the request's last one
 #pragma unroll
         for (int j = 0; j < 2 * kCols; ++j)
           if (!((j & 2) ? in1 : in0)) v[j] = behind;
       }
-      if (p.scores != nullptr) {
+      if (__builtin_expect(p.scores != nullptr, 0)) {
         float* dst = p.scores + ((w.req * p.max_pages + w.page + pg) * kSlotsPerPage + row) * p.score_cols +
                      w.group * N + 2 * (lane & 3);
 #pragma unroll
@@ -680,7 +734,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
 #pragma unroll
       for (int j = 0; j < 2 * kCols; ++j)
         top = fmaxf(top, fmaf(__uint_as_float(v[j]), c, -ref[(j >> 2) * 2 + (j & 1)]));
-      if (softmax_any(top > kRescaleAbove || !ok)) {
+      if (__builtin_expect(softmax_any(top > kRescaleAbove || !ok), 0)) {
         if (softmax_any(!ok)) {
           s.abort = 1;
           return;
@@ -722,22 +776,24 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
           tmem_wait_st();
         }
       }
+      __nv_bfloat162 pair[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {  // columns of j / 2, rows of j % 2
+        const int col = j & ~1;
+        const float a = exp2_fast(fmaf(__uint_as_float(v[2 * j]), c, -ref[col]));
+        const float b = exp2_fast(fmaf(__uint_as_float(v[2 * j + 1]), c, -ref[col + 1]));
+        sum[col] += a;
+        sum[col + 1] += b;
+        pair[j] = __floats2bfloat162_rn(a, b);
+      }
       if (i > 0)  // the products of the page before have read its P
-        ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
-      uint8_t* const probs = s.p;
+        ok = __all_sync(0xFFFFFFFFu,
+                        ok && wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
 #pragma unroll
-      for (int j = 0; j < N / 8; ++j) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float a = exp2_fast(fmaf(__uint_as_float(v[4 * j + 2 * half]), c, -ref[2 * j]));
-          const float b = exp2_fast(fmaf(__uint_as_float(v[4 * j + 2 * half + 1]), c, -ref[2 * j + 1]));
-          sum[2 * j] += a;
-          sum[2 * j + 1] += b;
-          const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
-          const uint32_t off = (row + 8 * half) * (2 * N) + 16 * j + 4 * (lane & 3);
-          constexpr uint32_t kMask = N / 8 - 1;  // 16-byte pieces of a row
-          *reinterpret_cast<__nv_bfloat162*>(probs + (off ^ (((off >> 7) & kMask) << 4))) = ab;
-        }
+      for (int j = 0; j < kCols; ++j) {
+        const uint32_t off = (row + 8 * (j & 1)) * (2 * N) + 16 * (j >> 1) + 4 * (lane & 3);
+        constexpr uint32_t kMask = N / 8 - 1;  // 16-byte pieces of a row
+        *reinterpret_cast<__nv_bfloat162*>(s.p + (off ^ (((off >> 7) & kMask) << 4))) = pair[j];
       }
       fence_async_shared();
       tc_fence_before();
@@ -799,8 +855,10 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
     if (t == 0) s.bad[segment & 7] = 0;
     tc_fence_after();
     if (!whole || !bad) {
+#pragma unroll 1
       for (int chunk = 0; chunk < 4; ++chunk) {
         const int d = chunk * 128 + warp * 32 + lane;
+#pragma unroll 1
         for (int b = 0; b < heads; b += 16) {
           uint32_t o[16];
           tmem_ld_32x16(tmem + chunk * N + b, o);
@@ -843,7 +901,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   if (warp == kIssueWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
   if (t == 0) {
     for (int i = 0; i < 2; ++i) {
-      for (int j = 0; j < 8; ++j) dev::mbar_init(&s.bar.block_full[i][j], 1);
+      for (int j = 0; j < 2; ++j) dev::mbar_init(&s.bar.half_full[i][j], 4);
       for (int j = 0; j < 4; ++j) dev::mbar_init(&s.bar.chunk_empty[i][j], 1);
       dev::mbar_init(&s.bar.s_full[i], 1);
     }
@@ -852,9 +910,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     dev::mbar_init(&s.bar.q_empty, 1);
     dev::mbar_init(&s.bar.o_full, 1);
     dev::mbar_init(&s.bar.drain, 1);
-    for (int i = 0; i < pieces<N>(); ++i) {
-      dev::mbar_init(&s.bar.piece_full[i], 1);
-      dev::mbar_init(&s.bar.piece_empty[i], 1);
+    for (int i = 0; i < depth<N>() * ring_groups<N>(); ++i) {
+      dev::mbar_init(&s.bar.piece_full[0][0] + i, 1);
+      dev::mbar_init(&s.bar.piece_empty[0][0] + i, 1);
     }
     for (int i = 0; i < kInfos; ++i) dev::mbar_init(&s.bar.info_full[i], 1);
     dev::fence_mbar_init();
@@ -866,42 +924,44 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   // pages before each thread's run of requests
   const int run = static_cast<int>((p.num_reqs + kAttendThreads - 1) / kAttendThreads);
   const int lo = min(static_cast<int>(p.num_reqs), t * run), hi = min(static_cast<int>(p.num_reqs), lo + run);
-  long long mine = 0;
+  int mine = 0;  // the host has checked that all pages fit 31 bits
   bool bad_length = false;
+#pragma unroll 1
   for (int r = lo; r < hi; ++r) {
     const int64_t length = p.lengths[r];
     mine += pages_of(p, length);
     bad_length = bad_length || length < 0 || length > p.max_slots;
   }
   if (bad_length && cta == 0) atomicCAS(p.error, 0u, kErrBadIndex);
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
     if (lane >= d) inc += o;
   }
   if (lane == 31) s.scan[warp] = inc;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long before = inc - mine, total = 0;
+  int before = inc - mine, total = 0;
   for (int i = 0; i < kAttendThreads / 32; ++i) {
     if (i < warp) before += s.scan[i];
     total += s.scan[i];
   }
   total *= p.groups;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total, 1LL)));
-  const long long start = cta < ctas ? share_start(total, cta, ctas) : 0;
-  const long long count = cta < ctas ? share_start(total, cta + 1, ctas) - start : 0;
+  const int ctas = min(static_cast<int>(gridDim.x), max(total, 1));
+  const int start = cta < ctas ? share_start(total, cta, ctas) : 0;
+  const int count = cta < ctas ? share_start(total, cta + 1, ctas) - start : 0;
   if (t == 0) {
     s.total = total;
     p.joins[cta] = make_int4(-1, 0, 0, 0);
   }
   if (count > 0 && start >= before * p.groups && start < (before + mine) * p.groups) {
-    long long off = start - before * p.groups;
+    int off = start - before * p.groups;
     int r = lo;
+#pragma unroll 1
     for (;; ++r) {
-      const long long here = static_cast<long long>(pages_of(p, p.lengths[r])) * p.groups;
+      const int here = pages_of(p, p.lengths[r]) * p.groups;
       if (off < here) break;
       off -= here;
     }
@@ -915,19 +975,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     if (warp < kSoftmaxWarps) {
       more_registers<kSoftmaxRegs>();
       softmax_role<N>(p, s, w, cta, ctas);
-    } else if (warp < kIssueWarp) {
-      fewer_registers<kDecodeRegs>();
-      if (warp - kSoftmaxWarps < decoders<N>()) {
-        decode_role<N>(p, s, warp - kSoftmaxWarps, count);
-      } else if (warp == kIssueWarp - 1) {
+    } else {
+      fewer_registers<kOtherRegs>();
+      const int worker = 3 * (warp / 4 - 1) + warp % 4;  // of those not on the issuer's scheduler
+      if (warp == kIssueWarp) {
+        issue_role<N>(p, s, count);
+      } else if (warp == kCopyWarp) {
+        copy_role<N>(p, s, w);
+      } else if (warp == kQueryWarp) {
+        query_role<N>(p, s, w);
+      } else if (worker < kGroups) {
+        decode_role<N>(p, s, worker, count);
+      } else if (worker == kGroups) {
         rope_role<N>(p, s, count);
       }
-    } else if (warp == kIssueWarp) {
-      if (elect_one()) issue_role<N>(p, s, count);
-    } else if (warp == kCopyWarp) {
-      copy_role<N>(p, s, w);
-    } else if (warp == kQueryWarp) {
-      query_role<N>(p, s, w);
     }
   }
   __syncwarp();

@@ -98,6 +98,8 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
                                                  slot_weights != nullptr);
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need)
     return KVC_ERR_INVALID_ARG;
+  // pages are counted in 31 bits, over all requests and head groups
+  if (num_reqs * max_pages_per_req * kvc::attend_shape(num_heads).groups > INT32_MAX) return KVC_ERR_UNSUPPORTED;
   int sms = 0;
   kvc::AttendParams p = {};
   const kvc_status st = kvc::operator_device(&sms, &p.error, &p.wait_limit);
