@@ -595,9 +595,10 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) 
   }
 }
 
-// The products of every page: whatever can be issued next, a half of the
-// following page's first product before the present page's second.  The whole
-// warp walks, one elected thread issues.  One short loop: the two questions
+// The products of every page: whatever can be issued next, a page's second
+// product, which frees the place of the page after next, before a half of the
+// next page's first.  The whole warp walks, one elected thread issues.  One
+// short loop: the two questions
 // travel together and behind products already queued, and every role's code has
 // to stay in the instruction cache beside the others'.
 template <int N>
@@ -621,7 +622,25 @@ __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count)
     bool first = i < count && dev::mbar_test_wait(&s.bar.half_full[stage][half], (i >> 1) & 1);
     if (begins) first = first && dev::mbar_test_wait(&s.bar.q_full, segment & 1);
     const bool second = done < i && dev::mbar_test_wait(&s.bar.p_full, done & 1);
-    if (__all_sync(0xFFFFFFFFu, first)) {
+    if (__all_sync(0xFFFFFFFFu, second)) {
+      tc_fence_after();
+      const int of = done & 1;
+      const bool last = of == 0 ? ends[0] : ends[1];
+      const uint32_t keys = operand_lo(all_keys + of * kKeyStage, kKeyBlock);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
+                                           probs + k * 32 * N / 16, !fresh || k > 0);
+          tc_commit(&s.bar.chunk_empty[of][c]);  // the decode of page i + 2 follows chunk by chunk
+        }
+      }
+      if (last && elect_one()) tc_commit(&s.bar.o_full);
+      fresh = last;
+      ++done;
+    } else if (__all_sync(0xFFFFFFFFu, first)) {
       tc_fence_after();
       const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + half * (4 * kKeyBlock), 16);
       const uint32_t queries = q + half * (4 * N * 128 / 16), into = tmem + 4 * N + stage * N;
@@ -645,24 +664,6 @@ __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count)
         }
       }
       ++halves;
-    } else if (__all_sync(0xFFFFFFFFu, second)) {
-      tc_fence_after();
-      const int of = done & 1;
-      const bool last = of == 0 ? ends[0] : ends[1];
-      const uint32_t keys = operand_lo(all_keys + of * kKeyStage, kKeyBlock);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
-                                           probs + k * 32 * N / 16, !fresh || k > 0);
-          tc_commit(&s.bar.chunk_empty[of][c]);  // the decode of page i + 2 follows chunk by chunk
-        }
-      }
-      if (last && elect_one()) tc_commit(&s.bar.o_full);
-      fresh = last;
-      ++done;
     } else {
       if (__any_sync(0xFFFFFFFFu, clock64() - since > p.wait_limit || s.abort)) {
         ok = false;
