@@ -79,9 +79,12 @@ constexpr int kScaleBytes = kSlotsPerPage * kScaleDim;
 // pages ahead of the decode: a page's place is taken again by page i + 5 at the
 // earliest.
 constexpr int kInfos = 8;
+// Pages by which the longest unit may exceed an equal share before units are
+// divided: joining the parts costs about as much as this many pages.
+constexpr int kUndivided = 3;
 constexpr float kRescaleAbove = 32.f;                   // log2
-constexpr int kJoinThreads = 128;
-constexpr int kWeightSlots = 64;                        // slots per CTA of its weights part
+constexpr int kJoinThreads = 512, kJoinCtasPerSm = 2;
+constexpr int kWeightSlots = 64;                        // slots at least for a CTA that forms weights
 
 // Groups of a page whose codes come through the ring, one warp and one or two
 // places each.  At N = 64 the 227 KB leave 6 places; with 7 groups in turn on
@@ -124,13 +127,14 @@ struct AttendShared {
   alignas(16) uint8_t scales[scale_slots<N>()][kScaleBytes];
   union {
     float red[kSoftmaxWarps][N];
-    int scan[kAttendThreads / 32];
+    int4 scan[kAttendThreads / 32];
   };
   float ref[N], factor[N];
   Barriers<N> bar;
   PageInfo info[kInfos];
   uint8_t bad[8];  // of the last segments: a page was outside the cache
   int total, start_req, start_off;
+  int start_pages;  // of the first unit
   uint32_t tmem;
   volatile int abort;
 };
@@ -690,7 +694,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
   const float c = p.scale == 0.f ? 1.f : p.scale * kLog2e;  // scores of scale 0 are zeros
   const uint32_t behind = c < 0.f ? 0x7F800000u : 0xFF800000u;  // times c: -inf
   const int row = warp * 16 + (lane >> 2);
-  int i = 0, at = share_start(s.total, cta, ctas);
+  int i = 0, at = share_start(s.total, cta, ctas);  // (used where units are divided)
   bool ok = true;  // once false, the next vote ends the role
 #pragma unroll 1
   for (int segment = 0; w.left > 0; ++segment) {
@@ -835,9 +839,8 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
     }
     if (t == 0) {
       if (w.page == 0) {  // the unit's first part: where its parts lie
-        const int last = share_of(s.total, at + w.pages - 1, ctas);
         p.unit_parts[static_cast<int64_t>(w.req) * p.groups + w.group] =
-            whole ? make_int2(-1, bad) : make_int2(part, last);
+            whole ? make_int2(-1, bad) : make_int2(part, share_of(s.total, at + w.pages - 1, ctas));
       }
       if (!whole) {
         p.part_bad[part] = bad;
@@ -925,51 +928,72 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   // pages before each thread's run of requests
   const int run = static_cast<int>((p.num_reqs + kAttendThreads - 1) / kAttendThreads);
   const int lo = min(static_cast<int>(p.num_reqs), t * run), hi = min(static_cast<int>(p.num_reqs), lo + run);
-  int mine = 0;  // the host has checked that all pages fit 31 bits
+  // the pages (the host has checked that all fit 31 bits) and the units
+  int mine = 0, mine_units = 0, longest = 0;
   bool bad_length = false;
 #pragma unroll 1
   for (int r = lo; r < hi; ++r) {
     const int64_t length = p.lengths[r];
-    mine += pages_of(p, length);
+    const int pages = pages_of(p, length);
+    mine += pages;
+    mine_units += pages > 0;
+    longest = max(longest, pages);
     bad_length = bad_length || length < 0 || length > p.max_slots;
   }
   if (bad_length && cta == 0) atomicCAS(p.error, 0u, kErrBadIndex);
-  int inc = mine;
+  int inc = mine, inc_units = mine_units;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-    if (lane >= d) inc += o;
+    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d), u = __shfl_up_sync(0xFFFFFFFFu, inc_units, d);
+    if (lane >= d) inc += o, inc_units += u;
   }
-  if (lane == 31) s.scan[warp] = inc;
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  if (lane == 31) s.scan[warp] = make_int4(inc, inc_units, longest, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int before = inc - mine, total = 0;
+  int before = inc - mine, before_units = inc_units - mine_units, total = 0, units = 0;
+#pragma unroll 1
   for (int i = 0; i < kAttendThreads / 32; ++i) {
-    if (i < warp) before += s.scan[i];
-    total += s.scan[i];
+    const int4 of = s.scan[i];
+    if (i < warp) before += of.x, before_units += of.y;
+    total += of.x;
+    units += of.y;
+    longest = max(longest, of.z);
   }
   total *= p.groups;
-  const int ctas = min(static_cast<int>(gridDim.x), max(total, 1));
-  const int start = cta < ctas ? share_start(total, cta, ctas) : 0;
-  const int count = cta < ctas ? share_start(total, cta + 1, ctas) - start : 0;
+  units *= p.groups;
+  // A unit to each CTA, if the longest takes no more than kUndivided pages over
+  // an equal share: no parts, nothing to join.
+  const int grid = static_cast<int>(gridDim.x);
+  const bool by_unit = units <= grid && longest <= total / grid + kUndivided;
+  const int ctas = by_unit ? units : min(grid, max(total, 1));
+  int start = 0, count = 0;
+  if (cta < ctas) {
+    start = by_unit ? cta : share_start(total, cta, ctas);
+    count = by_unit ? 1 : share_start(total, cta + 1, ctas) - start;
+  }
   if (t == 0) {
     s.total = total;
     p.joins[cta] = make_int4(-1, 0, 0, 0);
   }
-  if (count > 0 && start >= before * p.groups && start < (before + mine) * p.groups) {
-    int off = start - before * p.groups;
-    int r = lo;
+  const int first = by_unit ? before_units : before, here = by_unit ? mine_units : mine;
+  if (count > 0 && start >= first * p.groups && start < (first + here) * p.groups) {
+    int off = start - first * p.groups, r = lo;
 #pragma unroll 1
     for (;; ++r) {
-      const int here = pages_of(p, p.lengths[r]) * p.groups;
-      if (off < here) break;
-      off -= here;
+      const int pages = pages_of(p, p.lengths[r]), size = (by_unit ? pages > 0 : pages) * p.groups;
+      if (off < size) {
+        s.start_req = r;
+        s.start_off = by_unit ? off * pages : off;
+        s.start_pages = pages;
+        break;
+      }
+      off -= size;
     }
-    s.start_req = r;
-    s.start_off = off;
   }
   __syncthreads();
+  if (by_unit && count > 0) count = s.start_pages;
   if (count > 0) {
     Walk w;
     w.begin(p, s.start_req, s.start_off, count);
@@ -1004,118 +1028,202 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
 
 // ---- joining kernel -----------------------------------------------------------------
 
-// Log-sum-exp of one head of a unit from its parts' (m, l) and its sink: the
-// reference and the total above it.
-__device__ __forceinline__ float2 unit_total(const AttendParams& p, int n, int first, int last, int col,
-                                             int head) {
-  float top = p.sinks == nullptr ? -INFINITY : p.sinks[head] * kLog2e;
-  const float sink = top;
-  for (int part = first;; part = (part | 1) + 1) {
-    top = fmaxf(top, p.part_stats[part * n + col].x);
-    if (part >> 1 == last) break;
+// A divided unit: its parts lie in the first one's place and then in the first
+// places of the shares up to the last.
+struct Division {
+  int first, last;  // first part, last CTA
+  __device__ int count() const { return last - (first >> 1) + 1; }
+  __device__ int part(int j) const { return j == 0 ? first : 2 * ((first >> 1) + j); }
+};
+
+// Log-sum-exp (log2) of one head of a divided unit from its parts' (m, l) and
+// its sink, in one pass over the parts; whether one of them is bad.
+__device__ __forceinline__ float unit_lse(const AttendParams& p, int n, const Division& d, int col, int head,
+                                          bool* bad) {
+  float top = p.sinks == nullptr ? -FLT_MAX : fmaxf(p.sinks[head] * kLog2e, -FLT_MAX);
+  float total = p.sinks == nullptr ? 0.f : exp2_fast(p.sinks[head] * kLog2e - top);
+  const int count = d.count();
+  int any = 0;
+#pragma unroll 8
+  for (int j = 0; j < count; ++j) {
+    const float2 ml = p.part_stats[d.part(j) * n + col];
+    any |= p.part_bad[d.part(j)];
+    const float next = fmaxf(top, ml.x);
+    total = total * exp2_fast(top - next) + ml.y * exp2_fast(ml.x - next);
+    top = next;
   }
-  float total = p.sinks == nullptr ? 0.f : exp2_fast(sink - top);
-  for (int part = first;; part = (part | 1) + 1) {
-    const float2 ml = p.part_stats[part * n + col];
-    total += ml.y * exp2_fast(ml.x - top);
-    if (part >> 1 == last) break;
-  }
-  return make_float2(top, total);
+  *bad = any != 0;
+  return total == 0.f ? -INFINITY : top + log2f(total);
 }
 
-// CTAs 0 .. ctas * heads - 1: one head of the unit that share c completes (if
-// it was divided).  Then, per request: zeros for one without slots, and its
-// slots' weights.
-__global__ void __launch_bounds__(kJoinThreads) kvc_attend_join_kernel(const __grid_constant__ AttendParams p,
-                                                                        int n, int ctas, int chunks) {
+// One head of a divided unit: 128 threads with 4 dims each add parts `from`,
+// `from` + `step`, ...  Every warp forms the parts' weights for itself, in `w`.
+// Returns the sum; `scale` and `lse` are what finishes it.
+__device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const Division& d, int col, int head,
+                                             int from, int step, float* w, float* scale, float* lse, bool* bad) {
+  const int lane = threadIdx.x & 31, t = threadIdx.x & 127, count = d.count();
+  const float4* const parts = reinterpret_cast<const float4*>(p.parts) + col * (kHeadDim / 4) + t;
+  const int64_t apart = static_cast<int64_t>(n) * (kHeadDim / 4);
+  const float sink = p.sinks == nullptr ? -INFINITY : p.sinks[head] * kLog2e;
+  float top = sink, total = 0.f;
+  bool any_bad = false;
+#pragma unroll 1
+  for (int j = lane; j < count; j += 32) {
+    const float m = p.part_stats[d.part(j) * n + col].x;
+    any_bad = any_bad || p.part_bad[d.part(j)] != 0;
+    w[j] = m;
+    top = fmaxf(top, m);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+#pragma unroll 1
+  for (int j = lane; j < count; j += 32) {
+    const float f = exp2_fast(w[j] - top);
+    total += p.part_stats[d.part(j) * n + col].y * f;
+    w[j] = f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  if (p.sinks != nullptr) total += exp2_fast(sink - top);
+  *bad = __any_sync(0xFFFFFFFFu, any_bad);
+  *scale = total == 0.f ? 0.f : 1.f / total;
+  *lse = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
+  __syncwarp();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int j = from; j < count; j += step) {
+    const float f = w[j];
+    const float4 o = parts[d.part(j) * apart];
+    acc.x += f * o.x;
+    acc.y += f * o.y;
+    acc.z += f * o.z;
+    acc.w += f * o.w;
+  }
+  __syncwarp();  // w is free again
+  return acc;
+}
+
+__device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row, int t, float4 v, float f, float lse) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * f, v.w * f);
+  reinterpret_cast<uint2*>(p.out + row * kHeadDim)[t] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (t == 0) p.lse[row] = lse;
+}
+
+// Joins the divided units, zeroes the rows without slots, forms the weights.
+// An item is a head of a divided unit: one of 128 threads' work if that fills
+// the grid, else the whole CTA's, its four groups a quarter of the parts each.
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_kernel(const __grid_constant__ AttendParams p,
+                                                                        int n, int ctas, int weight_ctas) {
+  __shared__ int4 joins[kAttendCtas];
+  __shared__ int warp_joins[kJoinThreads / 32];
+  __shared__ float4 quarters[3][128];
+  __shared__ float part_weights[kJoinThreads / 32][kAttendCtas];
+  __shared__ __align__(16) float total[2 * 64];
+  __shared__ int skip;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int t = threadIdx.x;
-  const int join_ctas = ctas * p.group_heads;
-  if (blockIdx.x < join_ctas) {
-    const int4 join = p.joins[blockIdx.x / p.group_heads];
-    const int col = blockIdx.x % p.group_heads;
-    const int head = join.y * p.group_heads + col;
-    if (join.x < 0 || head >= p.num_heads) return;
-    for (int part = join.z;; part = (part | 1) + 1) {
-      if (p.part_bad[part]) return;
-      if (part >> 1 == join.w) break;
-    }
-    const float2 mt = unit_total(p, n, join.z, join.w, col, head);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int part = join.z;; part = (part | 1) + 1) {
-      const float f = exp2_fast(p.part_stats[part * n + col].x - mt.x);
-      const float4 o = reinterpret_cast<const float4*>(p.parts + (static_cast<int64_t>(part) * n + col) * kHeadDim)[t];
-      acc.x += f * o.x;
-      acc.y += f * o.y;
-      acc.z += f * o.z;
-      acc.w += f * o.w;
-      if (part >> 1 == join.w) break;
-    }
-    const float f = mt.y == 0.f ? 0.f : 1.f / mt.y;
-    const int64_t row = static_cast<int64_t>(join.x) * p.num_heads + head;
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-    reinterpret_cast<uint2*>(p.out + row * kHeadDim)[t] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    if (t == 0) p.lse[row] = mt.y == 0.f ? -INFINITY : (mt.x + log2f(mt.y)) / kLog2e;
-    return;
-  }
-  const int item = blockIdx.x - join_ctas;
-  const int r = item / chunks, chunk = item % chunks;
-  const int64_t length = p.lengths[r];
-  if (length < 0 || length > p.max_slots) return;
-  if (length == 0) {
-    if (chunk != 0) return;
-    const int64_t row0 = static_cast<int64_t>(r) * p.num_heads;
-    uint4* out = reinterpret_cast<uint4*>(p.out + row0 * kHeadDim);
-    for (int i = t; i < p.num_heads * (kHeadDim / 8); i += kJoinThreads) out[i] = make_uint4(0, 0, 0, 0);
-    for (int h = t; h < p.num_heads; h += kJoinThreads) p.lse[row0 + h] = p.sinks == nullptr ? -INFINITY : p.sinks[h];
-    return;
-  }
-  if (p.weights_out == nullptr) return;
-  // the heads' log2-sum-exp, by column of the scores; +inf where there is no head or no key
-  __shared__ float total[2 * 64];
-  __shared__ int skip;
-  if (t == 0) skip = 0;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  // the divided units, in order
+  const int4 mine = t < ctas ? p.joins[t] : make_int4(-1, 0, 0, 0);
+  const uint32_t there = __ballot_sync(0xFFFFFFFFu, mine.x >= 0);
+  if (lane == 0) warp_joins[warp] = __popc(there);
   __syncthreads();
-  for (int col = t; col < p.score_cols; col += kJoinThreads) {
-    const int group = col / n, c = col % n, head = group * p.group_heads + c;
-    float v = INFINITY;
-    if (c < p.group_heads && head < p.num_heads) {
-      const int2 parts = p.unit_parts[static_cast<int64_t>(r) * p.groups + group];
-      if (parts.x < 0) {
-        if (parts.y) skip = 1;
-        v = p.lse[static_cast<int64_t>(r) * p.num_heads + head] * kLog2e;
-      } else {
-        for (int part = parts.x;; part = (part | 1) + 1) {
-          if (p.part_bad[part]) skip = 1;
-          if (part >> 1 == parts.y) break;
+  int before = __popc(there & ((1u << lane) - 1)), divided = 0;
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < warp) before += warp_joins[i];
+    divided += warp_joins[i];
+  }
+  if (mine.x >= 0) joins[before] = mine;
+  __syncthreads();
+  const int items = divided * p.group_heads, grid = static_cast<int>(gridDim.x), group = t >> 7;
+  const bool apart = items >= 2 * grid;  // an item to each 128 threads
+  for (int item = apart ? 4 * static_cast<int>(blockIdx.x) + group : static_cast<int>(blockIdx.x); item < items;
+       item += apart ? 4 * grid : grid) {
+    const int4 join = joins[item / p.group_heads];
+    const int col = item % p.group_heads, head = join.y * p.group_heads + col;
+    if (head >= p.num_heads) continue;
+    float f, lse;
+    bool bad;
+    float4 v = join_parts(p, n, Division{join.z, join.w}, col, head, apart ? 0 : group, apart ? 1 : 4,
+                          part_weights[warp], &f, &lse, &bad);
+    if (!apart) {
+      if (group > 0) quarters[group - 1][t & 127] = v;
+      __syncthreads();
+      if (group == 0) {
+        for (int g = 0; g < 3; ++g) {
+          const float4 o = quarters[g][t];
+          v.x += o.x;
+          v.y += o.y;
+          v.z += o.z;
+          v.w += o.w;
         }
-        const float2 mt = unit_total(p, n, parts.x, parts.y, c, head);
-        v = mt.y == 0.f ? -INFINITY : mt.x + log2f(mt.y);
       }
-      if (v == -INFINITY) v = INFINITY;
+      __syncthreads();
     }
-    total[col] = v;
+    if (!bad && (apart || group == 0))
+      store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, t & 127, v, f, lse);
   }
-  __syncthreads();
-  if (skip) return;
-  const int lane = t & 31, warp = t >> 5;
-  const int width = p.score_cols < 32 ? static_cast<int>(p.score_cols) : 32, sub = lane / width, of = 32 / width;
-  for (int i = warp * of + sub; i < kWeightSlots; i += (kJoinThreads / 32) * of) {
-    const int64_t slot = static_cast<int64_t>(chunk) * kWeightSlots + i;
-    float sum = 0.f;
-    if (slot < length) {
-      const float* scores = p.scores + (r * p.max_pages * kSlotsPerPage + slot) * p.score_cols;
-      for (int col = lane % width; col < p.score_cols; col += width)
-        if (total[col] != INFINITY) sum += exp2_fast(scores[col] - total[col]);
+  // requests: `weight_ctas` CTAs for each
+  for (int item = blockIdx.x; item < p.num_reqs * weight_ctas; item += grid) {
+    const int r = item / weight_ctas, sub = item % weight_ctas;
+    const int64_t length = p.lengths[r];
+    if (length < 0 || length > p.max_slots) continue;
+    if (length == 0) {
+      if (sub != 0) continue;
+      const int64_t row0 = static_cast<int64_t>(r) * p.num_heads;
+      uint4* out = reinterpret_cast<uint4*>(p.out + row0 * kHeadDim);
+      for (int i = t; i < p.num_heads * (kHeadDim / 8); i += kJoinThreads) out[i] = make_uint4(0, 0, 0, 0);
+      for (int h = t; h < p.num_heads; h += kJoinThreads)
+        p.lse[row0 + h] = p.sinks == nullptr ? -INFINITY : p.sinks[h];
+      continue;
     }
-    for (int d = width / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (slot < length && lane % width == 0)
-      p.weights_out[r * p.weights_out_row_stride + slot] =
-          (p.weights_in == nullptr ? 0.f : p.weights_in[r * p.weights_in_row_stride + slot]) + sum;
+    if (p.weights_out == nullptr || length * sub / weight_ctas == length * (sub + 1) / weight_ctas) continue;
+    // the heads' log2-sum-exp, by column of the scores; +inf where there is no head or no key
+    if (t == 0) skip = 0;
+    __syncthreads();
+    for (int col = t; col < p.score_cols; col += kJoinThreads) {
+      const int unit = col / n, c = col % n, head = unit * p.group_heads + c;
+      float v = INFINITY;
+      if (c < p.group_heads && head < p.num_heads) {
+        const int2 parts = p.unit_parts[static_cast<int64_t>(r) * p.groups + unit];
+        if (parts.x < 0) {
+          if (parts.y) skip = 1;
+          v = p.lse[static_cast<int64_t>(r) * p.num_heads + head] * kLog2e;
+        } else {
+          bool bad;
+          v = unit_lse(p, n, Division{parts.x, parts.y}, c, head, &bad);
+          if (bad) skip = 1;
+        }
+        if (v == -INFINITY) v = INFINITY;
+      }
+      total[col] = v;
+    }
+    __syncthreads();
+    if (!skip) {
+      // 4 columns a thread, `lanes` threads a slot
+      const int lanes = static_cast<int>(p.score_cols) / 4, step = kJoinThreads / lanes;
+      const float4 l = *reinterpret_cast<const float4*>(total + 4 * (t % lanes));
+      const float* const weights_in = p.weights_in == nullptr ? nullptr : p.weights_in + r * p.weights_in_row_stride;
+      float* const weights_out = p.weights_out + r * p.weights_out_row_stride;
+      const float4* const scores =
+          reinterpret_cast<const float4*>(p.scores + r * p.max_pages * kSlotsPerPage * p.score_cols) + t % lanes;
+      const int begin = static_cast<int>(length * sub / weight_ctas), end = static_cast<int>(length * (sub + 1) / weight_ctas);
+#pragma unroll 4
+      for (int slot = begin + t / lanes; slot < end + t / lanes; slot += step) {  // a warp stays together
+        float sum = 0.f, old = 0.f;
+        if (slot < end) {
+          const float4 x = scores[static_cast<int64_t>(slot) * lanes];
+          if (weights_in != nullptr) old = weights_in[slot];
+          sum = (l.x == INFINITY ? 0.f : exp2_fast(x.x - l.x)) + (l.y == INFINITY ? 0.f : exp2_fast(x.y - l.y)) +
+                (l.z == INFINITY ? 0.f : exp2_fast(x.z - l.z)) + (l.w == INFINITY ? 0.f : exp2_fast(x.w - l.w));
+        }
+        for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if (slot < end && t % lanes == 0) weights_out[slot] = old + sum;
+      }
+    }
+    __syncthreads();  // total and skip are free again
   }
 }
 
@@ -1138,12 +1246,18 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N>, p);
   if (e != cudaSuccess) return e;
+  // as many as fit at once: they share the divided units' heads, then the requests
+  constexpr int kMost = kJoinCtasPerSm * kAttendCtas;
   const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kWeightSlots - 1) / kWeightSlots;
-  const int64_t grid = static_cast<int64_t>(ctas) * p.group_heads + p.num_reqs * (chunks > 0 ? chunks : 1);
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  int64_t weight_ctas = 2 * kMost / p.num_reqs;
+  weight_ctas = weight_ctas > chunks ? chunks : weight_ctas;
+  weight_ctas = weight_ctas < 1 ? 1 : weight_ctas;
+  const int64_t joins = static_cast<int64_t>(ctas) * p.group_heads, items = p.num_reqs * weight_ctas;
+  const int64_t work = joins > items ? joins : items;
+  cfg.gridDim = dim3(static_cast<unsigned>(work < kMost ? work : kMost));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kvc_attend_join_kernel, p, N, ctas, static_cast<int>(chunks > 0 ? chunks : 1));
+  return cudaLaunchKernelEx(&cfg, kvc_attend_join_kernel, p, N, ctas, static_cast<int>(weight_ctas));
 }
 
 }  // namespace
