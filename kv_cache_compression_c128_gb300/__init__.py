@@ -636,63 +636,94 @@ def compress_layers(state_caches, token_to_req, positions, boundary_token_indice
 
 
 # ---- operators on packed slots ------------------------------------------------
+#
+# These are called once per layer and token, with little work in a small batch:
+# the checks below read each attribute once and make no objects in passing.
 
-def _operator_checks():
-    """torch and the (name, tensor, dtype, dim, device) check of the operators
-    below: columns contiguous, rows at any stride."""
-    import torch
+_torch = None
 
-    def check(name, t, dtype, dim, dev):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-        if t.dim() != dim:
-            raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise ValueError(f"{name} must have contiguous columns")
 
-    return torch, check
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _refuse(name, t, dtype, dim, device):
+    """Raise for the first property of `t` that is not as an operator needs it."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    raise ValueError(f"{name} must have contiguous columns")
+
+
+def _rows(name, t, dtype, device):
+    """(rows, columns, row stride) of a 2-D tensor with contiguous columns."""
+    if not isinstance(t, _torch.Tensor) or t.dtype != dtype or t.get_device() != device or t.dim() != 2:
+        _refuse(name, t, dtype, 2, device)
+    rows, cols = t.shape
+    row, col = t.stride()
+    if col != 1 and cols > 1:
+        _refuse(name, t, dtype, 2, device)
+    return rows, cols, row
+
+
+def _dense(name, t, dtype, device, shape):
+    """A contiguous tensor of a given shape."""
+    if not isinstance(t, _torch.Tensor) or t.dtype != dtype or t.get_device() != device or t.dim() != len(shape):
+        _refuse(name, t, dtype, len(shape), device)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cache(kv_cache, page_table, lengths):
+    """(device index, pages, requests, page table columns, its row stride)"""
+    if not isinstance(kv_cache, _torch.Tensor) or not kv_cache.is_cuda:
+        raise ValueError("kv_cache must be a CUDA tensor (there is no CPU path)")
+    device = kv_cache.get_device()
+    if kv_cache.dtype != _torch.uint8 or kv_cache.dim() != 2:
+        _refuse("kv_cache", kv_cache, _torch.uint8, 2, device)
+    pages, width = kv_cache.shape
+    if width != KV_PAGE_BYTES or not kv_cache.is_contiguous():
+        raise ValueError(f"kv_cache must be contiguous [num_pages, {KV_PAGE_BYTES}] uint8")
+    reqs, columns, row = _rows("page_table", page_table, _torch.int32, device)
+    _dense("lengths", lengths, _torch.int32, device, (reqs,))
+    return device, pages, reqs, columns, row
 
 
 class _on:
-    """Context of an operator call: its device current, and its stream too
-    while results and workspaces are allocated (memory of another stream's
-    pool could still be in use there)."""
+    """Context of an operator call where the caller's device is not current, or
+    a stream is given: both current while results and workspaces are allocated
+    (memory of another stream's pool could still be in use there)."""
 
-    def __init__(self, torch, dev, stream):
-        self.torch, self.stream, self.entered = torch, stream, []
-        if torch.cuda.current_device() != dev.index:
-            self.entered.append(torch.cuda.device(dev))
-        if stream is not None:
-            self.entered.append(torch.cuda.stream(stream))
-        self.dev = dev
+    def __init__(self, device, stream):
+        cuda = _torch.cuda
+        self.entered = [cuda.device(device)] + ([] if stream is None else [cuda.stream(stream)])
 
     def __enter__(self):
         for c in self.entered:
             c.__enter__()
-        s = self.stream if self.stream is not None else self.torch.cuda.current_stream(self.dev)
-        return s.cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self.entered):
             c.__exit__(*exc)
 
 
-def _check_cache(check, torch, kv_cache, page_table, lengths):
-    dev = kv_cache.device
-    if dev.type != "cuda":
-        raise ValueError("kv_cache must be a CUDA tensor (there is no CPU path)")
-    check("kv_cache", kv_cache, torch.uint8, 2, dev)
-    if kv_cache.shape[1] != KV_PAGE_BYTES or not kv_cache.is_contiguous():
-        raise ValueError(f"kv_cache must be contiguous [num_pages, {KV_PAGE_BYTES}] uint8")
-    check("page_table", page_table, torch.int32, 2, dev)
-    check("lengths", lengths, torch.int32, 1, dev)
-    if lengths.shape[0] != page_table.shape[0]:
-        raise ValueError("page_table and lengths must have one row per request")
-    return dev
+def _run(call, device, stream):
+    """call(raw stream), on the operator's device and stream."""
+    cuda = _torch.cuda
+    if stream is None and cuda.current_device() == device:
+        return call(_torch._C._cuda_getCurrentRawStream(device))
+    with _on(device, stream):
+        return call(cuda.current_stream(device).cuda_stream)
 
 
 def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None, lse=None,
@@ -711,65 +742,65 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
     (zero without it; may be the same tensor) plus the slot's softmax weight
     summed over the heads: what `evict` goes by.  A request whose length or
     pages are out of range keeps its rows as they were and raises the device
-    error word (kvc_get_device_error).
+    error word (kvc_get_device_error).  A workspace given by the caller
+    (kvc_attend_workspace_bytes) serves calls that do not overlap.
     """
-    torch, check = _operator_checks()
-    dev = _check_cache(check, torch, kv_cache, page_table, lengths)
-    check("q", q, torch.bfloat16, 3, dev)
-    R, H, D = q.shape
+    torch = _torch or _load_torch()
+    device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.get_device() != device or q.dim() != 3:
+        _refuse("q", q, torch.bfloat16, 3, device)
+    shape = q.shape
+    reqs, H, D = shape
     if D != HEAD_DIM or not 1 <= H <= 128:
         raise ValueError("q must be [num_reqs, 1..128 heads, 512]")
-    if page_table.shape[0] != R:
+    if reqs != R:
         raise ValueError("q and page_table must have one row per request")
+    by_req, by_head, by_dim = q.stride()
+    if by_dim != 1:
+        _refuse("q", q, torch.bfloat16, 3, device)
     if sinks is not None:
-        check("sinks", sinks, torch.float32, 1, dev)
-        if sinks.shape[0] != H:
-            raise ValueError("sinks must have one entry per head")
-    S = 0
+        _dense("sinks", sinks, torch.float32, device, (H,))
+    S = weights_row = in_row = 0
     if slot_weights is not None:
-        check("slot_weights", slot_weights, torch.float32, 2, dev)
-        S = slot_weights.shape[1]
-        if slot_weights.shape[0] != R:
+        rows, S, weights_row = _rows("slot_weights", slot_weights, torch.float32, device)
+        if rows != R:
             raise ValueError("slot_weights must have one row per request")
     if slot_weights_in is not None:
-        check("slot_weights_in", slot_weights_in, torch.float32, 2, dev)
-        if slot_weights is None or slot_weights_in.shape != slot_weights.shape:
+        rows, cols, in_row = _rows("slot_weights_in", slot_weights_in, torch.float32, device)
+        if slot_weights is None or (rows, cols) != (R, S):
             raise ValueError("slot_weights_in needs slot_weights of the same shape")
-    with _on(torch, dev, stream) as sp:
-        if H > 1 and q.stride(1) == 0:  # one query for all heads
+    if out is not None:
+        _dense("out", out, torch.bfloat16, device, shape)
+    if lse is not None:
+        _dense("lse", lse, torch.float32, device, shape[:2])
+    if workspace is not None:
+        _dense("workspace", workspace, torch.uint8, device, (workspace.numel(),))
+    if R != 0 and columns == 0:
+        raise ValueError("page_table must have at least one column")
+
+    def call(raw):
+        nonlocal q, by_req, by_head, out, lse, workspace
+        if H > 1 and by_head == 0:  # one query for all heads
             q = q.contiguous()
+            by_req, by_head, _ = q.stride()
         if out is None:
-            out = torch.empty((R, H, HEAD_DIM), dtype=torch.bfloat16, device=dev)
-        else:
-            check("out", out, torch.bfloat16, 3, dev)
-            if out.shape != q.shape or not out.is_contiguous():
-                raise ValueError("out must be contiguous [num_reqs, num_heads, 512]")
+            out = torch.empty((R, H, HEAD_DIM), dtype=torch.bfloat16, device=kv_cache.device)
         if lse is None:
-            lse = torch.empty((R, H), dtype=torch.float32, device=dev)
-        else:
-            check("lse", lse, torch.float32, 2, dev)
-            if lse.shape != q.shape[:2] or not lse.is_contiguous():
-                raise ValueError("lse must be contiguous [num_reqs, num_heads]")
-        if R == 0 or page_table.shape[1] == 0:
-            if R != 0:
-                raise ValueError("page_table must have at least one column")
-            return out, lse
+            lse = torch.empty((R, H), dtype=torch.float32, device=kv_cache.device)
+        if R == 0:
+            return KVC_OK
         if workspace is None:
-            workspace = torch.empty(
-                kvc_attend_workspace_bytes(R, H, page_table.shape[1], slot_weights is not None),
-                dtype=torch.uint8, device=dev)
-        else:
-            check("workspace", workspace, torch.uint8, 1, dev)
-        st = kvc_attend(
-            q.data_ptr(), q.stride(0), q.stride(1), R, H, kv_cache.data_ptr(), kv_cache.shape[0],
-            page_table.data_ptr(), page_table.shape[1], page_table.stride(0), lengths.data_ptr(),
-            HEAD_DIM ** -0.5 if scale is None else scale,
+            workspace = torch.empty(kvc_attend_workspace_bytes(R, H, columns, slot_weights is not None),
+                                    dtype=torch.uint8, device=kv_cache.device)
+        return kvc_attend(
+            q.data_ptr(), by_req, by_head, R, H, kv_cache.data_ptr(), pages, page_table.data_ptr(),
+            columns, row, lengths.data_ptr(), HEAD_DIM ** -0.5 if scale is None else scale,
             None if sinks is None else sinks.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            None if slot_weights_in is None else slot_weights_in.data_ptr(),
-            0 if slot_weights_in is None else slot_weights_in.stride(0),
-            None if slot_weights is None else slot_weights.data_ptr(),
-            0 if slot_weights is None else slot_weights.stride(0), S, workspace.data_ptr(),
-            workspace.numel(), flags, sp)
+            None if slot_weights_in is None else slot_weights_in.data_ptr(), in_row,
+            None if slot_weights is None else slot_weights.data_ptr(), weights_row, S,
+            workspace.data_ptr(), workspace.numel(), flags, raw)
+
+    st = _run(call, device, stream)
     if st != KVC_OK:
         raise KvcError(st, "kvc_attend")
     return out, lse
@@ -783,38 +814,37 @@ def join(outs, lses, *, out=None, lse=None, stream=None):
     (-inf: the part held no key for the row).  Returns (out, lse); `out` may
     be one of outs and `lse` one of lses.
     """
-    torch, check = _operator_checks()
+    torch = _torch or _load_torch()
     if not 1 <= len(outs) <= 8 or len(lses) != len(outs):
         raise ValueError("outs and lses need one entry per part, 1 to 8 parts")
     first = outs[0]
-    dev, dtype, shape = first.device, first.dtype, first.shape
-    if dev.type != "cuda":
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise ValueError("outs must be CUDA tensors (there is no CPU path)")
-    if dtype not in (torch.float32, torch.bfloat16):
+    device, dtype, shape = first.get_device(), first.dtype, first.shape
+    if dtype != torch.bfloat16 and dtype != torch.float32:
         raise TypeError("outs must have dtype torch.float32 or torch.bfloat16")
     if len(shape) < 1 or shape[-1] != HEAD_DIM:
         raise ValueError("outs must be [..., 512]")
+    rows = shape[:-1]
+    for o, x in zip(outs, lses):
+        _dense("every part of outs", o, dtype, device, shape)
+        _dense("every part of lses", x, torch.float32, device, rows)
+    if out is not None:
+        _dense("out", out, dtype, device, shape)
+    if lse is not None:
+        _dense("lse", lse, torch.float32, device, rows)
 
-    def same(name, t, dt, sh):
-        check(name, t, dt, len(sh), dev) if len(sh) else None
-        if t.shape != sh or t.dtype != dt or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {tuple(sh)} {dt} on {dev}")
-
-    for i in range(len(outs)):
-        same(f"outs[{i}]", outs[i], dtype, shape)
-        same(f"lses[{i}]", lses[i], torch.float32, shape[:-1])
-    with _on(torch, dev, stream) as sp:
+    def call(raw):
+        nonlocal out, lse
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            same("out", out, dtype, shape)
+            out = torch.empty(shape, dtype=dtype, device=first.device)
         if lse is None:
-            lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-        else:
-            same("lse", lse, torch.float32, shape[:-1])
-        st = kvc_join([t.data_ptr() for t in outs], [t.data_ptr() for t in lses], lse.numel(),
-                      KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32,
-                      out.data_ptr(), lse.data_ptr(), sp)
+            lse = torch.empty(rows, dtype=torch.float32, device=first.device)
+        return kvc_join([t.data_ptr() for t in outs], [t.data_ptr() for t in lses], lse.numel(),
+                        KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32, out.data_ptr(),
+                        lse.data_ptr(), raw)
+
+    st = _run(call, device, stream)
     if st != KVC_OK:
         raise KvcError(st, "kvc_join")
     return out, lse
@@ -839,60 +869,58 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
     order (entries behind the new length are left as they were).  lengths_out,
     slot_weights_out and births_out may be the inputs themselves.
     """
-    torch, check = _operator_checks()
-    dev = _check_cache(check, torch, kv_cache, page_table, lengths)
-    R, keep, recent = lengths.shape[0], int(keep), int(recent)
+    torch = _torch or _load_torch()
+    device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
+    keep, recent = int(keep), int(recent)
     if keep < 0 or not 0 <= recent <= keep:
         raise ValueError("keep must be >= 0 and recent between 0 and keep")
-    check("slot_weights", slot_weights, torch.float32, 2, dev)
-    S = slot_weights.shape[1]
-    if slot_weights.shape[0] != R:
+    rows, S, weights_row = _rows("slot_weights", slot_weights, torch.float32, device)
+    if rows != R:
         raise ValueError("slot_weights must have one row per request")
+    births_row = weights_out_row = births_out_row = 0
     if births is not None:
-        check("births", births, torch.int32, 2, dev)
-        if births.shape != slot_weights.shape:
+        rows, cols, births_row = _rows("births", births, torch.int32, device)
+        if (rows, cols) != (R, S):
             raise ValueError("births must have the shape of slot_weights")
     elif recent > 0 or births_out is not None:
         raise ValueError("recent and births_out need births")
-    for name, t, dt in (("slot_weights_out", slot_weights_out, torch.float32),
-                        ("births_out", births_out, torch.int32)):
-        if t is not None:
-            check(name, t, dt, 2, dev)
-            if t.shape[0] != R or t.shape[1] < min(keep, S):
-                raise ValueError(f"{name} must be [num_reqs, at least min(keep, slots)]")
-    with _on(torch, dev, stream) as sp:
+    if slot_weights_out is not None:
+        rows, cols, weights_out_row = _rows("slot_weights_out", slot_weights_out, torch.float32, device)
+        if rows != R or cols < min(keep, S):
+            raise ValueError("slot_weights_out must be [num_reqs, at least min(keep, slots)]")
+    if births_out is not None:
+        rows, cols, births_out_row = _rows("births_out", births_out, torch.int32, device)
+        if rows != R or cols < min(keep, S):
+            raise ValueError("births_out must be [num_reqs, at least min(keep, slots)]")
+    if lengths_out is not None:
+        _dense("lengths_out", lengths_out, torch.int32, device, (R,))
+    if kept is not None:
+        _dense("kept", kept, torch.int32, device, (R, keep))
+    if workspace is not None:
+        _dense("workspace", workspace, torch.uint8, device, (workspace.numel(),))
+    if R != 0 and columns == 0:
+        raise ValueError("page_table must have at least one column")
+
+    def call(raw):
+        nonlocal lengths_out, kept, workspace
         if lengths_out is None:
-            lengths_out = torch.empty_like(lengths)
-        else:
-            check("lengths_out", lengths_out, torch.int32, 1, dev)
-            if lengths_out.shape[0] != R:
-                raise ValueError("lengths_out must have one entry per request")
+            lengths_out = torch.empty((R,), dtype=torch.int32, device=kv_cache.device)
         if kept is None:
-            kept = torch.empty((R, keep), dtype=torch.int32, device=dev)
-        else:
-            check("kept", kept, torch.int32, 2, dev)
-            if kept.shape != (R, keep) or not kept.is_contiguous():
-                raise ValueError("kept must be contiguous [num_reqs, keep]")
-        if R == 0 or page_table.shape[1] == 0:
-            if R != 0:
-                raise ValueError("page_table must have at least one column")
-            return lengths_out, kept
+            kept = torch.empty((R, keep), dtype=torch.int32, device=kv_cache.device)
+        if R == 0:
+            return KVC_OK
         if workspace is None:
-            workspace = torch.empty(kvc_evict_workspace_bytes(R, page_table.shape[1], keep),
-                                    dtype=torch.uint8, device=dev)
-        else:
-            check("workspace", workspace, torch.uint8, 1, dev)
-        st = kvc_evict(
-            kv_cache.data_ptr(), kv_cache.shape[0], page_table.data_ptr(), R, page_table.shape[1],
-            page_table.stride(0), lengths.data_ptr(), slot_weights.data_ptr(),
-            slot_weights.stride(0), S, None if births is None else births.data_ptr(),
-            0 if births is None else births.stride(0), keep, recent, lengths_out.data_ptr(),
-            kept.data_ptr() if keep else None,
-            None if slot_weights_out is None else slot_weights_out.data_ptr(),
-            0 if slot_weights_out is None else slot_weights_out.stride(0),
-            None if births_out is None else births_out.data_ptr(),
-            0 if births_out is None else births_out.stride(0), workspace.data_ptr(),
-            workspace.numel(), sp)
+            workspace = torch.empty(kvc_evict_workspace_bytes(R, columns, keep), dtype=torch.uint8,
+                                    device=kv_cache.device)
+        return kvc_evict(
+            kv_cache.data_ptr(), pages, page_table.data_ptr(), R, columns, row, lengths.data_ptr(),
+            slot_weights.data_ptr(), weights_row, S, None if births is None else births.data_ptr(),
+            births_row, keep, recent, lengths_out.data_ptr(), kept.data_ptr() if keep else None,
+            None if slot_weights_out is None else slot_weights_out.data_ptr(), weights_out_row,
+            None if births_out is None else births_out.data_ptr(), births_out_row,
+            workspace.data_ptr(), workspace.numel(), raw)
+
+    st = _run(call, device, stream)
     if st != KVC_OK:
         raise KvcError(st, "kvc_evict")
     return lengths_out, kept

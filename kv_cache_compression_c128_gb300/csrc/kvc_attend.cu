@@ -118,6 +118,15 @@ struct Barriers {
   unsigned long long piece_full[depth<N>()][ring_groups<N>()], piece_empty[depth<N>()][ring_groups<N>()], info_full[kInfos];
 };
 
+// What is left of a segment once its products are done: the rows of O, dims on
+// the lanes and heads on the columns, times `factor` to `out` if the segment is
+// the whole unit, as they are to its part otherwise.
+struct Rows {
+  int64_t row0;     // of out
+  int part, heads;  // heads 0: nothing
+  int whole;
+};
+
 template <int N>
 struct AttendShared {
   alignas(1024) uint8_t keys[2][kKeyStage];
@@ -129,12 +138,14 @@ struct AttendShared {
     float red[kSoftmaxWarps][N];
     int4 scan[kAttendThreads / 32];
   };
-  float ref[N], factor[N];
+  float ref[N];
+  alignas(8) float factor[N];
   Barriers<N> bar;
   PageInfo info[kInfos];
   uint8_t bad[8];  // of the last segments: a page was outside the cache
-  int total, start_req, start_off;
-  int start_pages;  // of the first unit
+  int total;
+  int start[4];  // request, length, unit and page of the share's first page
+  Rows rows;     // of the last segment
   uint32_t tmem;
   volatile int abort;
 };
@@ -299,15 +310,6 @@ struct Walk {
   int req, group, page, pages, length;
   int left;  // pages of the share from here on
 
-  __device__ void begin(const AttendParams& p, int r, int off, int count) {
-    req = r;
-    left = count;
-    if (count <= 0) return;
-    length = p.lengths[r];
-    pages = pages_of(p, length);
-    group = off / pages;
-    page = off % pages;
-  }
   __device__ int segment() const {
     return min(pages - page, left);
   }
@@ -684,6 +686,80 @@ __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count)
   wait_for(&s.bar.drain, 0, kDefaultWaitLimitCycles);
 }
 
+// Columns `from` .. `to` - 1 of the four chunks' 4 N, the lanes of a warp.
+template <int N>
+__device__ __forceinline__ void write_rows(const AttendParams& p, const AttendShared<N>& s, const Rows& rows, int from,
+                                           int to) {
+  constexpr int kWide = N == 16 ? 16 : 32;  // columns at a time
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const uint32_t tmem = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+  for (int at = from; at < to; at += kWide) {
+    const int b = at % N, d = at / N * 128 + warp * 32 + lane;
+    if (b >= rows.heads) continue;
+    uint32_t o[kWide];
+#pragma unroll
+    for (int j = 0; j < kWide; j += 16) tmem_ld_32x16(tmem + at + j, o + j);
+    tmem_wait_ld();
+    if (rows.whole) {
+      const bool odd = lane & 1;
+      uint16_t* const out = p.out + (rows.row0 + b + odd) * kHeadDim + (d & ~1);
+#pragma unroll
+      for (int j = 0; j < kWide; j += 2) {
+        // lanes 2 i and 2 i + 1 trade: one stores both dims of head j, the other of j + 1
+        const float2 f = *reinterpret_cast<const float2*>(&s.factor[b + j]);
+        const float a = __uint_as_float(o[j]) * f.x, e = __uint_as_float(o[j + 1]) * f.y;
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : e, 1);
+        const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, e) : __floats2bfloat162_rn(a, got);
+        if (b + j + odd < rows.heads) *reinterpret_cast<__nv_bfloat162*>(out + j * kHeadDim) = v;
+      }
+    } else {
+      float* const dst = p.parts + (static_cast<int64_t>(rows.part) * N + b) * kHeadDim + d;
+#pragma unroll
+      for (int j = 0; j < kWide; ++j)
+        if (b + j < rows.heads) dst[j * kHeadDim] = __uint_as_float(o[j]);
+    }
+  }
+}
+
+// Combines, over the eight lanes of equal lane % 4, kCount values a lane each:
+// halves of the values are traded instead of all of them, so that
+// kCount - 1 + ... shuffles do what 3 kCount would.  Lane l ends up with values
+// kCount / 8 * (l / 4 with its bits reversed) and on.
+template <int kCount, typename Op>
+__device__ __forceinline__ void combine_rows(float (&v)[kCount], int lane, Op op) {
+  int n = kCount;
+#pragma unroll
+  for (int d = 16; d >= 4; d >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & d;
+#pragma unroll
+      for (int j = 0; j < kCount / 2; ++j) {
+        if (j < n) {
+          const float send = up ? v[j] : v[j + n], keep = up ? v[j + n] : v[j];
+          v[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, d));
+        }
+      }
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], d));
+    }
+  }
+}
+
+// Stores what combine_rows left: value j of a thread belongs to column
+// 8 (j / 2) + 2 (lane % 4) + j % 2.
+template <int kCount>
+__device__ __forceinline__ void store_combined(const float (&v)[kCount], int lane, float* columns) {
+  constexpr int kLeft = kCount >= 8 ? kCount / 8 : 1;
+  int j0 = 0;
+  if (kCount >= 2) j0 += (lane & 16) ? kCount / 2 : 0;
+  if (kCount >= 4) j0 += (lane & 8) ? kCount / 4 : 0;
+  if (kCount >= 8) j0 += (lane & 4) ? kCount / 8 : 0;
+#pragma unroll
+  for (int k = 0; k < kLeft; ++k) columns[8 * ((j0 + k) >> 1) + 2 * (lane & 3) + ((j0 + k) & 1)] = v[k];
+}
+
 // Softmax warps.  Warp w has slots 16 w .. 16 w + 15 of a page: thread t the
 // slots t / 4 and t / 4 + 8 of them, and columns 2 (t % 4) + {0, 1} of each 8.
 template <int N>
@@ -745,14 +821,12 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
           return;
         }
         // the columns' maxima over the page
+        float m[kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          float m = fmaxf(__uint_as_float(v[4 * (j >> 1) + (j & 1)]) * c,
-                          __uint_as_float(v[4 * (j >> 1) + 2 + (j & 1)]) * c);
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-          if (lane < 4) s.red[warp][8 * (j >> 1) + 2 * lane + (j & 1)] = m;
-        }
+        for (int j = 0; j < kCols; ++j)
+          m[j] = fmaxf(__uint_as_float(v[4 * (j >> 1) + (j & 1)]) * c, __uint_as_float(v[4 * (j >> 1) + 2 + (j & 1)]) * c);
+        combine_rows(m, lane, [](float a, float b) { return fmaxf(a, b); });
+        store_combined(m, lane, s.red[warp]);
         softmax_sync();
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
@@ -805,13 +879,11 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       dev::mbar_arrive(&s.bar.p_full);
     }
     // the segment's end: columns' sums, then the rows of O
+    combine_rows(sum, lane, [](float a, float b) { return a + b; });
+    store_combined(sum, lane, s.red[warp]);
+    if (warp == 0 && lane < 4) {
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], d);
-      const int col = 8 * (j >> 1) + 2 * lane + (j & 1);
-      if (lane < 4) s.red[warp][col] = sum[j];
-      if (warp == 0 && lane < 4) s.ref[col] = ref[j];
+      for (int j = 0; j < kCols; ++j) s.ref[8 * (j >> 1) + 2 * lane + (j & 1)] = ref[j];
     }
     softmax_sync();
     const bool whole = n == w.pages, bad = s.bad[segment & 7] != 0;
@@ -858,37 +930,12 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
     }
     if (t == 0) s.bad[segment & 7] = 0;
     tc_fence_after();
-    if (!whole || !bad) {
-#pragma unroll 1
-      for (int chunk = 0; chunk < 4; ++chunk) {
-        const int d = chunk * 128 + warp * 32 + lane;
-#pragma unroll 1
-        for (int b = 0; b < heads; b += 16) {
-          uint32_t o[16];
-          tmem_ld_32x16(tmem + chunk * N + b, o);
-          tmem_wait_ld();
-          if (whole) {
-            uint16_t* const out = p.out + (row0 + b) * kHeadDim;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              // lanes 2 i and 2 i + 1 trade: one stores both dims of head j, the other of j + 1
-              const float a = __uint_as_float(o[j]) * s.factor[b + j];
-              const float e = __uint_as_float(o[j + 1]) * s.factor[b + j + 1];
-              const bool odd = lane & 1;
-              const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : e, 1);
-              const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, e) : __floats2bfloat162_rn(a, got);
-              if (b + j + odd < heads)
-                *reinterpret_cast<__nv_bfloat162*>(out + (j + odd) * kHeadDim + (d & ~1)) = v;
-            }
-          } else {
-            float* const dst = p.parts + (static_cast<int64_t>(part) * N + b) * kHeadDim + d;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (b + j < heads) dst[j * kHeadDim] = __uint_as_float(o[j]);
-          }
-        }
-      }
+    const Rows rows{row0, part, whole && bad ? 0 : heads, whole};
+    if (w.left == n) {  // of the last segment the whole CTA writes the rows
+      if (t == 0) s.rows = rows;
+      return;
     }
+    write_rows<N>(p, s, rows, 0, 4 * N);
     tc_fence_before();
     softmax_sync();  // s.red, s.factor and O are free again
     at += n;
@@ -925,10 +972,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // pages before each thread's run of requests
-  const int run = static_cast<int>((p.num_reqs + kAttendThreads - 1) / kAttendThreads);
-  const int lo = min(static_cast<int>(p.num_reqs), t * run), hi = min(static_cast<int>(p.num_reqs), lo + run);
-  // the pages (the host has checked that all fit 31 bits) and the units
+  // Where the share lies: the pages (the host has checked that all fit 31 bits)
+  // and the units before each thread's run of requests.  Up to 32 requests
+  // every warp finds it for itself, a request a lane.
+  const int reqs = static_cast<int>(p.num_reqs);
+  const bool few = reqs <= 32;
+  const int run = few ? 1 : (reqs + kAttendThreads - 1) / kAttendThreads;
+  const int lo = min(reqs, (few ? lane : t) * run), hi = min(reqs, lo + run);
   int mine = 0, mine_units = 0, longest = 0;
   bool bad_length = false;
 #pragma unroll 1
@@ -941,25 +991,28 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     bad_length = bad_length || length < 0 || length > p.max_slots;
   }
   if (bad_length && cta == 0) atomicCAS(p.error, 0u, kErrBadIndex);
-  int inc = mine, inc_units = mine_units;
+  int before = mine, before_units = mine_units;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d), u = __shfl_up_sync(0xFFFFFFFFu, inc_units, d);
-    if (lane >= d) inc += o, inc_units += u;
+    const int o = __shfl_up_sync(0xFFFFFFFFu, before, d), u = __shfl_up_sync(0xFFFFFFFFu, before_units, d);
+    if (lane >= d) before += o, before_units += u;
   }
   longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-  if (lane == 31) s.scan[warp] = make_int4(inc, inc_units, longest, 0);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int before = inc - mine, before_units = inc_units - mine_units, total = 0, units = 0;
+  int total = __shfl_sync(0xFFFFFFFFu, before, 31), units = __shfl_sync(0xFFFFFFFFu, before_units, 31);
+  before -= mine;
+  before_units -= mine_units;
+  if (!few) {
+    if (lane == 0) s.scan[warp] = make_int4(total, units, longest, 0);
+    __syncthreads();
+    total = units = 0;
 #pragma unroll 1
-  for (int i = 0; i < kAttendThreads / 32; ++i) {
-    const int4 of = s.scan[i];
-    if (i < warp) before += of.x, before_units += of.y;
-    total += of.x;
-    units += of.y;
-    longest = max(longest, of.z);
+    for (int i = 0; i < kAttendThreads / 32; ++i) {
+      const int4 of = s.scan[i];
+      if (i < warp) before += of.x, before_units += of.y;
+      total += of.x;
+      units += of.y;
+      longest = max(longest, of.z);
+    }
   }
   total *= p.groups;
   units *= p.groups;
@@ -973,30 +1026,39 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     start = by_unit ? cta : share_start(total, cta, ctas);
     count = by_unit ? 1 : share_start(total, cta + 1, ctas) - start;
   }
-  if (t == 0) {
-    s.total = total;
-    p.joins[cta] = make_int4(-1, 0, 0, 0);
-  }
   const int first = by_unit ? before_units : before, here = by_unit ? mine_units : mine;
-  if (count > 0 && start >= first * p.groups && start < (first + here) * p.groups) {
+  if (count > 0 && start >= first * p.groups && start < (first + here) * p.groups && (!few || warp == 0)) {
     int off = start - first * p.groups, r = lo;
 #pragma unroll 1
     for (;; ++r) {
-      const int pages = pages_of(p, p.lengths[r]), size = (by_unit ? pages > 0 : pages) * p.groups;
+      const int length = p.lengths[r], pages = pages_of(p, length), size = (by_unit ? pages > 0 : pages) * p.groups;
       if (off < size) {
-        s.start_req = r;
-        s.start_off = by_unit ? off * pages : off;
-        s.start_pages = pages;
+        s.start[0] = r;
+        s.start[1] = length;
+        s.start[2] = by_unit ? off : off / pages;
+        s.start[3] = by_unit ? 0 : off % pages;
         break;
       }
       off -= size;
     }
   }
+  if (t == 0) {
+    s.total = total;
+    s.rows.heads = 0;
+    p.joins[cta] = make_int4(-1, 0, 0, 0);
+  }
+  tc_fence_before();
   __syncthreads();
-  if (by_unit && count > 0) count = s.start_pages;
+  tc_fence_after();
   if (count > 0) {
     Walk w;
-    w.begin(p, s.start_req, s.start_off, count);
+    w.req = s.start[0];
+    w.length = s.start[1];
+    w.group = s.start[2];
+    w.page = s.start[3];
+    w.pages = pages_of(p, w.length);
+    if (by_unit) count = w.pages;
+    w.left = count;
     if (warp < kSoftmaxWarps) {
       more_registers<kSoftmaxRegs>();
       softmax_role<N>(p, s, w, cta, ctas);
@@ -1020,9 +1082,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (t == 0) {
-    if (s.abort) atomicCAS(p.error, 0u, kErrTimeout);
+  if (s.rows.heads > 0) write_rows<N>(p, s, s.rows, (warp >> 2) * N, (warp >> 2) * N + N);
+  if (t == 0 && s.abort) {
+    atomicCAS(p.error, 0u, kErrTimeout);
+    p.joins[cta] = make_int4(-2, 0, 0, 0);
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (warp == kIssueWarp) tmem_free(s.tmem, tmem_columns<N>());
 }
 
@@ -1127,6 +1194,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   // the divided units, in order
   const int4 mine = t < ctas ? p.joins[t] : make_int4(-1, 0, 0, 0);
+  // what a CTA that gave up has not written is not read
+  if (__syncthreads_or(mine.x == -2)) return;
   const uint32_t there = __ballot_sync(0xFFFFFFFFu, mine.x >= 0);
   if (lane == 0) warp_joins[warp] = __popc(there);
   __syncthreads();
