@@ -32,7 +32,9 @@ __device__ __forceinline__ void unpack(uint4 v, float* f) {
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kJoinWarps * 32) kvc_join_kernel(JoinParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kvc_join_kernel(const __grid_constant__ JoinParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // 16-byte pieces of a row: 64 (bf16) or 128 (fp32); lane, lane + 32, ...
   constexpr int kPieces = kBf16 ? 2 : 4, kDims = kBf16 ? 8 : 4;
   const int lane = threadIdx.x & 31;
@@ -94,12 +96,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_join_kernel(JoinParams p)
 }  // namespace
 
 cudaError_t launch_join(const JoinParams& p, cudaStream_t stream) {
-  const int64_t ctas = (p.num_rows + kJoinWarps - 1) / kJoinWarps;
-  if (p.bf16)
-    kvc_join_kernel<true><<<static_cast<unsigned>(ctas), kJoinWarps * 32, 0, stream>>>(p);
-  else
-    kvc_join_kernel<false><<<static_cast<unsigned>(ctas), kJoinWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.num_rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.bf16 ? cudaLaunchKernelEx(&cfg, kvc_join_kernel<true>, p) : cudaLaunchKernelEx(&cfg, kvc_join_kernel<false>, p);
 }
 
 }  // namespace kvc

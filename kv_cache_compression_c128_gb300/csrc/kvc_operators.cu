@@ -246,7 +246,7 @@ kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* pag
   p.births_out = births_out;
   p.births_out_row_stride = births_out_row_stride;
   p.counts = static_cast<int32_t*>(workspace);
-  p.moves = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) +
+  p.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) +
                                        round16(sizeof(int32_t) * num_reqs));
   p.move_stride = behind < keep ? behind : keep;
   const cudaError_t e = kvc::launch_evict(p, static_cast<cudaStream_t>(stream));
