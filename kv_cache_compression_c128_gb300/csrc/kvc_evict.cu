@@ -13,8 +13,8 @@
 //
 // One CTA per request selects and writes the small arrays and the list of
 // moves; a grid of warps then moves the slots, 584 bytes read and written each.
-// Up to 8192 slots a request the CTA keeps 32-bit keys in registers, a run of
-// neighbours a thread, and finds the keep-th largest two bits at a time by
+// Up to 8192 slots a request the CTA keeps 32-bit keys in registers, 8 a
+// thread, and finds the keep-th largest two bits at a time by
 // counting: 16 rounds of one barrier each, whatever the weights are (a histogram
 // of digits took 24.7 us with its scans and its second pass over the keys on
 // 64 x 8192, this TIME_SELECT).  Longer requests go by digits, with the keys in
@@ -38,7 +38,7 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kDigitBits = 11;  // 32-bit keys in digits of 11, 11 and 10 bits
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kCachedKeys = 40960;  // keys held in shared memory (160 KiB); the rest are formed anew
-constexpr int kMoveWarps = 8;
+constexpr int kMoveWarps = 8, kMoveCtasPerSm = 3;
 constexpr int kPerThread = 8;
 constexpr int kShortSlots = kSelectThreads * kPerThread;  // 8192
 constexpr int kFewMoves = 64;
@@ -73,6 +73,12 @@ __device__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sums) {
   }
   __syncthreads();
   return warp_sums[warp] + inc - v;
+}
+
+// A move as the list holds it: the slots' numbers in the cache, page * 64 + place.
+__device__ __forceinline__ longlong2 move_of(const int32_t* table, int to, int of) {
+  return make_longlong2(static_cast<long long>(table[to / kSlotsPerPage]) * kSlotsPerPage + to % kSlotsPerPage,
+                        static_cast<long long>(table[of / kSlotsPerPage]) * kSlotsPerPage + of % kSlotsPerPage);
 }
 
 struct SelectShared {
@@ -119,7 +125,7 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_long_kernel(const __
       p.weights_out == nullptr ? nullptr : p.weights_out + r * p.weights_out_row_stride;
   int32_t* const births_out =
       p.births_out == nullptr ? nullptr : p.births_out + r * p.births_out_row_stride;
-  int2* const list = p.moves + r * p.move_stride;  // to, of
+  longlong2* const list = p.moves + r * p.move_stride;  // places first, then the slots' numbers
 
   uint32_t threshold = 0;  // keys above it are kept
   uint32_t equal_left = 0;  // and this many of those equal to it, from the lowest index
@@ -224,7 +230,8 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_long_kernel(const __
   __syncthreads();
   const int moves = static_cast<int>(s.left);
   for (int i = t; i < moves; i += kSelectThreads) {
-    const int to = list[i].x, of = list[i].y;
+    const int to = static_cast<int>(list[i].x), of = static_cast<int>(list[i].y);
+    list[i] = move_of(table, to, of);
     if (kept != nullptr) kept[to] = of;
     if (weights_out != nullptr) weights_out[to] = weights[of];
     if (births_out != nullptr) births_out[to] = births[of];
@@ -238,47 +245,57 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_long_kernel(const __
 }
 
 // Eight moves by one warp: 8 x 36 pieces of 16 bytes are 9 a lane, and lanes
-// 0..7 have a scale record each.  Lane l < 8 holds move l's addresses.
-__device__ __forceinline__ void move_eight(uint8_t* kv, const int32_t* table, const int2* moves, int count) {
+// 0..7 have a move and its scale record each.
+__device__ __forceinline__ void move_eight(uint8_t* kv, longlong2 m, int count) {
   const int lane = threadIdx.x & 31;
-  uint8_t *dst = nullptr, *src = nullptr;
+  uint64_t dst = 0, src = 0;
   uint2 scale = make_uint2(0, 0);
   uint8_t* scale_to = nullptr;
   if (lane < count) {
-    const int2 m = moves[lane];  // to, of
-    uint8_t* const to = kv + table[m.x / kSlotsPerPage] * kPageBytes;
-    uint8_t* const of = kv + table[m.y / kSlotsPerPage] * kPageBytes;
-    dst = to + (m.x % kSlotsPerPage) * kTokenStride;
-    src = of + (m.y % kSlotsPerPage) * kTokenStride;
-    scale_to = to + kScaleBase + (m.x % kSlotsPerPage) * kScaleDim;
-    scale = *reinterpret_cast<const uint2*>(of + kScaleBase + (m.y % kSlotsPerPage) * kScaleDim);
+    uint8_t* const to = kv + m.x / kSlotsPerPage * kPageBytes;
+    const uint8_t* const of = kv + m.y / kSlotsPerPage * kPageBytes;
+    const int p = static_cast<int>(m.x % kSlotsPerPage), q = static_cast<int>(m.y % kSlotsPerPage);
+    dst = reinterpret_cast<uint64_t>(to + p * kTokenStride);
+    src = reinterpret_cast<uint64_t>(of + q * kTokenStride);
+    scale_to = to + kScaleBase + p * kScaleDim;
+    scale = *reinterpret_cast<const uint2*>(of + kScaleBase + q * kScaleDim);
   }
   uint4 v[9];
 #pragma unroll
   for (int k = 0; k < 9; ++k) {
-    const int slot = (32 * k + lane) / 36, piece = (32 * k + lane) % 36;
-    const uint64_t from = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), slot);
+    const int slot = (32 * k + lane) / 36, piece = (32 * k + lane) - 36 * slot;
+    const uint64_t from = __shfl_sync(0xFFFFFFFFu, src, slot);
     if (slot < count) v[k] = *reinterpret_cast<const uint4*>(from + 16 * piece);
   }
 #pragma unroll
   for (int k = 0; k < 9; ++k) {
-    const int slot = (32 * k + lane) / 36, piece = (32 * k + lane) % 36;
-    const uint64_t to = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(dst), slot);
+    const int slot = (32 * k + lane) / 36, piece = (32 * k + lane) - 36 * slot;
+    const uint64_t to = __shfl_sync(0xFFFFFFFFu, dst, slot);
     if (slot < count) *reinterpret_cast<uint4*>(to + 16 * piece) = v[k];
   }
   if (lane < count) *reinterpret_cast<uint2*>(scale_to) = scale;
 }
 
-// The moves of a request by the warps of grid.y CTAs.
-__global__ void __launch_bounds__(kMoveWarps * 32) kvc_evict_move_kernel(const __grid_constant__ EvictParams p) {
+// The moves of a request by the warps of grid.y CTAs, which are all resident:
+// a warp asks for its next moves before it makes the present ones.
+__global__ void __launch_bounds__(kMoveWarps * 32, kMoveCtasPerSm) kvc_evict_move_kernel(
+    const __grid_constant__ EvictParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t r = blockIdx.x;
+  const int lane = threadIdx.x & 31, step = 8 * gridDim.y * kMoveWarps;
+  const longlong2* const list = p.moves + r * p.move_stride;
   const int moves = p.counts[r];
-  const int32_t* const table = p.page_table + r * p.page_table_row_stride;
-  const int2* const list = p.moves + r * p.move_stride;
-  for (int i = 8 * (blockIdx.y * kMoveWarps + (threadIdx.x >> 5)); i < moves; i += 8 * gridDim.y * kMoveWarps)
-    move_eight(p.kv_cache, table, list + i, min(8, moves - i));
+  int i = 8 * (blockIdx.y * kMoveWarps + (threadIdx.x >> 5));
+  longlong2 m = make_longlong2(0, 0);
+  if (lane < 8 && i + lane < moves) m = list[i + lane];
+#pragma unroll 1
+  for (; i < moves; i += step) {
+    longlong2 next = make_longlong2(0, 0);
+    if (lane < 8 && i + step + lane < moves) next = list[i + step + lane];
+    move_eight(p.kv_cache, m, min(8, moves - i));
+    m = next;
+  }
 }
 
 // ---- up to kShortSlots slots a request --------------------------------------------
@@ -286,9 +303,38 @@ __global__ void __launch_bounds__(kMoveWarps * 32) kvc_evict_move_kernel(const _
 struct ShortShared {
   int holes[kShortSlots / 2], movers[kShortSlots / 2];  // as many as can be: of L slots, min(keep, L - keep)
   uint32_t counts[2][kSelectWarps];
-  uint32_t warp_sums[kSelectWarps];
+  uint32_t ranks[kPerThread][kSelectWarps], rows[kPerThread];
   int newest[kSelectWarps];
 };
+
+// Thread t has slots 1024 j + t, j < 8.  From two truth values of each, the
+// ranks in slot order of those that are true: `first` in the high halves,
+// `second` in the low ones (8192 at most).  Returns both totals; all call.
+__device__ uint32_t rank_slots(const bool* first, const bool* second, uint32_t* rank, ShortShared& s) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const uint32_t below = (1u << lane) - 1;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const uint32_t a = __ballot_sync(0xFFFFFFFFu, first[j]), b = __ballot_sync(0xFFFFFFFFu, second[j]);
+    rank[j] = static_cast<uint32_t>(__popc(a & below)) << 16 | __popc(b & below);
+    if (lane == 0) s.ranks[j][warp] = static_cast<uint32_t>(__popc(a)) << 16 | __popc(b);
+  }
+  __syncthreads();
+  if (warp < kPerThread) {
+    const uint32_t v = s.ranks[warp][lane], inc = warp_inclusive(v, lane);
+    s.ranks[warp][lane] = inc - v;
+    if (lane == 31) s.rows[warp] = inc;
+  }
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    rank[j] += total + s.ranks[j][warp];
+    total += s.rows[j];
+  }
+  return total;
+}
 
 template <bool kMoves>
 __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const __grid_constant__ EvictParams p) {
@@ -304,15 +350,15 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const _
   const int32_t* const births = p.births == nullptr ? nullptr : p.births + r * p.births_row_stride;
   const bool fits = length >= 0 && length <= p.max_slots;
   const int L = fits ? static_cast<int>(length) : 0, keep = static_cast<int>(p.keep < L ? p.keep : L);
-  const int width = (L + kSelectThreads - 1) / kSelectThreads, lo = t * width;  // slots lo .. lo + width - 1
+  const int width = (L + kSelectThreads - 1) / kSelectThreads;  // slots of a thread: 1024 j + t
   // every load that the selection needs, at once
   float w[kPerThread];
   int born[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const bool in = j < width && lo + j < L;
-    w[j] = in ? weights[lo + j] : 0.f;
-    born[j] = in && births != nullptr ? births[lo + j] : INT32_MIN;
+    const int n = kSelectThreads * j + t;
+    w[j] = n < L ? weights[n] : 0.f;
+    born[j] = n < L && births != nullptr ? births[n] : INT32_MIN;
   }
   bool ok = fits;
   if (t * kSlotsPerPage < L) ok = static_cast<uint32_t>(table[t]) < p.num_pages;  // 128 pages at most
@@ -335,20 +381,20 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const _
   const long long protect_above =
       p.recent > 0 ? static_cast<long long>(__reduce_max_sync(0xFFFFFFFFu, s.newest[lane])) - p.recent : INT64_MAX;
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
-    const bool in = j < width && lo + j < L;
-    key[j] = !in ? 0u : born[j] > protect_above ? 0xFFFFFFFFu : order_key(w[j]);
-  }
-  // the keep-th largest key: the largest x with at least `keep` keys >= x
+  for (int j = 0; j < kPerThread; ++j)
+    key[j] = kSelectThreads * j + t >= L ? 0u : born[j] > protect_above ? 0xFFFFFFFFu : order_key(w[j]);
+  // the keep-th largest key: the largest x with at least `keep` keys >= x, or
+  // any x that exactly `keep` keys reach
   uint32_t threshold = 0;
   if (keep > 0 && keep < L) {
 #pragma unroll 1
-    for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
+    for (int shift = 30, turn = 0, found = 0; shift >= 0 && !found; shift -= 2, turn ^= 1) {
       const uint32_t x1 = threshold | 1u << shift, x2 = threshold | 2u << shift, x3 = threshold | 3u << shift;
       uint32_t mine = 0;  // how many reach x1, x2, x3, in 10 bits each: 256 of a warp at most
 #pragma unroll
       for (int j = 0; j < kPerThread; ++j)
-        mine += (key[j] >= x1 ? 1u : 0u) + (key[j] >= x2 ? 1u << 10 : 0u) + (key[j] >= x3 ? 1u << 20 : 0u);
+        if (j < width)
+          mine += (key[j] >= x1 ? 1u : 0u) + (key[j] >= x2 ? 1u << 10 : 0u) + (key[j] >= x3 ? 1u << 20 : 0u);
       mine = __reduce_add_sync(0xFFFFFFFFu, mine);
       if (lane == 0) s.counts[turn][warp] = mine;
       __syncthreads();
@@ -357,61 +403,48 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const _
       const uint32_t n2 = __reduce_add_sync(0xFFFFFFFFu, all >> 10 & 1023u);
       const uint32_t n3 = __reduce_add_sync(0xFFFFFFFFu, all >> 20);
       threshold = n3 >= keep ? x3 : n2 >= keep ? x2 : n1 >= keep ? x1 : threshold;
+      found = n1 == keep || n2 == keep || n3 == keep;
     }
   }
   // of the keys equal to it, as many as are left to keep, from the lowest index
-  uint32_t above = 0, equal = 0;
+  bool stay[kPerThread], other[kPerThread];
+  uint32_t rank[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const bool in = j < width && lo + j < L;
-    above += in && key[j] > threshold;
-    equal += in && key[j] == threshold;
+    const bool in = kSelectThreads * j + t < L;
+    stay[j] = in && (keep == L || (keep > 0 && key[j] > threshold));
+    other[j] = in && keep > 0 && keep < L && key[j] == threshold;
   }
-  uint32_t stays = 0;  // by bit, of this thread's slots
-  if (keep == L) {
-    stays = 0xFFu;
-  } else if (keep > 0) {
-    // 8192 slots at most: two sums of 16 bits in one scan
-    const uint32_t before = block_exclusive(above << 16 | equal, s.warp_sums);
-    if (t == kSelectThreads - 1) s.counts[0][0] = (before >> 16) + above;
-    __syncthreads();
-    const uint32_t spare = keep - s.counts[0][0];
-    uint32_t rank = before & 0xFFFFu;
+  if (keep < L) {
+    const uint32_t spare = keep - (rank_slots(stay, other, rank, s) >> 16);
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      if (key[j] > threshold || (key[j] == threshold && rank < spare)) stays |= 1u << j;
-      rank += key[j] == threshold;
-    }
+    for (int j = 0; j < kPerThread; ++j) stay[j] = stay[j] || (other[j] && (rank[j] & 0xFFFFu) < spare);
   }
-  uint32_t n_holes = 0, n_movers = 0;
+  bool hole[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const int n = lo + j;
-    const bool in = j < width && n < L, stay = in && (stays >> j & 1u);
-    n_holes += in && !stay && n < keep;
-    n_movers += stay && n >= keep;
+    const int n = kSelectThreads * j + t;
+    hole[j] = n < keep && !stay[j];
+    other[j] = n >= keep && stay[j];  // moves
   }
-  const uint32_t before = block_exclusive(n_holes << 16 | n_movers, s.warp_sums);
-  int h = before >> 16, m = before & 0xFFFFu;
-  if (t == kSelectThreads - 1) s.counts[1][0] = m + n_movers;
+  const int moves = keep == L ? 0 : rank_slots(hole, other, rank, s) & 0xFFFFu;
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const int n = lo + j;
-    const bool in = j < width && n < L, stay = in && (stays >> j & 1u);
-    if (in && !stay && n < keep) s.holes[h++] = n;
-    if (stay && n >= keep) s.movers[m++] = n;
-    if (stay && n < keep) {
+    const int n = kSelectThreads * j + t;
+    if (hole[j]) s.holes[rank[j] >> 16] = n;
+    if (other[j]) s.movers[rank[j] & 0xFFFFu] = n;
+    if (n < keep && stay[j]) {
       if (kept != nullptr) kept[n] = n;
       if (weights_out != nullptr) weights_out[n] = w[j];
       if (births_out != nullptr) births_out[n] = born[j];
     }
   }
   __syncthreads();
-  const int moves = static_cast<int>(s.counts[1][0]);
-  int2* const list = p.moves + r * p.move_stride;
+  longlong2* const list = p.moves + r * p.move_stride;
   for (int i = t; i < moves; i += kSelectThreads) {
     const int to = s.holes[i], of = s.movers[i];
-    list[i] = make_int2(to, of);
+    const longlong2 move = move_of(table, to, of);
+    list[i] = move;
     if (kept != nullptr) kept[to] = of;
     // (an array written in place: sources lie at and behind the new length)
     if (weights_out != nullptr) weights_out[to] = weights[of];
@@ -424,8 +457,11 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const _
     p.lengths_out[r] = keep;
   }
   if constexpr (kMoves) {
-    __syncthreads();
-    for (int i = 8 * warp; i < moves; i += 8 * kSelectWarps) move_eight(p.kv_cache, table, list + i, min(8, moves - i));
+    if (moves == 0) return;
+    for (int i = 8 * warp; i < moves; i += 8 * kSelectWarps) {
+      const int of_list = min(i + (lane & 7), moves - 1);
+      move_eight(p.kv_cache, move_of(table, s.holes[of_list], s.movers[of_list]), min(8, moves - i));
+    }
   }
 }
 
@@ -468,10 +504,10 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     e = launch(kvc_evict_short_kernel<false>, reqs, kSelectThreads, sizeof(ShortShared), p, stream);
   }
   if (e != cudaSuccess || p.move_stride == 0) return e;
-  // a round of 8 moves for each warp if all the moves there can be are made,
-  // unless that is more than fits the card several times
+  // as many CTAs as fit at once, shared out evenly over the requests, and no
+  // more than all the moves there can be need
   const int64_t wide = (p.move_stride + 8 * kMoveWarps - 1) / (8 * kMoveWarps);
-  const int64_t most = 2432 / p.num_reqs > 0 ? 2432 / p.num_reqs : 1;
+  const int64_t share = kMoveCtasPerSm * 152 / p.num_reqs, most = share > 0 ? share : 1;
   return launch(kvc_evict_move_kernel, dim3(reqs.x, static_cast<unsigned>(wide < most ? wide : most)),
                 kMoveWarps * 32, 0, p, stream);
 }

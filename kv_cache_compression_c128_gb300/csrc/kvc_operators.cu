@@ -192,7 +192,7 @@ size_t kvc_evict_workspace_bytes(int64_t num_reqs, int64_t max_pages_per_req, in
   const int64_t slots = max_pages_per_req * kvc::kSlotsPerPage;
   const int64_t behind = slots > keep ? slots - keep : 0;
   const int64_t stride = behind < keep ? behind : keep;
-  return round16(sizeof(int32_t) * num_reqs) + round16(sizeof(int32_t) * 2 * num_reqs * stride) + 16;
+  return round16(sizeof(int32_t) * num_reqs) + sizeof(longlong2) * num_reqs * stride + 16;
 }
 
 kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* page_table,
@@ -246,7 +246,7 @@ kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* pag
   p.births_out = births_out;
   p.births_out_row_stride = births_out_row_stride;
   p.counts = static_cast<int32_t*>(workspace);
-  p.moves = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) +
+  p.moves = reinterpret_cast<longlong2*>(static_cast<uint8_t*>(workspace) +
                                        round16(sizeof(int32_t) * num_reqs));
   p.move_stride = behind < keep ? behind : keep;
   const cudaError_t e = kvc::launch_evict(p, static_cast<cudaStream_t>(stream));

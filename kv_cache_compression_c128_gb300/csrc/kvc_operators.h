@@ -87,7 +87,7 @@ struct EvictParams {
   int32_t* births_out;
   int64_t births_out_row_stride;
   int32_t* counts;  // workspace: moves of each request
-  int2* moves;      // workspace: per request, move_stride places (to, of)
+  longlong2* moves; // workspace: per request, move_stride slots of the cache (to, of)
   int64_t move_stride;
   uint32_t* error;
 };
