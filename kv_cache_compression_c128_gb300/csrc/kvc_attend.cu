@@ -74,10 +74,9 @@ constexpr int kKeyStage = 8 * kKeyBlock;                // a decoded page
 constexpr int kGroups = 7;                              // of 64 codes with one scale
 constexpr int kPieceBytes = kSlotsPerPage * kGroup;     // a page's codes of one group
 constexpr int kScaleBytes = kSlotsPerPage * kScaleDim;
-// Pages described at a time.  The products of page i wait for its RoPE words,
-// the decode of page i + 2 then for theirs, and the copies run less than two
-// pages ahead of the decode: a page's place is taken again by page i + 5 at the
-// earliest.
+// Pages described at a time.  While the RoPE words of page j are not there, its
+// products are not issued, the decode is at page j + 2 at most, and the copies
+// at page j + 3 + depth(): a page's place here is taken again eight pages later.
 constexpr int kInfos = 8;
 // Pages by which the longest unit may exceed an equal share before units are
 // divided: joining the parts costs about as much as this many pages.
@@ -94,8 +93,8 @@ constexpr int kWeightSlots = 64;                        // slots at least for a 
 template <int N>
 __host__ __device__ constexpr int ring_groups() { return N == 64 ? 6 : 7; }
 // Pages that the ring holds, and pages whose scales are kept for its groups:
-// the copy of page i's scales waits for the place of its first piece, so that
-// all pieces of page i - 1 - depth() are read, and their scales before them.
+// page i's are asked for when all pieces of page i - 1 - depth() are read, and
+// their scales before them.
 template <int N>
 __host__ __device__ constexpr int depth() { return N == 64 ? 1 : 2; }
 template <int N>
@@ -404,12 +403,15 @@ __device__ __forceinline__ int heads_of(const AttendParams& p, int group) {
   return min(p.group_heads, p.num_heads - group * p.group_heads);
 }
 
-// Copies the codes and scales of every page of the share.
+// Copies the codes and scales of every page of the share: lane g the codes of
+// group g, lane 31 the scales.  (One lane after the other's wait, announcement
+// and copy took some 500 cycles a piece, 3500 a page, and held up all the rest.)
 template <int N>
 __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
   constexpr int kDepth = depth<N>(), kScales = scale_slots<N>(), kRing = ring_groups<N>();
   const int lane = threadIdx.x & 31;
-  int i = 0, g = 0;  // pages begun; of the last one, the pieces asked for (lane 0)
+  int i = 0;       // pages begun
+  int asked = 0;   // of this lane's pieces, or pages' scales
   bool ok = true;
 #pragma unroll 1
   for (int segment = 0; ok && w.left > 0; ++segment) {
@@ -417,52 +419,45 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
     const int32_t* table = p.page_table + w.req * p.page_table_row_stride + w.page;
     int ids = 0;  // of 32 pages, one a lane
 #pragma unroll 1
-    for (int pg = 0; ok && pg < count; ++pg) {
+    for (int pg = 0; ok && pg < count; ++pg, ++i) {
       if ((pg & 31) == 0) ids = pg + lane < count ? __ldg(table + pg + lane) : 0;
-      const int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
+      int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
       const bool there = static_cast<uint32_t>(id) < p.num_pages;
-      const int place = i % kDepth, turn = i / kDepth;
-      if (lane == 0) {
+      if (!there) id = 0;
+      if (lane == 31) {
         if (!there) {
           s.bad[segment & 7] = 1;
           atomicCAS(p.error, 0u, kErrBadIndex);
         }
         const int valid = there ? min(kSlotsPerPage, w.length - (w.page + pg) * kSlotsPerPage) : 0;
-        const PageInfo info{there ? id : 0, static_cast<int16_t>(valid), static_cast<int16_t>(pg + 1 == count)};
-#pragma unroll 1
-        for (g = 0; g < kRing; ++g) {
-          if (turn > 0 && !wait_for(&s.bar.piece_empty[place][g], (turn - 1) & 1, p.wait_limit)) {
-            ok = false;
-            break;
-          }
-          if (g == 0) {
-            s.info[i % kInfos] = info;
-            dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], kScaleBytes);
-            copy_bytes(s.scales[i % kScales], p.kv_cache + info.id * kPageBytes + kScaleBase, kScaleBytes,
-                       &s.bar.info_full[i % kInfos]);
-          }
-          dev::mbar_arrive_expect_tx(&s.bar.piece_full[place][g], kPieceBytes);
-          copy_box(s.codes[place][g], &p.code_map, g * kGroup, 0, info.id, &s.bar.piece_full[place][g]);
-        }
-        ok = ok && !s.abort;
+        s.info[i % kInfos] = PageInfo{id, static_cast<int16_t>(valid), static_cast<int16_t>(pg + 1 == count)};
+        dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], kScaleBytes);
+        copy_bytes(s.scales[i % kScales], p.kv_cache + id * kPageBytes + kScaleBase, kScaleBytes,
+                   &s.bar.info_full[i % kInfos]);
+        ++asked;
       }
-      ++i;
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      const int place = i % kDepth, turn = i / kDepth;
+      if (lane < kRing) {
+        ok = turn == 0 || wait_for(&s.bar.piece_empty[place][lane], (turn - 1) & 1, p.wait_limit);
+        if (ok) {
+          dev::mbar_arrive_expect_tx(&s.bar.piece_full[place][lane], kPieceBytes);
+          copy_box(s.codes[place][lane], &p.code_map, lane * kGroup, 0, id, &s.bar.piece_full[place][lane]);
+          ++asked;
+        }
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok && !s.abort);
     }
     w.advance(p, count);
   }
   if (!ok) s.abort = 1;
-  if (lane == 0) {  // no copy may land in memory that the CTA has given back
-    const int whole = i > 0 && g < kRing ? i - 1 : i;  // pages asked for in full; g pieces of page `whole` besides
+  // no copy may land in memory that the CTA has given back
+  if (lane < kRing) {
 #pragma unroll 1
-    for (int k = 0; k < kDepth * kRing; ++k) {
-      const int place = k / kRing, piece = k % kRing;
-      const int times = (whole + kDepth - 1 - place) / kDepth + (whole < i && whole % kDepth == place && piece < g);
-      if (times > 0) wait_for(&s.bar.piece_full[place][piece], (times - 1) & 1, kDefaultWaitLimitCycles);
-    }
-    const int infos = whole + (whole < i && g > 0);
+    for (int j = max(0, asked - kDepth); j < asked; ++j)
+      wait_for(&s.bar.piece_full[j % kDepth][lane], (j / kDepth) & 1, kDefaultWaitLimitCycles);
+  } else if (lane == 31) {
 #pragma unroll 1
-    for (int j = max(0, infos - kInfos); j < infos; ++j)
+    for (int j = max(0, asked - kInfos); j < asked; ++j)
       wait_for(&s.bar.info_full[j % kInfos], (j / kInfos) & 1, kDefaultWaitLimitCycles);
   }
   __syncwarp();
