@@ -28,7 +28,7 @@
 // TMA in 7 pieces of 64 slots x 64 bytes through a ring of kPieces: 24 KB (N 64)
 // or 56 KB stay on their way whatever the decode does.  (Plain loads of the
 // same bytes kept some 14 KB on the way, for the cache that they pass through
-// is what shared memory leaves of it, and took 193 us where this takes TIME_TMA
+// is what shared memory leaves of it, and took 193 us where this takes 123
 // on 64 requests x 8192 slots x 64 heads.)  The RoPE
 // words come through the registers of one warp.
 // The pages of all (request, head group) units are laid end to end
@@ -45,7 +45,6 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "kvc_decode.cuh"
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
 #include "kvc_operators.h"
@@ -85,11 +84,11 @@ constexpr float kRescaleAbove = 32.f;                   // log2
 constexpr int kJoinThreads = 512, kJoinCtasPerSm = 2;
 constexpr int kWeightSlots = 64;                        // slots at least for a CTA that forms weights
 
-// Groups of a page whose codes come through the ring, one warp and one or two
-// places each.  At N = 64 the 227 KB leave 6 places; with 7 groups in turn on
-// them the seventh piece of a page waited for a warp that was held up by the
-// first one, and every product with it (147 us on the case above; TIME_OWN so).
-// The seventh group is read ahead by its warp then, as the RoPE words are.
+// Groups of a page whose codes come through the ring, one warp and depth()
+// places each.  At N = 64 the 227 KB leave six places: the seventh group's warp
+// loads its codes itself.  (Seven groups in turn on six places held the seventh
+// piece up behind the first one's store; half places asked for twice a page, or
+// loads a page ahead into registers, took longer.)
 template <int N>
 __host__ __device__ constexpr int ring_groups() { return N == 64 ? 6 : 7; }
 // Pages that the ring holds, and pages whose scales are kept for its groups:
@@ -385,7 +384,8 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 // multiply-add by 2^(b - 121) less 128 2^(b - 127) leaves code 2^(b - 127),
 // 8 bits that are exact down to bf16's last subnormal.  b <= 247, so that
 // both constants are bf16 values: `up` = (b + 6) << 7, `less` = -((b + 7) << 7)
-// as bits, in both halves.
+// as bits, in both halves.  For a larger b the values of 247 are doubled
+// b - 247 times: exact, or infinite where the value is.
 __device__ __forceinline__ void decode4_bf16(uint32_t word, uint32_t up, uint32_t less, uint32_t* lo,
                                              uint32_t* hi) {
   const uint32_t u = word ^ 0x80808080u;
@@ -485,28 +485,61 @@ __device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
   }
 }
 
+// Eight times 16 codes and their scale bytes as 16 bf16.
+__device__ __forceinline__ void decode_rows(const uint4 (&raw)[8], const uint32_t (&scale)[8], uint4 (&lo)[8],
+                                            uint4 (&hi)[8]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    most = max(most, scale[j]);
+    const uint32_t b = min(scale[j], 247u), up = b * 0x00800080u + 0x03000300u, less = b * 0x00800080u + 0x83808380u;
+    decode4_bf16(raw[j].x, up, less, &lo[j].x, &lo[j].y);
+    decode4_bf16(raw[j].y, up, less, &lo[j].z, &lo[j].w);
+    decode4_bf16(raw[j].z, up, less, &hi[j].x, &hi[j].y);
+    decode4_bf16(raw[j].w, up, less, &hi[j].z, &hi[j].w);
+  }
+  if (__builtin_expect(__any_sync(0xFFFFFFFFu, most > 247u), 0)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t more = (127u + max(scale[j], 247u) - 247u) * 0x00800080u;  // 2^(b - 247)
+      lo[j] = make_uint4(mul_bf16x2(lo[j].x, more), mul_bf16x2(lo[j].y, more), mul_bf16x2(lo[j].z, more),
+                         mul_bf16x2(lo[j].w, more));
+      hi[j] = make_uint4(mul_bf16x2(hi[j].x, more), mul_bf16x2(hi[j].y, more), mul_bf16x2(hi[j].z, more),
+                         mul_bf16x2(hi[j].w, more));
+    }
+  }
+}
+
 // Decodes group g of every page: 64 slots x 64 codes, 8 times 8 slots, lane l
 // slot l / 4 of the 8 and codes 16 (l % 4) .. + 15.
 template <int N>
 __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, int count) {
-  constexpr int kDepth = depth<N>(), kScales = scale_slots<N>(), kRing = ring_groups<N>();
+  constexpr int kDepth = depth<N>(), kScales = scale_slots<N>();
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  uint32_t scale[8];
+  uint4 raw[8];
+  bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
-    const int stage = i & 1;
-    bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
+    const int stage = i & 1, place = i % kDepth;
+    ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
     const int valid = s.info[i % kInfos].valid;
-    uint32_t scale[8];
-    uint4 raw[8];
-    if (g < kRing) {
-      const int place = i % kDepth;
+    if (g < ring_groups<N>()) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
       ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit);
 #pragma unroll
       for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[place][g] + (lane + 32 * j) * 16);
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
+      // The place is given back once the values are there, not once they have
+      // been asked for: an arrival does not wait for the loads before it, and
+      // beside the products a load can take longer than the copy that then
+      // overwrites what it reads.  So who arrives hangs on the values (it does
+      // not matter who).
+      uint32_t all = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) all ^= raw[j].x ^ scale[j];
+      const int arrives = __all_sync(0xFFFFFFFFu, all == 1u) ? 1 : 0;
+      if (lane == arrives) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
     } else {
       const uint8_t* page = p.kv_cache + s.info[i % kInfos].id * kPageBytes;
 #pragma unroll
@@ -522,32 +555,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
     }
     // decoded before its place is free, so that only the stores are left then
     uint4 lo[8], hi[8];
-    uint32_t most = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) most = max(most, scale[j]);
-    if (__builtin_expect(__all_sync(0xFFFFFFFFu, most <= 247u), 1)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t up = scale[j] * 0x00800080u + 0x03000300u, less = scale[j] * 0x00800080u + 0x83808380u;
-        decode4_bf16(raw[j].x, up, less, &lo[j].x, &lo[j].y);
-        decode4_bf16(raw[j].y, up, less, &lo[j].z, &lo[j].w);
-        decode4_bf16(raw[j].z, up, less, &hi[j].x, &hi[j].y);
-        decode4_bf16(raw[j].w, up, less, &hi[j].z, &hi[j].w);
-      }
-    } else {  // values of 2^121 and above
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float hs = half_scale(scale[j]);
-        float f[16];
-        decode4(raw[j].x, hs, f);
-        decode4(raw[j].y, hs, f + 4);
-        decode4(raw[j].z, hs, f + 8);
-        decode4(raw[j].w, hs, f + 12);
-        lo[j] = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
-        hi[j] = make_uint4(bf16_pair(f[8], f[9]), bf16_pair(f[10], f[11]), bf16_pair(f[12], f[13]),
-                           bf16_pair(f[14], f[15]));
-      }
-    }
+    decode_rows(raw, scale, lo, hi);
     if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit);
     if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
       s.abort = 1;
@@ -565,7 +573,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
   }
 }
 
-// The RoPE words of every page, read ahead into registers (8 KB, which plain
+// The RoPE words of every page, read into registers ahead (8 KB, which plain
 // loads can keep on their way) and stored once their place is free: lane l has
 // piece l % 8 of rows l / 8 + 4 j.
 template <int N>
@@ -615,47 +623,57 @@ __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count)
   bool begins = true;            // the next half begins a segment
   bool ends[2] = {true, false};  // the page of each stage ends its segment
   bool fresh = true;             // the next second product is its segment's first
-  bool ok = true;
-  long long since = clock64();
+  bool ok = true, idle = false;
+  long long since = 0;  // idle
 #pragma unroll 1
   while (done < count) {
     const int i = halves >> 1, half = halves & 1, stage = i & 1;
-    bool first = i < count && dev::mbar_test_wait(&s.bar.half_full[stage][half], (i >> 1) & 1);
+    const uint32_t parity = (i >> 1) & 1;
+    // asked all at once: an answer takes long while products keep shared memory busy
+    bool first = dev::mbar_test_wait(&s.bar.half_full[stage][half], parity);
+    const bool other = dev::mbar_test_wait(&s.bar.half_full[stage][1], parity);
+    const bool second = dev::mbar_test_wait(&s.bar.p_full, done & 1);
     if (begins) first = first && dev::mbar_test_wait(&s.bar.q_full, segment & 1);
-    const bool second = done < i && dev::mbar_test_wait(&s.bar.p_full, done & 1);
-    if (__all_sync(0xFFFFFFFFu, second)) {
+    if (done < i && __all_sync(0xFFFFFFFFu, second)) {
       tc_fence_after();
       const int of = done & 1;
       const bool last = of == 0 ? ends[0] : ends[1];
       const uint32_t keys = operand_lo(all_keys + of * kKeyStage, kKeyBlock);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        if (elect_one()) {
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
                                            probs + k * 32 * N / 16, !fresh || k > 0);
           tc_commit(&s.bar.chunk_empty[of][c]);  // the decode of page i + 2 follows chunk by chunk
         }
+        if (last) tc_commit(&s.bar.o_full);
       }
-      if (last && elect_one()) tc_commit(&s.bar.o_full);
+      __syncwarp();
       fresh = last;
       ++done;
-    } else if (__all_sync(0xFFFFFFFFu, first)) {
+    } else if (i < count && __all_sync(0xFFFFFFFFu, first)) {
       tc_fence_after();
-      const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + half * (4 * kKeyBlock), 16);
-      const uint32_t queries = q + half * (4 * N * 128 / 16), into = tmem + 4 * N + stage * N;
-      if (elect_one()) {
+      const uint32_t into = tmem + 4 * N + stage * N;
+      const int to = half == 1 || __all_sync(0xFFFFFFFFu, other) ? 2 : 1;
+#pragma unroll 1
+      for (int h = half; h < to; ++h) {
+        const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + h * (4 * kKeyBlock), 16);
+        const uint32_t queries = q + h * (4 * N * 128 / 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 4; ++b)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma<kRows, kRows, kFirst>(into, keys + (b * kKeyBlock + 32 * k) / 16,
-                                         queries + (b * (N * 128) + 32 * k) / 16, half + b + k > 0);
+            for (int k = 0; k < 4; ++k)
+              tc_mma<kRows, kRows, kFirst>(into, keys + (b * kKeyBlock + 32 * k) / 16,
+                                           queries + (b * (N * 128) + 32 * k) / 16, h + b + k > 0);
+        }
+        __syncwarp();
       }
       segment += begins;
       begins = false;
-      if (half == 1) {
+      if (to == 2) {
         begins = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
         ends[0] = stage == 0 ? begins : ends[0];
         ends[1] = stage == 1 ? begins : ends[1];
@@ -663,16 +681,20 @@ __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count)
           tc_commit(&s.bar.s_full[stage]);
           if (begins) tc_commit(&s.bar.q_empty);
         }
+        __syncwarp();
       }
-      ++halves;
+      halves += to - half;
     } else {
-      if (__any_sync(0xFFFFFFFFu, clock64() - since > p.wait_limit || s.abort)) {
+      const long long now = clock64();
+      if (!idle) since = now;
+      idle = true;
+      if (__any_sync(0xFFFFFFFFu, now - since > p.wait_limit || s.abort)) {
         ok = false;
         break;
       }
       continue;
     }
-    since = clock64();
+    idle = false;
   }
   if (!ok) s.abort = 1;
   // no product may run on when the CTA's memory is given back
@@ -871,7 +893,8 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
       }
       fence_async_shared();
       tc_fence_before();
-      dev::mbar_arrive(&s.bar.p_full);
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&s.bar.p_full);
     }
     // the segment's end: columns' sums, then the rows of O
     combine_rows(sum, lane, [](float a, float b) { return a + b; });
@@ -951,7 +974,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
       for (int j = 0; j < 4; ++j) dev::mbar_init(&s.bar.chunk_empty[i][j], 1);
       dev::mbar_init(&s.bar.s_full[i], 1);
     }
-    dev::mbar_init(&s.bar.p_full, kSoftmaxThreads);
+    dev::mbar_init(&s.bar.p_full, kSoftmaxWarps);
     dev::mbar_init(&s.bar.q_full, 1);
     dev::mbar_init(&s.bar.q_empty, 1);
     dev::mbar_init(&s.bar.o_full, 1);

@@ -17,7 +17,7 @@
 // thread, and finds the keep-th largest two bits at a time by
 // counting: 16 rounds of one barrier each, whatever the weights are (a histogram
 // of digits took 24.7 us with its scans and its second pass over the keys on
-// 64 x 8192, this TIME_SELECT).  Longer requests go by digits, with the keys in
+// 64 x 8192, this 23 us).  Longer requests go by digits, with the keys in
 // shared memory.  Where a request can move 64 slots at most (it has outgrown
 // its share by less than a page), the selecting CTA moves them itself and the
 // second kernel is not launched.

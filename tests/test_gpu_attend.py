@@ -313,3 +313,114 @@ def test_lengths_change_between_replays(kvc):
         want = plain.attend(q.double().numpy(), kv, table, np.array(now), SCALE)
         _check(out, want[0], want[3], "out")
         _check(lse, want[1], want[4], "lse")
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 7, 40])
+@pytest.mark.parametrize("H", [5, 32, 64, 128])
+def test_any_number_of_shares(kvc, ctas, H):
+    # few CTAs: many segments each; 40: units cut in places of all kinds
+    _, kv, table, lengths, q, sinks = _case(21 + ctas, [700, 64, 0, 1, 130, 65, 333, 1291], H, sinks=True)
+    _compare(kvc, kv, table, lengths, q, sinks, weights=True, flags=ctas)
+
+
+@pytest.mark.parametrize("R,H", [(33, 64), (1500, 8)])
+def test_requests_beyond_a_warp_and_a_block(kvc, R, H):
+    rng = np.random.default_rng(22)
+    lengths = [int(x) for x in rng.integers(0, 3, R)]
+    lengths[R // 2] = 200
+    _, kv, table, lengths, q, _ = _case(23, lengths, H)
+    _compare(kvc, kv, table, lengths, q, weights=True)
+
+
+def test_bad_pages_in_a_divided_request(kvc):
+    # a bad page in the middle of a request that many CTAs share
+    rng, kv, table, lengths, q, _ = _case(24, [64 * 90, 64 * 70, 100], 64)
+    cuda = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    want = plain.attend(q.double().numpy(), kv, table, lengths, SCALE)
+    table = table.copy()
+    table[0, 41] = 1 << 30
+    out = torch.full((3, 64, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3, 64), 3.0, device="cuda")
+    w = torch.full((3, 64 * 90), 7.0, device="cuda")
+    kvc.attend(q.cuda(), cuda(kv), cuda(table), cuda(lengths), out=out, lse=lse, slot_weights=w)
+    assert _error(kvc) == kvc.KVC_ERR_BAD_INDEX
+    assert (out[0] == 3).all() and (lse[0] == 3).all() and (w[0] == 7).all()
+    for r in (1, 2):
+        n = int(lengths[r])
+        _check(out[r], want[0][r], want[3][r], "out")
+        _check(w[r, :n], want[2][r, :n], want[5][r, :n], "weights")
+
+
+@pytest.mark.parametrize("limit", [1, 3000])
+def test_waits_that_run_out(kvc, limit):
+    # shortened pipeline waits make the call give up: the error is reported, the
+    # context stays usable and the next call is right
+    _, kv, table, lengths, q, sinks = _case(25, [1000, 90, 700], 64, sinks=True)
+    cuda = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    try:
+        assert kvc.kvc_selftest_set_wait_limit(limit) == 0
+        w = torch.zeros((3, 1000), device="cuda")
+        kvc.attend(q.cuda(), cuda(kv), cuda(table), cuda(lengths), sinks=cuda(sinks), slot_weights=w)
+        assert _error(kvc) == kvc.KVC_ERR_TIMEOUT
+    finally:
+        kvc.kvc_selftest_set_wait_limit(0)
+    _compare(kvc, kv, table, lengths, q, sinks, weights=True)
+
+
+def test_calls_in_a_row_share_a_workspace(kvc):
+    # 40 calls of different shapes on one workspace, nothing waited for between
+    cases, got = [], []
+    ws = torch.empty(kvc.kvc_attend_workspace_bytes(8, 128, 40, True), dtype=torch.uint8, device="cuda")
+    cuda = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    for i in range(8):
+        rng = np.random.default_rng(26 + i)
+        lengths = [int(x) for x in rng.integers(0, 64 * 40, rng.integers(1, 9))]
+        _, kv, table, lengths, q, _ = _case(40 + i, lengths, int(rng.integers(1, 129)))
+        cases.append((q, kv, table, lengths, [q.cuda(), cuda(kv), cuda(table), cuda(lengths)]))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c in cases:
+            w = torch.zeros((len(c[3]), 64 * 40), device="cuda")
+            got.append(kvc.attend(*c[4], slot_weights=w, workspace=ws) + (w,))
+    assert _error(kvc) == 0
+    for i, (q, kv, table, lengths, _) in enumerate(cases):
+        want = plain.attend(q.double().numpy(), kv, table, lengths, SCALE)
+        _check(got[i][0], want[0], want[3], "out")
+        _check(got[i][1], want[1], want[4], "lse")
+        for again in got[i::8]:
+            assert all(torch.equal(a, b) for a, b in zip(again, got[i]))
+
+
+def test_keys_of_large_values(kvc):
+    # scale bytes above 247: values of 2^121 and more, exact in the sum
+    rng = np.random.default_rng(27)
+    kv = plain.random_cache(rng, 1)
+    rows = kv[0, :SCALE_BASE].reshape(64, TOKEN_STRIDE)
+    rows[:, :448] = 0
+    rows[:, :64] = rng.integers(0, 256, (64, 64), dtype=np.uint8)
+    kv[0, SCALE_BASE:].reshape(64, SCALE_DIM)[:, :7] = rng.integers(240, 249, (64, 7), dtype=np.uint8)
+    lengths = np.array([64], np.int32)
+    q = torch.zeros((1, 4, 512), dtype=torch.bfloat16)
+    q[:, :, 448:] = torch.from_numpy(rng.standard_normal((1, 4, 64)).astype(np.float32)).to(torch.bfloat16)
+    _compare(kvc, kv, np.zeros((1, 1), np.int32), lengths, q)
+
+
+@pytest.mark.parametrize("lengths,H", [([64 * 152 * 4], 64), ([410, 2199, 1464, 1083, 965, 724, 826, 1673], 88), ([8192], 128),
+                                       ([2000] * 20, 32), ([900] * 40, 16)])
+def test_many_calls_give_the_same_bits(kvc, lengths, H):
+    # several pages a CTA, so that every place of the rings is used again; a place
+    # given back too early shows as rare differences between calls
+    _, kv, table, lengths, q, _ = _case(60 + H, lengths, H)
+    cuda = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    args = (q.cuda(), cuda(kv), cuda(table), cuda(lengths))
+    ws = torch.empty(kvc.kvc_attend_workspace_bytes(len(lengths), H, table.shape[1], True), dtype=torch.uint8, device="cuda")
+    w = torch.zeros((len(lengths), int(max(lengths))), device="cuda")
+    first = kvc.attend(*args, slot_weights=w, workspace=ws) + (w.clone(),)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        out, lse = kvc.attend(*args, slot_weights=w, workspace=ws)
+        differ += (out != first[0]).any() | (lse != first[1]).any() | (w != first[2]).any()
+    assert int(differ) == 0
+    want = plain.attend(q.double().numpy(), kv, table, lengths, SCALE)
+    _check(out, want[0], want[3], "out")
+    _check(w, np.where(np.arange(w.shape[1]) < lengths[:, None], want[2], 0), want[5], "weights")
