@@ -334,7 +334,12 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
  * cache, records KVC_ERR_BAD_INDEX in the device error word and leaves that
  * request's out, lse and slot_weights as they were; the other requests are
  * computed.  The same inputs give the same bits on every call.  num_reqs at
- * most 65535.  Allocates nothing.
+ * most 65535, num_kv_pages and num_reqs * max_pages_per_req * ceil(num_heads /
+ * 64) below 2^31.  A pipeline wait that runs past its limit records
+ * KVC_ERR_TIMEOUT; the call's rows and weights are then partly as they were.
+ * Slots that hold infinities or NaN give what the sums above give, and so do
+ * slots so large that their sum (each times exp(s_n - max), before the division)
+ * leaves the fp32 range.  Allocates nothing.
  */
 size_t kvc_attend_workspace_bytes(int64_t num_reqs, int32_t num_heads, int64_t max_pages_per_req,
                                   int32_t with_slot_weights);
@@ -485,7 +490,8 @@ kvc_status kvc_selftest_wait_timeout(uint64_t limit_cycles, void* stream);
 /*
  * Test hook for the kernels' abort path: sets the limit, in SM clock cycles,
  * on each pipeline wait (a copy stage, a hand-off between warps) of every
- * compression launched afterwards by this process, on any device.
+ * compression and attention (kvc_attend) launched afterwards by this process,
+ * on any device.
  * limit_cycles 0 restores the default (4e9 cycles, about 2 s); 1 .. 4e9 sets
  * it; larger values return KVC_ERR_INVALID_ARG.  Limits below 100000 cycles
  * are polled without suspending the waiting thread, so they run out on time.

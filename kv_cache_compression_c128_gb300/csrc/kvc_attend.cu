@@ -24,18 +24,29 @@
 // stays in range, so O is rescaled only where a score exceeds m by 2^32.
 //
 // Warps of a CTA: 0..3 softmax and epilogue, one issues the products, one copies
-// the codes, one the queries, seven decode, one brings the RoPE words.  The codes of a page come by
-// TMA in 7 pieces of 64 slots x 64 bytes through a ring of kPieces: 24 KB (N 64)
-// or 56 KB stay on their way whatever the decode does.  (Plain loads of the
-// same bytes kept some 14 KB on the way, for the cache that they pass through
-// is what shared memory leaves of it, and took 193 us where this takes 123
-// on 64 requests x 8192 slots x 64 heads.)  The RoPE
-// words come through the registers of one warp.
-// The pages of all (request, head group) units are laid end to end
-// and cut into equal shares, one per CTA; a unit that a cut divides leaves its
-// parts (m, l, O) in the workspace, and a second kernel joins them in the order
-// of the shares, so the same lengths give the same bits.  That kernel also
-// forms the slots' weights, from the scores that the first one left behind.
+// the codes, one the queries, seven decode, one brings the RoPE words.  The codes
+// of a page come by TMA, a piece of 64 slots x 64 bytes for each scale group,
+// through a ring: 24 KB (N 64) or 56 KB stay on their way whatever the decode
+// does.  (Plain loads kept some 14 KB on the way, for the cache that they pass
+// through is what shared memory leaves of it: 193 us on 64 requests x 8192 slots
+// x 64 heads where the ring takes 123.)
+//
+// The pages of all (request, head group) units are laid end to end and cut into
+// equal shares, one per CTA; a unit that a cut divides leaves its parts (m, l, O)
+// in the workspace, and a second kernel joins them in the order of the shares, so
+// the same lengths give the same bits.  That kernel also forms the slots' weights,
+// from the scores that the first one left behind.
+//
+// What bounds it: a page's products take 1792 cycles at N = 64 and 1380 at 16,
+// all of them operand reads from shared memory at 128 bytes a cycle (measured
+// alone: 32 and 48 cycles for the M 64 and M 128 instruction at N 64, 23.5 and 39
+// at N 16).  The decode's stores and loads of the same memory add some 1000, and a
+// page takes about 4000 in all (2.1 us; 64 requests x 8192 slots x 64 heads: 123
+// us, 2.5 TB/s and 0.56 PFLOP/s): beside the products every other access of
+// shared memory is slow, a barrier's question 250 to 450 cycles.  Hence few
+// questions, one short issuing loop, rolled loops throughout (straight code of
+// every role does not stay in the instruction cache: 180 us unrolled), and no
+// more places than one for each decoding warp.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,7 +54,6 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
-#include <type_traits>
 
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
@@ -523,7 +533,8 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1, place = i % kDepth;
     ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
-    const int valid = s.info[i % kInfos].valid;
+    // (what is not described, after a wait that ran out, is not an address)
+    const PageInfo info = ok ? s.info[i % kInfos] : PageInfo{0, 0, 0};
     if (g < ring_groups<N>()) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
@@ -541,17 +552,17 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
       const int arrives = __all_sync(0xFFFFFFFFu, all == 1u) ? 1 : 0;
       if (lane == arrives) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
     } else {
-      const uint8_t* page = p.kv_cache + s.info[i % kInfos].id * kPageBytes;
+      const uint8_t* page = p.kv_cache + info.id * kPageBytes;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         raw[j] = load16(page + (r + 8 * j) * kTokenStride + g * kGroup + 16 * c);
         scale[j] = __ldg(page + kScaleBase + (r + 8 * j) * kScaleDim + g);
       }
     }
-    if (__builtin_expect(valid < kSlotsPerPage, 0)) {  // code 0 in every place of the slots that do not count
+    if (__builtin_expect(info.valid < kSlotsPerPage, 0)) {  // code 0 in every place of the slots that do not count
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (r + 8 * j >= valid) raw[j] = make_uint4(0, 0, 0, 0), scale[j] = 0;
+        if (r + 8 * j >= info.valid) raw[j] = make_uint4(0, 0, 0, 0), scale[j] = 0;
     }
     // decoded before its place is free, so that only the stores are left then
     uint4 lo[8], hi[8];
@@ -583,7 +594,7 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) 
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1;
     bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
-    const PageInfo info = s.info[i % kInfos];
+    const PageInfo info = ok ? s.info[i % kInfos] : PageInfo{0, 0, 0};
     const uint8_t* src = p.kv_cache + info.id * kPageBytes + r * kTokenStride + kNopeDim + 16 * c;
     uint4 v[16];
 #pragma unroll

@@ -392,13 +392,14 @@ def test_calls_in_a_row_share_a_workspace(kvc):
 
 
 def test_keys_of_large_values(kvc):
-    # scale bytes above 247: values of 2^121 and more, exact in the sum
+    # The sum of a row is formed in fp32 before it is divided, so 64 slots of
+    # 128 * 2^(b - 127) have to stay below 2^128: b up to 241 (7 + 114 + 6 = 127).
     rng = np.random.default_rng(27)
     kv = plain.random_cache(rng, 1)
     rows = kv[0, :SCALE_BASE].reshape(64, TOKEN_STRIDE)
     rows[:, :448] = 0
     rows[:, :64] = rng.integers(0, 256, (64, 64), dtype=np.uint8)
-    kv[0, SCALE_BASE:].reshape(64, SCALE_DIM)[:, :7] = rng.integers(240, 249, (64, 7), dtype=np.uint8)
+    kv[0, SCALE_BASE:].reshape(64, SCALE_DIM)[:, :7] = rng.integers(231, 242, (64, 7), dtype=np.uint8)
     lengths = np.array([64], np.int32)
     q = torch.zeros((1, 4, 512), dtype=torch.bfloat16)
     q[:, :, 448:] = torch.from_numpy(rng.standard_normal((1, 4, 64)).astype(np.float32)).to(torch.bfloat16)
