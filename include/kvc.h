@@ -315,12 +315,13 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
  *              page_table_row_stride; only the entries below
  *              ceil(lengths[r] / 64) are read.  Requests may share pages.
  * lengths      int32 [num_reqs], 0 .. max_pages_per_req * 64.
- * scale        finite.
+ * scale        finite, and so is scale * log2(e).
  * sinks        fp32 [num_heads] or NULL.
  * out          bf16 [num_reqs, num_heads, 512], 16-byte aligned.
  * lse          fp32 [num_reqs, num_heads] or NULL.
  * slot_weights fp32 [num_reqs, max_slots] at its row stride, or NULL; entries
- *              at and behind lengths[r] are left as they were.
+ *              at and behind lengths[r] are left as they were.  Its rows do not
+ *              overlap (with several requests, row stride >= max_slots).
  * slot_weights_in  fp32 of the same shape at its row stride, or NULL for
  *              zeros; may be slot_weights itself (accumulation in place).
  * max_slots    columns of slot_weights (not read without it).
@@ -384,7 +385,8 @@ kvc_status kvc_join(const void* const* outs, const float* const* lses, int32_t n
  *
  * kv_cache     uint8 [num_kv_pages, 37376]; the moved slots' 576 + 8 bytes
  *              are written at their new places, all other bytes left alone.
- *              No page may belong to two requests of the call.
+ *              No page may belong to two requests of the call, or stand twice
+ *              among a request's.
  * page_table, lengths   as for kvc_attend.
  * slot_weights fp32 [num_reqs, max_slots] at its row stride.
  * births       int32 of the same shape at its row stride, or NULL if recent
@@ -396,7 +398,8 @@ kvc_status kvc_join(const void* const* outs, const float* const* lses, int32_t n
  *              now at each place, -1 from `new` on.
  * slot_weights_out, births_out   optional [num_reqs, >= min(keep, max_slots)]
  *              at their row strides: the arrays in the new order, left as
- *              they were from `new` on; may be slot_weights and births.
+ *              they were from `new` on; may be slot_weights and births.  Their
+ *              rows do not overlap.
  * workspace    kvc_evict_workspace_bytes(...) bytes, as for kvc_attend.
  *
  * A bad length or page is treated as in kvc_attend: that request, its row of

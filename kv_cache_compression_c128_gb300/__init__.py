@@ -743,7 +743,8 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
     summed over the heads: what `evict` goes by.  A request whose length or
     pages are out of range keeps its rows as they were and raises the device
     error word (kvc_get_device_error).  A workspace given by the caller
-    (kvc_attend_workspace_bytes) serves calls that do not overlap.
+    (kvc_attend_workspace_bytes) serves calls that do not overlap.  A serving
+    form: no gradient is recorded.
     """
     torch = _torch or _load_torch()
     device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
@@ -765,6 +766,8 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
         rows, S, weights_row = _rows("slot_weights", slot_weights, torch.float32, device)
         if rows != R:
             raise ValueError("slot_weights must have one row per request")
+        if S == 0 and R != 0:
+            raise ValueError("slot_weights must have at least one column")
     if slot_weights_in is not None:
         rows, cols, in_row = _rows("slot_weights_in", slot_weights_in, torch.float32, device)
         if slot_weights is None or (rows, cols) != (R, S):
@@ -774,6 +777,8 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
     if lse is not None:
         _dense("lse", lse, torch.float32, device, shape[:2])
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            _refuse("workspace", workspace, torch.uint8, 1, device)
         _dense("workspace", workspace, torch.uint8, device, (workspace.numel(),))
     if R != 0 and columns == 0:
         raise ValueError("page_table must have at least one column")
@@ -812,7 +817,7 @@ def join(outs, lses, *, out=None, lse=None, stream=None):
     outs: 1 to 8 contiguous [..., 512] tensors, all bf16 or all fp32, of one
     shape; lses: as many contiguous fp32 tensors of that shape without the 512
     (-inf: the part held no key for the row).  Returns (out, lse); `out` may
-    be one of outs and `lse` one of lses.
+    be one of outs and `lse` one of lses.  No gradient is recorded.
     """
     torch = _torch or _load_torch()
     if not 1 <= len(outs) <= 8 or len(lses) != len(outs):
@@ -861,7 +866,7 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
     index first among equals, NaN last.  Slots that stay below the new length
     keep their places; the i-th place that falls free takes the i-th slot that
     stays from behind.  The slots' bytes move within kv_cache; no page may
-    belong to two requests.
+    belong to two requests or stand twice in one's table.
 
     Returns (lengths_out int32 [R], kept int32 [R, keep]): the new lengths,
     and the former place of the slot at each place (-1 behind the new length).
@@ -897,6 +902,8 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
     if kept is not None:
         _dense("kept", kept, torch.int32, device, (R, keep))
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            _refuse("workspace", workspace, torch.uint8, 1, device)
         _dense("workspace", workspace, torch.uint8, device, (workspace.numel(),))
     if R != 0 and columns == 0:
         raise ValueError("page_table must have at least one column")

@@ -27,6 +27,11 @@ bool pages_ok(const void* kv_cache, int64_t num_kv_pages, const int32_t* page_ta
          aligned(page_table, 4) && aligned(lengths, 4);
 }
 
+// Rows that are written do not overlap.
+bool rows_apart(int64_t num_reqs, int64_t row_stride, int64_t columns) {
+  return num_reqs <= 1 || row_stride >= columns;
+}
+
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 // Byte offsets in an attention's workspace.
@@ -77,8 +82,9 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
                       int64_t slot_weights_in_row_stride, float* slot_weights,
                       int64_t slot_weights_row_stride, int64_t max_slots, void* workspace,
                       size_t workspace_bytes, uint32_t flags, void* stream) {
-  if (num_reqs < 0 || num_heads < 1 || num_heads > kvc::kMaxHeads || !std::isfinite(scale) ||
-      (flags & ~KVC_FLAG_GRID_MASK) != 0)
+  // (the kernel works in powers of two: scale times log2(e) is finite too)
+  if (num_reqs < 0 || num_heads < 1 || num_heads > kvc::kMaxHeads ||
+      !std::isfinite(scale * 1.44269504f) || (flags & ~KVC_FLAG_GRID_MASK) != 0)
     return KVC_ERR_INVALID_ARG;
   if (num_reqs == 0) return KVC_OK;
   if (!pages_ok(kv_cache, num_kv_pages, page_table, num_reqs, max_pages_per_req,
@@ -92,7 +98,8 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
   if (slot_weights == nullptr && slot_weights_in != nullptr) return KVC_ERR_INVALID_ARG;
   if (slot_weights != nullptr &&
       (max_slots < 0 || slot_weights_row_stride < 0 || slot_weights_in_row_stride < 0 ||
-       !aligned(slot_weights, 4) || !aligned(slot_weights_in, 4)))
+       !aligned(slot_weights, 4) || !aligned(slot_weights_in, 4) ||
+       !rows_apart(num_reqs, slot_weights_row_stride, max_slots)))
     return KVC_ERR_INVALID_ARG;
   const size_t need = kvc_attend_workspace_bytes(num_reqs, num_heads, max_pages_per_req,
                                                  slot_weights != nullptr);
@@ -187,7 +194,9 @@ kvc_status kvc_join(const void* const* outs, const float* const* lses, int32_t n
 }
 
 size_t kvc_evict_workspace_bytes(int64_t num_reqs, int64_t max_pages_per_req, int64_t keep) {
-  if (num_reqs < 0 || max_pages_per_req < 0 || keep < 0) return 0;
+  if (num_reqs < 0 || num_reqs > kMaxRequests || max_pages_per_req < 0 ||
+      max_pages_per_req > kMaxSlots / kvc::kSlotsPerPage || keep < 0 || keep > kMaxSlots)
+    return 0;
   // as many moves as slots can lie behind `keep`, or before it
   const int64_t slots = max_pages_per_req * kvc::kSlotsPerPage;
   const int64_t behind = slots > keep ? slots - keep : 0;
@@ -215,6 +224,10 @@ kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* pag
       births_out_row_stride < 0 || !aligned(slot_weights, 4) || !aligned(births, 4) ||
       !aligned(lengths_out, 4) || !aligned(kept, 4) || !aligned(slot_weights_out, 4) ||
       !aligned(births_out, 4))
+    return KVC_ERR_INVALID_ARG;
+  const int64_t stay = keep < max_slots ? keep : max_slots;
+  if ((slot_weights_out != nullptr && !rows_apart(num_reqs, slot_weights_out_row_stride, stay)) ||
+      (births_out != nullptr && !rows_apart(num_reqs, births_out_row_stride, stay)))
     return KVC_ERR_INVALID_ARG;
   const size_t need = kvc_evict_workspace_bytes(num_reqs, max_pages_per_req, keep);
   if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < need)

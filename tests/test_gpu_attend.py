@@ -425,3 +425,34 @@ def test_many_calls_give_the_same_bits(kvc, lengths, H):
     want = plain.attend(q.double().numpy(), kv, table, lengths, SCALE)
     _check(out, want[0], want[3], "out")
     _check(w, np.where(np.arange(w.shape[1]) < lengths[:, None], want[2], 0), want[5], "weights")
+
+
+def test_refusals_of_the_wrapper(kvc):
+    kv = torch.zeros((4, PAGE_BYTES), dtype=torch.uint8, device="cuda")
+    table, n = torch.zeros((2, 2), dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    q = torch.zeros((2, 8, 512), dtype=torch.bfloat16, device="cuda")
+    attend = lambda **more: kvc.attend(**dict(dict(q=q, kv_cache=kv, page_table=table, lengths=n), **more))
+    for error, more in [
+            (TypeError, dict(q=q.float())), (ValueError, dict(q=q[:, :, :256])), (ValueError, dict(q=q[:1])),
+            (ValueError, dict(q=q.transpose(1, 2).contiguous().transpose(1, 2))), (ValueError, dict(kv_cache=kv[:, :64])),
+            (TypeError, dict(page_table=table.long())), (ValueError, dict(page_table=table[:, :0])),
+            (TypeError, dict(lengths=n.long())), (ValueError, dict(lengths=n[:1])), (TypeError, dict(lengths=[1, 1])),
+            (ValueError, dict(sinks=torch.zeros(7, device="cuda"))), (ValueError, dict(lse=torch.zeros(2, 8))),
+            (ValueError, dict(slot_weights=torch.zeros((2, 0), device="cuda"))),
+            (ValueError, dict(slot_weights=torch.zeros((3, 128), device="cuda"))),
+            (kvc.KvcError, dict(slot_weights=torch.zeros(128, device="cuda").expand(2, 128))),
+            (ValueError, dict(slot_weights_in=torch.zeros((2, 128), device="cuda"))),
+            (TypeError, dict(workspace=[0])), (kvc.KvcError, dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))),
+            (kvc.KvcError, dict(scale=3e38)), (kvc.KvcError, dict(flags=1 << 16))]:
+        with pytest.raises(error):
+            attend(**more)
+    out, lse = attend()
+    assert _error(kvc) == 0 and torch.equal(out, torch.zeros_like(out)) and torch.equal(lse, torch.zeros_like(lse))
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("lengths,H", [([0, 100, 0, 192], 64), ([0] * 9 + [1] + [0] * 200, 8), ([64, 0, 33], 100), ([0, 0], 128)])
+def test_short_requests_beside_empty_ones(kvc, lengths, H, sinks):
+    _, kv, table, n, q, s = _case(77, lengths, H, sinks=sinks)
+    _compare(kvc, kv, table, n, q, s)
+    _compare(kvc, kv, table, n, q, s, flags=1)

@@ -195,3 +195,22 @@ def test_stream_and_graph(kvc):
     g.replay()
     g.replay()
     assert np.array_equal(b.cpu().numpy(), want_kv) and np.array_equal(kept.cpu().numpy(), want_kept)
+
+
+def test_refusals_of_the_wrapper(kvc):
+    kv = torch.zeros((4, PAGE_BYTES), dtype=torch.uint8, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    n, w = torch.ones(2, dtype=torch.int32, device="cuda"), torch.ones((2, 128), device="cuda")
+    births = torch.zeros((2, 128), dtype=torch.int32, device="cuda")
+    evict = lambda **more: kvc.evict(**dict(dict(kv_cache=kv, page_table=table, lengths=n, slot_weights=w, keep=4), **more))
+    for error, more in [
+            (ValueError, dict(keep=-1)), (ValueError, dict(recent=5, births=births)), (ValueError, dict(recent=1)),
+            (ValueError, dict(births_out=births)), (TypeError, dict(slot_weights=w.double())), (ValueError, dict(slot_weights=w[:1])),
+            (ValueError, dict(slot_weights=w.t().contiguous().t())), (ValueError, dict(births=births[:, :64])),
+            (ValueError, dict(slot_weights_out=w[:, :3])), (kvc.KvcError, dict(slot_weights_out=w[0].expand(2, 128))),
+            (ValueError, dict(kept=torch.zeros((2, 3), dtype=torch.int32, device="cuda"))), (TypeError, dict(workspace=3)),
+            (ValueError, dict(page_table=table[:, :0])), (TypeError, dict(lengths=n.float()))]:
+        with pytest.raises(error):
+            evict(**more)
+    new, kept = evict()
+    assert new.tolist() == [1, 1] and kept.tolist() == [[0, -1, -1, -1]] * 2

@@ -97,3 +97,22 @@ def test_wrappers_refuse_cpu_tensors_and_wrong_types(kvc):
         kvc.join([torch.zeros(1, 512)], [torch.zeros(1)])
     with pytest.raises(ValueError, match="one entry per part"):
         kvc.join([torch.zeros(1, 512)], [])
+
+
+@pytest.mark.parametrize("change", [dict(scale=3e38), dict(slot_weights=0xA0000, slot_weights_row_stride=0, max_slots=512),
+                                    dict(slot_weights=0xA0000, slot_weights_row_stride=511, max_slots=512)])
+def test_attend_refuses_scales_near_the_end_and_rows_that_overlap(kvc, change):
+    assert kvc.kvc_attend(**dict(_ATTEND, **change)) == kvc.KVC_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(slot_weights_out=0x90000, slot_weights_out_row_stride=99), dict(births_out=0x90000, births_out_row_stride=0),
+    dict(births_out=0x90000, births_out_row_stride=49, max_slots=50, keep=64)])
+def test_evict_refuses_rows_that_overlap(kvc, change):
+    assert kvc.kvc_evict(**dict(_EVICT, **change)) == kvc.KVC_ERR_INVALID_ARG
+
+
+def test_workspace_sizes_beyond_the_limits_are_zero(kvc):
+    for args in [(65536, 8, 8), (8, 1 << 58, 8), (8, 8, 1 << 62)]:
+        assert kvc.kvc_evict_workspace_bytes(*args) == 0
+    assert kvc.kvc_evict_workspace_bytes(65535, (1 << 30) // 64, 1 << 29) >= 65535 * (16 << 29)
