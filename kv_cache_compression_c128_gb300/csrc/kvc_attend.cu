@@ -91,7 +91,7 @@ constexpr int kInfos = 8;
 // divided: joining the parts costs about as much as this many pages.
 constexpr int kUndivided = 3;
 constexpr float kRescaleAbove = 32.f;                   // log2
-constexpr int kJoinThreads = 512, kJoinCtasPerSm = 2;
+constexpr int kJoinThreads = kAttendThreads, kJoinCtasPerSm = 2;
 constexpr int kWeightSlots = 64;                        // slots at least for a CTA that forms weights
 
 // Groups of a page whose codes come through the ring, one warp and depth()
@@ -972,6 +972,15 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
   }
 }
 
+// A request without slots: zeros and the sinks; all kAttendThreads threads.
+__device__ __forceinline__ void write_empty(const AttendParams& p, int64_t r) {
+  const int64_t row0 = r * p.num_heads;
+  uint4* const out = reinterpret_cast<uint4*>(p.out + row0 * kHeadDim);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < p.num_heads * (kHeadDim / 8); i += kAttendThreads) out[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < p.num_heads) p.lse[row0 + threadIdx.x] = p.sinks == nullptr ? -INFINITY : p.sinks[threadIdx.x];
+}
+
 template <int N>
 __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(1024) uint8_t raw_shared[];
@@ -1112,6 +1121,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   __syncthreads();
   tc_fence_after();
   if (s.rows.heads > 0) write_rows<N>(p, s, s.rows, (warp >> 2) * N, (warp >> 2) * N + N);
+  if (p.alone) {
+#pragma unroll 1
+    for (int r = cta; r < reqs; r += grid)
+      if (p.lengths[r] == 0) write_empty(p, r);
+  }
   if (t == 0 && s.abort) {
     atomicCAS(p.error, 0u, kErrTimeout);
     p.joins[cta] = make_int4(-2, 0, 0, 0);
@@ -1270,11 +1284,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
     if (length < 0 || length > p.max_slots) continue;
     if (length == 0) {
       if (sub != 0) continue;
-      const int64_t row0 = static_cast<int64_t>(r) * p.num_heads;
-      uint4* out = reinterpret_cast<uint4*>(p.out + row0 * kHeadDim);
-      for (int i = t; i < p.num_heads * (kHeadDim / 8); i += kJoinThreads) out[i] = make_uint4(0, 0, 0, 0);
-      for (int h = t; h < p.num_heads; h += kJoinThreads)
-        p.lse[row0 + h] = p.sinks == nullptr ? -INFINITY : p.sinks[h];
+      write_empty(p, r);
       continue;
     }
     if (p.weights_out == nullptr || length * sub / weight_ctas == length * (sub + 1) / weight_ctas) continue;
@@ -1343,7 +1353,7 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N>, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.alone) return e;
   // as many as fit at once: they share the divided units' heads, then the requests
   constexpr int kMost = kJoinCtasPerSm * kAttendCtas;
   const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kWeightSlots - 1) / kWeightSlots;
@@ -1366,6 +1376,10 @@ AttendShape attend_shape(int num_heads) {
   s.group_heads = (num_heads + s.groups - 1) / s.groups;
   s.columns = s.group_heads <= 16 ? 16 : s.group_heads <= 32 ? 32 : 64;
   return s;
+}
+
+bool attend_alone(const AttendParams& p, int ctas) {
+  return p.weights_out == nullptr && p.max_pages <= kUndivided && p.num_reqs * p.groups <= ctas;
 }
 
 cudaError_t launch_attend(const AttendParams& p, int columns, int ctas, cudaStream_t stream) {

@@ -164,6 +164,7 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
   int64_t ctas = sms < kvc::kAttendCtas ? sms : kvc::kAttendCtas;
   if (num_reqs * max_pages_per_req * shape.groups < ctas) ctas = num_reqs * max_pages_per_req * shape.groups;
   if ((flags & KVC_FLAG_GRID_MASK) != 0 && (flags & KVC_FLAG_GRID_MASK) < ctas) ctas = flags & KVC_FLAG_GRID_MASK;
+  p.alone = kvc::attend_alone(p, static_cast<int>(ctas));
   const cudaError_t e =
       kvc::launch_attend(p, shape.columns, static_cast<int>(ctas), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
