@@ -52,6 +52,7 @@
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -90,8 +91,10 @@ constexpr int kInfos = 8;
 // Pages by which the longest unit may exceed an equal share before units are
 // divided: joining the parts costs about as much as this many pages.
 constexpr int kUndivided = 3;
+constexpr int kFewReqs = 160;  // more are never shared out by units: there are fewer CTAs
 constexpr float kRescaleAbove = 32.f;                   // log2
 constexpr int kJoinThreads = kAttendThreads, kJoinCtasPerSm = 2;
+constexpr int kStatsPerLane = (kAttendCtas + 31) / 32;  // of a unit's parts
 constexpr int kWeightSlots = 64;                        // slots at least for a CTA that forms weights
 
 // Groups of a page whose codes come through the ring, one warp and depth()
@@ -151,7 +154,7 @@ struct AttendShared {
   Barriers<N> bar;
   PageInfo info[kInfos];
   uint8_t bad[8];  // of the last segments: a page was outside the cache
-  int total;
+  int count, ctas, total, each;  // pages in all, and of a share that begins anew with every unit (0: equal shares)
   int start[4];  // request, length, unit and page of the share's first page
   Rows rows;     // of the last segment
   uint32_t tmem;
@@ -303,6 +306,15 @@ __device__ __forceinline__ bool softmax_any(bool x) {
       : "r"(static_cast<uint32_t>(x)), "n"(kSoftmaxThreads)
       : "memory");
   return r != 0;
+}
+
+__device__ __forceinline__ int warp_inclusive(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
 }
 
 // ---- the walk over a CTA's share -------------------------------------------------
@@ -791,14 +803,15 @@ __device__ __forceinline__ void store_combined(const float (&v)[kCount], int lan
 // Softmax warps.  Warp w has slots 16 w .. 16 w + 15 of a page: thread t the
 // slots t / 4 and t / 4 + 8 of them, and columns 2 (t % 4) + {0, 1} of each 8.
 template <int N>
-__device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, int cta, int ctas) {
+__device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
   constexpr int kCols = N / 4;  // columns of a thread
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t tmem = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const float c = p.scale == 0.f ? 1.f : p.scale * kLog2e;  // scores of scale 0 are zeros
   const uint32_t behind = c < 0.f ? 0x7F800000u : 0xFF800000u;  // times c: -inf
   const int row = warp * 16 + (lane >> 2);
-  int i = 0, at = share_start(s.total, cta, ctas);  // (used where units are divided)
+  const int cta = blockIdx.x;
+  int i = 0, at = share_start(s.total, cta, s.ctas);  // (used with equal shares)
   bool ok = true;  // once false, the next vote ends the role
 #pragma unroll 1
   for (int segment = 0; w.left > 0; ++segment) {
@@ -941,13 +954,14 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
     if (t == 0) {
       if (w.page == 0) {  // the unit's first part: where its parts lie
         p.unit_parts[static_cast<int64_t>(w.req) * p.groups + w.group] =
-            whole ? make_int2(-1, bad) : make_int2(part, share_of(s.total, at + w.pages - 1, ctas));
+            whole ? make_int2(-1, bad)
+                  : make_int2(part, s.each > 0 ? cta + (w.pages - 1) / s.each : share_of(s.total, at + w.pages - 1, s.ctas));
       }
       if (!whole) {
         p.part_bad[part] = bad;
         if (w.page + n == w.pages) {  // the unit's last part: this share's joins it
-          const int first = share_of(s.total, at - w.page, ctas);
-          const bool at_start = share_start(s.total, first, ctas) == at - w.page;
+          const int first = s.each > 0 ? cta - w.page / s.each : share_of(s.total, at - w.page, s.ctas);
+          const bool at_start = s.each > 0 || share_start(s.total, first, s.ctas) == at - w.page;
           p.joins[cta] = make_int4(w.req, w.group, 2 * first + !at_start, cta);
         }
       }
@@ -970,6 +984,43 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w, 
     at += n;
     w.advance(p, n);
   }
+}
+
+// Shares of `each` pages that begin anew with every unit: the fewest pages for
+// which the CTAs suffice, if not too many over an equal share (each 0: none).
+// An equal share of several units ends several times, some 4 us each at N = 64:
+// 32 requests of up to 4000 slots take 34.7 us with equal shares and 26.1 with
+// these, 96 of up to 1500 37.4 and 28.8 (64 heads); 32 of up to 4000 at 16 heads
+// 24.9 and 21.2.  Every warp tries a number; `own` and `before` are the finder's
+// lanes'.  The search takes 1 us.
+struct Shares {
+  int each, count, finder, own, before;
+};
+template <int N>
+__device__ __forceinline__ Shares aligned_shares(const AttendParams& p, int4* scan, int lo, int hi, int total, int units,
+                                              int shortest, int grid) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, least = (total + grid - 1) / grid;
+  Shares of = {0, 0, 0, 0, 0};
+  // pages that it is worth: more for N = 64's longer end, and where a share could hold several short units
+  const int several = min(least / __reduce_min_sync(0xFFFFFFFFu, shortest), 2);
+  const int most = total / grid + (N == 64 ? 4 + 4 * several : 2);
+  // a unit's last share is half empty on average: not tried where that is too much
+  if (total / most + units / 2 > grid) return of;
+#pragma unroll 1
+  for (int r = lo; r < hi; ++r) of.own += (pages_of(p, p.lengths[r]) + least + warp - 1) / (least + warp);
+  const int all = __reduce_add_sync(0xFFFFFFFFu, of.own) * p.groups;
+  if (lane == 0) scan[warp].x = all;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < kAttendThreads / 32 && least + i <= most; ++i) {
+    of.count = scan[i].x;
+    if (of.count > grid) continue;
+    of.each = least + i;
+    of.finder = i;
+    of.before = warp_inclusive(of.own, lane) - of.own;
+    break;
+  }
+  return of;
 }
 
 // A request without slots: zeros and the sinks; all kAttendThreads threads.
@@ -1011,30 +1062,33 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // Where the share lies: the pages (the host has checked that all fit 31 bits)
-  // and the units before each thread's run of requests.  Up to 32 requests
-  // every warp finds it for itself, a request a lane.
-  const int reqs = static_cast<int>(p.num_reqs);
-  const bool few = reqs <= 32;
-  const int run = few ? 1 : (reqs + kAttendThreads - 1) / kAttendThreads;
+  // and the units before each thread's run of requests.  Up to kFewReqs requests
+  // every warp finds it for itself, a run of requests a lane.
+  const int reqs = static_cast<int>(p.num_reqs), grid = static_cast<int>(gridDim.x);
+  const bool few = reqs <= kFewReqs;
+  const int run = few ? (reqs + 31) / 32 : (reqs + kAttendThreads - 1) / kAttendThreads;
   const int lo = min(reqs, (few ? lane : t) * run), hi = min(reqs, lo + run);
-  int mine = 0, mine_units = 0, longest = 0;
+  int mine = 0, mine_units = 0, longest = 0, shortest = INT_MAX;
   bool bad_length = false;
-#pragma unroll 1
-  for (int r = lo; r < hi; ++r) {
+  auto take = [&](int r) {
     const int64_t length = p.lengths[r];
     const int pages = pages_of(p, length);
     mine += pages;
     mine_units += pages > 0;
     longest = max(longest, pages);
+    if (pages > 0) shortest = min(shortest, pages);
     bad_length = bad_length || length < 0 || length > p.max_slots;
+  };
+  if (few) {
+#pragma unroll
+    for (int k = 0; k < kFewReqs / 32; ++k)  // all on their way at once
+      if (lo + k < hi) take(lo + k);
+  } else {
+#pragma unroll 1
+    for (int r = lo; r < hi; ++r) take(r);
   }
   if (bad_length && cta == 0) atomicCAS(p.error, 0u, kErrBadIndex);
-  int before = mine, before_units = mine_units;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, before, d), u = __shfl_up_sync(0xFFFFFFFFu, before_units, d);
-    if (lane >= d) before += o, before_units += u;
-  }
+  int before = warp_inclusive(mine, lane), before_units = warp_inclusive(mine_units, lane);
   longest = __reduce_max_sync(0xFFFFFFFFu, longest);
   int total = __shfl_sync(0xFFFFFFFFu, before, 31), units = __shfl_sync(0xFFFFFFFFu, before_units, 31);
   before -= mine;
@@ -1056,25 +1110,37 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   units *= p.groups;
   // A unit to each CTA, if the longest takes no more than kUndivided pages over
   // an equal share: no parts, nothing to join.
-  const int grid = static_cast<int>(gridDim.x);
-  const bool by_unit = units <= grid && longest <= total / grid + kUndivided;
-  const int ctas = by_unit ? units : min(grid, max(total, 1));
+  int each = longest, own = mine_units, shares = units, finder = 0;
+  bool aligned = units <= grid && longest <= total / grid + kUndivided;
+  if (!aligned && few && units <= grid) {
+    const Shares found = aligned_shares<N>(p, s.scan, lo, hi, total, units, shortest, grid);
+    aligned = found.each > 0;
+    if (aligned) {
+      each = found.each;
+      own = found.own;
+      shares = found.count;
+      finder = found.finder;
+      before_units = found.before;
+    }
+  }
+  const int ctas = aligned ? shares : min(grid, max(total, 1));
   int start = 0, count = 0;
   if (cta < ctas) {
-    start = by_unit ? cta : share_start(total, cta, ctas);
-    count = by_unit ? 1 : share_start(total, cta + 1, ctas) - start;
+    start = aligned ? cta : share_start(total, cta, ctas);
+    count = aligned ? 1 : share_start(total, cta + 1, ctas) - start;
   }
-  const int first = by_unit ? before_units : before, here = by_unit ? mine_units : mine;
-  if (count > 0 && start >= first * p.groups && start < (first + here) * p.groups && (!few || warp == 0)) {
+  const int first = aligned ? before_units : before, here = aligned ? own : mine;
+  if (count > 0 && start >= first * p.groups && start < (first + here) * p.groups && (!few || warp == finder)) {
     int off = start - first * p.groups, r = lo;
 #pragma unroll 1
     for (;; ++r) {
-      const int length = p.lengths[r], pages = pages_of(p, length), size = (by_unit ? pages > 0 : pages) * p.groups;
+      const int length = p.lengths[r], pages = pages_of(p, length);
+      const int of_unit = aligned ? (pages + each - 1) / each : pages, size = of_unit * p.groups;
       if (off < size) {
         s.start[0] = r;
         s.start[1] = length;
-        s.start[2] = by_unit ? off : off / pages;
-        s.start[3] = by_unit ? 0 : off % pages;
+        s.start[2] = off / of_unit;
+        s.start[3] = off % of_unit * (aligned ? each : 1);
         break;
       }
       off -= size;
@@ -1082,24 +1148,27 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   }
   if (t == 0) {
     s.total = total;
+    s.ctas = ctas;
+    s.count = count;
+    s.each = aligned ? each : 0;
     s.rows.heads = 0;
     p.joins[cta] = make_int4(-1, 0, 0, 0);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (count > 0) {
+  if (s.count > 0) {
     Walk w;
     w.req = s.start[0];
     w.length = s.start[1];
     w.group = s.start[2];
     w.page = s.start[3];
     w.pages = pages_of(p, w.length);
-    if (by_unit) count = w.pages;
+    const int count = s.each > 0 ? min(s.each, w.pages - w.page) : s.count;
     w.left = count;
     if (warp < kSoftmaxWarps) {
       more_registers<kSoftmaxRegs>();
-      softmax_role<N>(p, s, w, cta, ctas);
+      softmax_role<N>(p, s, w);
     } else {
       fewer_registers<kOtherRegs>();
       const int worker = 3 * (warp / 4 - 1) + warp % 4;  // of those not on the issuer's scheduler
@@ -1146,56 +1215,42 @@ struct Division {
   __device__ int part(int j) const { return j == 0 ? first : 2 * ((first >> 1) + j); }
 };
 
-// Log-sum-exp (log2) of one head of a divided unit from its parts' (m, l) and
-// its sink, in one pass over the parts; whether one of them is bad.
-__device__ __forceinline__ float unit_lse(const AttendParams& p, int n, const Division& d, int col, int head,
-                                          bool* bad) {
-  float top = p.sinks == nullptr ? -FLT_MAX : fmaxf(p.sinks[head] * kLog2e, -FLT_MAX);
-  float total = p.sinks == nullptr ? 0.f : exp2_fast(p.sinks[head] * kLog2e - top);
-  const int count = d.count();
-  int any = 0;
-#pragma unroll 8
-  for (int j = 0; j < count; ++j) {
-    const float2 ml = p.part_stats[d.part(j) * n + col];
-    any |= p.part_bad[d.part(j)];
-    const float next = fmaxf(top, ml.x);
-    total = total * exp2_fast(top - next) + ml.y * exp2_fast(ml.x - next);
-    top = next;
-  }
-  *bad = any != 0;
-  return total == 0.f ? -INFINITY : top + log2f(total);
-}
-
-// One head of a divided unit: 128 threads with 4 dims each add parts `from`,
-// `from` + `step`, ...  Every warp forms the parts' weights for itself, in `w`.
-// Returns the sum; `scale` and `lse` are what finishes it.
-__device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const Division& d, int col, int head,
+// One head of a divided unit: 4 dims a thread of those at `t`, the sum of parts
+// `from`, `from` + `step`, ...  Every warp forms the parts' weights for itself,
+// in `w`.  Returns the sum; `scale` and `lse` are what finishes it.
+__device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const Division& d, int col, int head, int t,
                                              int from, int step, float* w, float* scale, float* lse, bool* bad) {
-  const int lane = threadIdx.x & 31, t = threadIdx.x & 127, count = d.count();
+  const int lane = threadIdx.x & 31, count = d.count();
   const float4* const parts = reinterpret_cast<const float4*>(p.parts) + col * (kHeadDim / 4) + t;
   const int64_t apart = static_cast<int64_t>(n) * (kHeadDim / 4);
   const float sink = p.sinks == nullptr ? -INFINITY : p.sinks[head] * kLog2e;
-  float top = sink, total = 0.f;
-  bool any_bad = false;
-#pragma unroll 1
-  for (int j = lane; j < count; j += 32) {
-    const float m = p.part_stats[d.part(j) * n + col].x;
-    any_bad = any_bad || p.part_bad[d.part(j)] != 0;
-    w[j] = m;
-    top = fmaxf(top, m);
+  float2 ml[kStatsPerLane];  // all at once: one latency, not one for each
+  int any = 0;
+#pragma unroll
+  for (int k = 0; k < kStatsPerLane; ++k) {
+    const int j = lane + 32 * k;
+    ml[k] = make_float2(-FLT_MAX, 0.f);
+    if (j < count) {
+      ml[k] = p.part_stats[d.part(j) * n + col];
+      any |= p.part_bad[d.part(j)];
+    }
   }
+  float top = sink, total = 0.f;
+#pragma unroll
+  for (int k = 0; k < kStatsPerLane; ++k) top = fmaxf(top, ml[k].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-#pragma unroll 1
-  for (int j = lane; j < count; j += 32) {
-    const float f = exp2_fast(w[j] - top);
-    total += p.part_stats[d.part(j) * n + col].y * f;
-    w[j] = f;
+#pragma unroll
+  for (int k = 0; k < kStatsPerLane; ++k) {
+    if (32 * k >= count) break;
+    const float f = exp2_fast(ml[k].x - top);
+    total += ml[k].y * f;
+    w[lane + 32 * k] = f;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if (p.sinks != nullptr) total += exp2_fast(sink - top);
-  *bad = __any_sync(0xFFFFFFFFu, any_bad);
+  *bad = __any_sync(0xFFFFFFFFu, any != 0);
   *scale = total == 0.f ? 0.f : 1.f / total;
   *lse = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
   __syncwarp();
@@ -1213,6 +1268,31 @@ __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const
   return acc;
 }
 
+// Log-sum-exp (log2) of one head of a divided unit, by `with` threads of a warp.
+__device__ __forceinline__ float unit_lse(const AttendParams& p, int n, const Division& d, int col, int head,
+                                          int first, int with, int* skip) {
+  const uint32_t who = 0xFFFFFFFFu >> (32 - with) << (threadIdx.x & 31 & ~(with - 1));
+  float top = p.sinks == nullptr ? -FLT_MAX : fmaxf(p.sinks[head] * kLog2e, -FLT_MAX);
+  float total = p.sinks == nullptr || first != 0 ? 0.f : exp2_fast(p.sinks[head] * kLog2e - top);
+  const int count = d.count();
+  int any = 0;
+#pragma unroll 8
+  for (int j = first; j < count; j += with) {
+    const float2 ml = p.part_stats[d.part(j) * n + col];
+    any |= p.part_bad[d.part(j)];
+    const float next = fmaxf(top, ml.x);
+    total = total * exp2_fast(top - next) + ml.y * exp2_fast(ml.x - next);
+    top = next;
+  }
+  for (int o = with / 2; o > 0; o >>= 1) {
+    const float other = __shfl_xor_sync(who, top, o), sum = __shfl_xor_sync(who, total, o), next = fmaxf(top, other);
+    total = total * exp2_fast(top - next) + sum * exp2_fast(other - next);
+    top = next;
+  }
+  if (any) *skip = 1;
+  return total == 0.f ? -INFINITY : top + log2f(total);
+}
+
 __device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row, int t, float4 v, float f, float lse) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * f, v.y * f);
   const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * f, v.w * f);
@@ -1222,14 +1302,16 @@ __device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row,
 }
 
 // Joins the divided units, zeroes the rows without slots, forms the weights.
-// An item is a head of a divided unit: one of 128 threads' work if that fills
-// the grid, else the whole CTA's, its four groups a quarter of the parts each.
+// An item is a head of a divided unit, 128 threads' work if that fills the grid.
+// Else it is a CTA's, whose four groups of 128 take a quarter of the parts each,
+// or, where that leaves CTAs without work, 2 or 4 CTAs', each for a part of the
+// dims and with as many more groups.
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_kernel(const __grid_constant__ AttendParams p,
                                                                         int n, int ctas, int weight_ctas) {
   __shared__ int4 joins[kAttendCtas];
   __shared__ int warp_joins[kJoinThreads / 32];
-  __shared__ float4 quarters[3][128];
-  __shared__ float part_weights[kJoinThreads / 32][kAttendCtas];
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ float part_weights[kJoinThreads / 32][32 * kStatsPerLane];
   __shared__ __align__(16) float total[2 * 64];
   __shared__ int skip;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1249,23 +1331,26 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   }
   if (mine.x >= 0) joins[before] = mine;
   __syncthreads();
-  const int items = divided * p.group_heads, grid = static_cast<int>(gridDim.x), group = t >> 7;
-  const bool apart = items >= 2 * grid;  // an item to each 128 threads
+  const int heads = divided * p.group_heads, grid = static_cast<int>(gridDim.x);
+  const bool apart = heads >= 2 * grid;  // a head to each 128 threads
+  const int cuts = 4 * heads <= grid ? 4 : 2 * heads <= grid ? 2 : 1, size = 128 / cuts;
+  const int group = t / size, groups = kJoinThreads / size, items = heads * cuts;
   for (int item = apart ? 4 * static_cast<int>(blockIdx.x) + group : static_cast<int>(blockIdx.x); item < items;
        item += apart ? 4 * grid : grid) {
-    const int4 join = joins[item / p.group_heads];
-    const int col = item % p.group_heads, head = join.y * p.group_heads + col;
+    const int unit = item / cuts, at = item % cuts * size + t % size;
+    const int4 join = joins[unit / p.group_heads];
+    const int col = unit % p.group_heads, head = join.y * p.group_heads + col;
     if (head >= p.num_heads) continue;
     float f, lse;
     bool bad;
-    float4 v = join_parts(p, n, Division{join.z, join.w}, col, head, apart ? 0 : group, apart ? 1 : 4,
+    float4 v = join_parts(p, n, Division{join.z, join.w}, col, head, at, apart ? 0 : group, apart ? 1 : groups,
                           part_weights[warp], &f, &lse, &bad);
     if (!apart) {
-      if (group > 0) quarters[group - 1][t & 127] = v;
+      sums[t] = v;
       __syncthreads();
       if (group == 0) {
-        for (int g = 0; g < 3; ++g) {
-          const float4 o = quarters[g][t];
+        for (int g = 1; g < groups; ++g) {
+          const float4 o = sums[g * size + t];
           v.x += o.x;
           v.y += o.y;
           v.z += o.z;
@@ -1275,7 +1360,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
       __syncthreads();
     }
     if (!bad && (apart || group == 0))
-      store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, t & 127, v, f, lse);
+      store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, at, v, f, lse);
   }
   // requests: `weight_ctas` CTAs for each
   for (int item = blockIdx.x; item < p.num_reqs * weight_ctas; item += grid) {
@@ -1291,7 +1376,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
     // the heads' log2-sum-exp, by column of the scores; +inf where there is no head or no key
     if (t == 0) skip = 0;
     __syncthreads();
-    for (int col = t; col < p.score_cols; col += kJoinThreads) {
+    {
+      // a column to each kJoinThreads / score_cols threads (4 .. 32), which share its parts
+      const int with = kJoinThreads / static_cast<int>(p.score_cols), col = t / with, first = t % with;
       const int unit = col / n, c = col % n, head = unit * p.group_heads + c;
       float v = INFINITY;
       if (c < p.group_heads && head < p.num_heads) {
@@ -1300,13 +1387,11 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
           if (parts.y) skip = 1;
           v = p.lse[static_cast<int64_t>(r) * p.num_heads + head] * kLog2e;
         } else {
-          bool bad;
-          v = unit_lse(p, n, Division{parts.x, parts.y}, c, head, &bad);
-          if (bad) skip = 1;
+          v = unit_lse(p, n, Division{parts.x, parts.y}, c, head, first, with, &skip);
         }
         if (v == -INFINITY) v = INFINITY;
       }
-      total[col] = v;
+      if (first == 0) total[col] = v;
     }
     __syncthreads();
     if (!skip) {
@@ -1360,7 +1445,7 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   int64_t weight_ctas = 2 * kMost / p.num_reqs;
   weight_ctas = weight_ctas > chunks ? chunks : weight_ctas;
   weight_ctas = weight_ctas < 1 ? 1 : weight_ctas;
-  const int64_t joins = static_cast<int64_t>(ctas) * p.group_heads, items = p.num_reqs * weight_ctas;
+  const int64_t joins = 4 * static_cast<int64_t>(ctas) * p.group_heads, items = p.num_reqs * weight_ctas;
   const int64_t work = joins > items ? joins : items;
   cfg.gridDim = dim3(static_cast<unsigned>(work < kMost ? work : kMost));
   cfg.blockDim = dim3(kJoinThreads);

@@ -456,3 +456,14 @@ def test_short_requests_beside_empty_ones(kvc, lengths, H, sinks):
     _, kv, table, n, q, s = _case(77, lengths, H, sinks=sinks)
     _compare(kvc, kv, table, n, q, s)
     _compare(kvc, kv, table, n, q, s, flags=1)
+
+
+@pytest.mark.parametrize("H", [8, 24, 64])
+@pytest.mark.parametrize("R,top,flags", [(5, 3000, 0), (5, 3000, 9), (20, 1500, 0), (20, 1500, 33), (40, 900, 0), (40, 900, 61),
+                                         (100, 700, 0), (160, 300, 0), (161, 300, 0)])
+def test_ragged_batches(kvc, R, top, flags, H):
+    rng = np.random.default_rng(R + top)
+    lengths = rng.integers(0, top + 1, R).tolist()
+    lengths[R // 2], lengths[-1] = 0, top
+    _, kv, table, n, q, s = _case(31, lengths, H, sinks=True)
+    _compare(kvc, kv, table, n, q, s, weights=True, flags=flags)
