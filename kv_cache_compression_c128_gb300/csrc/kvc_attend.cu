@@ -29,24 +29,29 @@
 // through a ring: 24 KB (N 64) or 56 KB stay on their way whatever the decode
 // does.  (Plain loads kept some 14 KB on the way, for the cache that they pass
 // through is what shared memory leaves of it: 193 us on 64 requests x 8192 slots
-// x 64 heads where the ring takes 123.)
+// x 64 heads where the ring takes 125.)
 //
-// The pages of all (request, head group) units are laid end to end and cut into
-// equal shares, one per CTA; a unit that a cut divides leaves its parts (m, l, O)
-// in the workspace, and a second kernel joins them in the order of the shares, so
-// the same lengths give the same bits.  That kernel also forms the slots' weights,
-// from the scores that the first one left behind.
+// The (request, head group) units are cut into shares of pages, one per CTA: a
+// unit to each where the longest takes hardly more than an equal share; else
+// shares that begin anew with every unit; else all units' pages laid end to end
+// and cut into equal shares.  The rule sees the lengths, on the device.  A unit
+// that is divided leaves its parts (m, l, O) in the workspace, and a second kernel
+// joins them in the order of the shares, so the same lengths give the same bits.
+// That kernel also forms the slots' weights, from the scores that the first one
+// left behind.
 //
 // What bounds it: a page's products take 1792 cycles at N = 64 and 1380 at 16,
 // all of them operand reads from shared memory at 128 bytes a cycle (measured
 // alone: 32 and 48 cycles for the M 64 and M 128 instruction at N 64, 23.5 and 39
 // at N 16).  The decode's stores and loads of the same memory add some 1000, and a
-// page takes about 4000 in all (2.1 us; 64 requests x 8192 slots x 64 heads: 123
-// us, 2.5 TB/s and 0.56 PFLOP/s): beside the products every other access of
+// page takes about 4000 in all (2.1 us; 64 requests x 8192 slots x 64 heads: 125
+// us, 2.5 TB/s and 0.55 PFLOP/s): beside the products every other access of
 // shared memory is slow, a barrier's question 250 to 450 cycles.  Hence few
-// questions, one short issuing loop, rolled loops throughout (straight code of
-// every role does not stay in the instruction cache: 180 us unrolled), and no
-// more places than one for each decoding warp.
+// questions, one short issuing loop, rolled loops throughout (180 us with straight
+// code in every role, which does not stay in the instruction cache), and no more
+// places than one for each decoding warp.  Small calls are bound by latency: 64
+// slots of one request take 9 us, lengths, page ids, codes, two products and the
+// rows one after the other.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -70,9 +75,8 @@ using dev::smem_addr;
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-// Every fourth warp shares a scheduler and its instruction cache: the products'
-// issuer sits with the two copying warps, apart from the decode, whose long
-// loop body would push its short one out.
+// Every fourth warp shares a scheduler: the products' issuer sits with the two
+// copying warps, which mostly wait, apart from the decode and its long loop.
 constexpr int kIssueWarp = 7, kCopyWarp = 11, kQueryWarp = 15;
 constexpr int kAttendThreads = 16 * 32;
 // Registers of a thread by group of four warps: 512 x 128 at launch, shared
@@ -91,11 +95,12 @@ constexpr int kInfos = 8;
 // Pages by which the longest unit may exceed an equal share before units are
 // divided: joining the parts costs about as much as this many pages.
 constexpr int kUndivided = 3;
-constexpr int kFewReqs = 160;  // more are never shared out by units: there are fewer CTAs
+// Requests at most for which shares begin anew with every unit (152 CTAs take no
+// more units; a run of five requests a lane).
+constexpr int kFewReqs = 160;
 constexpr float kRescaleAbove = 32.f;                   // log2
 constexpr int kJoinThreads = kAttendThreads, kJoinCtasPerSm = 2;
 constexpr int kStatsPerLane = (kAttendCtas + 31) / 32;  // of a unit's parts
-constexpr int kWeightSlots = 64;                        // slots at least for a CTA that forms weights
 
 // Groups of a page whose codes come through the ring, one warp and depth()
 // places each.  At N = 64 the 227 KB leave six places: the seventh group's warp
@@ -630,9 +635,9 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) 
 // The products of every page: whatever can be issued next, a page's second
 // product, which frees the place of the page after next, before a half of the
 // next page's first.  The whole warp walks, one elected thread issues.  One
-// short loop: the two questions
-// travel together and behind products already queued, and every role's code has
-// to stay in the instruction cache beside the others'.
+// short loop: the questions travel together and behind products already queued,
+// and every role's code has to stay in the instruction cache beside the others'.
+// (Questions by one lane instead of all: 137 us where this takes 125.)
 template <int N>
 __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count) {
   constexpr uint32_t kFirst = instruction(64, N, false), kSecond = instruction(128, N, true);
@@ -1439,10 +1444,11 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N>, p);
   if (e != cudaSuccess || p.alone) return e;
-  // as many as fit at once: they share the divided units' heads, then the requests
+  // as many as fit at once: they share the divided units' heads, then the requests,
+  // one turn each (24 requests of up to 2050 slots, 32 heads: 23.1 us, in two turns 26.4)
   constexpr int kMost = kJoinCtasPerSm * kAttendCtas;
-  const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kWeightSlots - 1) / kWeightSlots;
-  int64_t weight_ctas = 2 * kMost / p.num_reqs;
+  const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage;
+  int64_t weight_ctas = kMost / p.num_reqs;
   weight_ctas = weight_ctas > chunks ? chunks : weight_ctas;
   weight_ctas = weight_ctas < 1 ? 1 : weight_ctas;
   const int64_t joins = 4 * static_cast<int64_t>(ctas) * p.group_heads, items = p.num_reqs * weight_ctas;

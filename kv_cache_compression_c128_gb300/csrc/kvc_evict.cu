@@ -465,11 +465,7 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const _
   }
 }
 
-}  // namespace
-
-namespace {
-
-// Sets a kernel's shared memory once per context and launches it.
+// Launches a kernel that waits for the one ahead of it on the stream by itself.
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, dim3 grid, int threads, size_t smem, const EvictParams& p, cudaStream_t stream) {
   if (smem > 48 * 1024) {
