@@ -467,3 +467,20 @@ def test_ragged_batches(kvc, R, top, flags, H):
     lengths[R // 2], lengths[-1] = 0, top
     _, kv, table, n, q, s = _case(31, lengths, H, sinks=True)
     _compare(kvc, kv, table, n, q, s, weights=True, flags=flags)
+
+
+def test_calls_on_several_streams_at_once(kvc):
+    cases = [_case(5, [1500, 3, 0, 900, 2000], 64, sinks=True), _case(6, list(range(0, 700, 9)), 8), _case(7, [8000], 128)]
+    cuda = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    given = [(q.cuda(), cuda(kv), cuda(table), cuda(n), cuda(s)) for _, kv, table, n, q, s in cases]
+    alone = [kvc.attend(q, kv, table, n, sinks=s) for q, kv, table, n, s in given]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in given]
+    got = []
+    for _ in range(30):
+        got.append([kvc.attend(q, kv, table, n, sinks=s, stream=stream) for (q, kv, table, n, s), stream in zip(given, streams)])
+    torch.cuda.synchronize()
+    assert _error(kvc) == 0
+    for turn in got:
+        for (out, lse), (want, want_lse) in zip(turn, alone):
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, want_lse)
