@@ -1260,7 +1260,7 @@ __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const
   *lse = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
   __syncwarp();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
   for (int j = from; j < count; j += step) {
     const float f = w[j];
     const float4 o = parts[d.part(j) * apart];
