@@ -1445,7 +1445,7 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N>, p);
   if (e != cudaSuccess || p.alone) return e;
   // as many as fit at once: they share the divided units' heads, then the requests,
-  // one turn each (24 requests of up to 2050 slots, 32 heads: 23.1 us, in two turns 26.4)
+  // one turn each (24 requests of up to 2050 slots, 32 heads: 22.6 us, in two turns 3 more)
   constexpr int kMost = kJoinCtasPerSm * kAttendCtas;
   const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage;
   int64_t weight_ctas = kMost / p.num_reqs;
