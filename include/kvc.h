@@ -302,8 +302,10 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
  *   slot_weights[r, n] = slot_weights_in[r, n] + sum_h exp(s_n - L_h)
  * A row that sees no key (length 0 or every score -inf, and no sink) is zeros
  * with lse -inf and adds nothing to the weights.  Scores, sums and results
- * are formed in fp32; the softmax weights are rounded to bf16 for the product
- * with the values, and out to bf16 at the end.
+ * are formed in fp32, scores and sinks in powers of two (beyond 2.3e38, where
+ * s_n * log2(e) leaves the range, they count as infinite); the softmax weights
+ * are rounded to bf16 for the product with the values, and out to bf16 at the
+ * end.
  *
  * q            bf16, head h of request r at q + r * q_req_stride + h *
  *              q_head_stride (elements, multiples of 8; a request stride of 0

@@ -813,7 +813,6 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t tmem = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const float c = p.scale == 0.f ? 1.f : p.scale * kLog2e;  // scores of scale 0 are zeros
-  const uint32_t behind = c < 0.f ? 0x7F800000u : 0xFF800000u;  // times c: -inf
   const int row = warp * 16 + (lane >> 2);
   const int cta = blockIdx.x;
   int i = 0, at = share_start(s.total, cta, s.ctas);  // (used with equal shares)
@@ -830,6 +829,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
       ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit));
       tc_fence_after();
       uint32_t v[2 * kCols];
+      float x[2 * kCols];  // scores in powers of two
 #pragma unroll
       for (int j = 0; j < N / 16; ++j) tmem_ld_16x16(tmem + 4 * N + stage * N + 16 * j, v + 8 * j);
       tmem_wait_ld();
@@ -839,28 +839,31 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
 #pragma unroll
         for (int j = 0; j < 2 * kCols; ++j) v[j] = 0;
       }
+      // Rounded once, before anything is subtracted: the reference is one of
+      // these numbers, and the largest score's distance from it has to be 0
+      // (v c - ref in one step keeps what rounding took from the reference:
+      // from |v c| of 2^31 on more than the 126 after which exp2 is 0 or
+      // infinite, and the row was zeros or NaN).
+#pragma unroll
+      for (int j = 0; j < 2 * kCols; ++j) x[j] = __fmul_rn(__uint_as_float(v[j]), c);
       if (__builtin_expect(valid < kSlotsPerPage, 0)) {  // slots behind the request's last one
 #pragma unroll
         for (int j = 0; j < 2 * kCols; ++j)
-          if (!((j & 2) ? in1 : in0)) v[j] = behind;
+          if (!((j & 2) ? in1 : in0)) x[j] = -INFINITY;
       }
       if (__builtin_expect(p.scores != nullptr, 0)) {
         float* dst = p.scores + ((w.req * p.max_pages + w.page + pg) * kSlotsPerPage + row) * p.score_cols +
                      w.group * N + 2 * (lane & 3);
 #pragma unroll
         for (int j = 0; j < N / 8; ++j) {
-          if (in0)
-            *reinterpret_cast<float2*>(dst + 8 * j) =
-                make_float2(__uint_as_float(v[4 * j]) * c, __uint_as_float(v[4 * j + 1]) * c);
-          if (in1)
-            *reinterpret_cast<float2*>(dst + 8 * p.score_cols + 8 * j) =
-                make_float2(__uint_as_float(v[4 * j + 2]) * c, __uint_as_float(v[4 * j + 3]) * c);
+          if (in0) *reinterpret_cast<float2*>(dst + 8 * j) = make_float2(x[4 * j], x[4 * j + 1]);
+          if (in1) *reinterpret_cast<float2*>(dst + 8 * p.score_cols + 8 * j) = make_float2(x[4 * j + 2], x[4 * j + 3]);
         }
       }
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 2 * kCols; ++j)
-        top = fmaxf(top, fmaf(__uint_as_float(v[j]), c, -ref[(j >> 2) * 2 + (j & 1)]));
+        top = fmaxf(top, __fsub_rn(x[j], ref[(j >> 2) * 2 + (j & 1)]));
       if (__builtin_expect(softmax_any(top > kRescaleAbove || !ok), 0)) {
         if (softmax_any(!ok)) {
           s.abort = 1;
@@ -869,8 +872,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
         // the columns' maxima over the page
         float m[kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
-          m[j] = fmaxf(__uint_as_float(v[4 * (j >> 1) + (j & 1)]) * c, __uint_as_float(v[4 * (j >> 1) + 2 + (j & 1)]) * c);
+        for (int j = 0; j < kCols; ++j) m[j] = fmaxf(x[4 * (j >> 1) + (j & 1)], x[4 * (j >> 1) + 2 + (j & 1)]);
         combine_rows(m, lane, [](float a, float b) { return fmaxf(a, b); });
         store_combined(m, lane, s.red[warp]);
         softmax_sync();
@@ -905,8 +907,8 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {  // columns of j / 2, rows of j % 2
         const int col = j & ~1;
-        const float a = exp2_fast(fmaf(__uint_as_float(v[2 * j]), c, -ref[col]));
-        const float b = exp2_fast(fmaf(__uint_as_float(v[2 * j + 1]), c, -ref[col + 1]));
+        const float a = exp2_fast(__fsub_rn(x[2 * j], ref[col]));
+        const float b = exp2_fast(__fsub_rn(x[2 * j + 1], ref[col + 1]));
         sum[col] += a;
         sum[col + 1] += b;
         pair[j] = __floats2bfloat162_rn(a, b);

@@ -1,0 +1,85 @@
+"""kvc.attend at the ends of the fp32 range: scores far beyond what a difference resolves."""
+import numpy as np
+import pytest
+import torch
+
+import slots_testlib as plain
+from kvc_testlib import PAGE_BYTES, SCALE_BASE, SCALE_DIM, TOKEN_STRIDE
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvc():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import kv_cache_compression_c128_gb300 as kvc
+
+    kvc.build()
+    return kvc
+
+
+def _error(kvc):
+    return kvc.kvc_get_device_error(torch.cuda.current_stream().cuda_stream)
+
+
+def _cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _equal_slots(rng, first):
+    """A page of 64 equal slots whose dim 0 is `first` (scale byte 127: 2^0)."""
+    kv = plain.random_cache(rng, 1)
+    rows, scales = kv[0, :SCALE_BASE].reshape(64, TOKEN_STRIDE), kv[0, SCALE_BASE:].reshape(64, SCALE_DIM)
+    rows[:], scales[:] = rows[0], scales[0]
+    rows[:, 0], scales[:, 0] = np.int8(first).view(np.uint8), 127
+    return kv
+
+
+def _one_score(rng, H, size):
+    """Queries that are zero but for dim 0: `size` to twice that in bf16, each head its own."""
+    q = torch.zeros((1, H, 512))
+    q[0, :, 0] = torch.from_numpy((size * (1 + rng.random(H))).astype(np.float32))
+    return q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("size", [1e5, 2.0 ** 31, 3e9, 1e10, 1e20, 1e30, 1e37, -1e5, -(2.0 ** 31), -3e9, -1e10, -1e20, -1e37])
+@pytest.mark.parametrize("n,flags", [(1, 0), (2, 0), (64, 0), (200, 1), (3000, 0), (3000, 7)])
+def test_equal_slots_of_large_scores(kvc, n, flags, size):
+    # Every weight is 2^0 before the division, the sums n and n k_d are whole
+    # numbers of units that fp32 holds (8 bits of k_d, 12 of n), and the
+    # quotient is k_d again once rounded to bf16.
+    rng = np.random.default_rng(n)
+    kv = _equal_slots(rng, 1)
+    q = _one_score(rng, 40, size)
+    table = torch.zeros((1, -(-n // 64)), dtype=torch.int32, device="cuda")
+    scale = float(np.float32(0.7))
+    out, lse = kvc.attend(q.cuda(), _cuda(kv), table, torch.tensor([n], dtype=torch.int32, device="cuda"), scale, flags=flags)
+    assert _error(kvc) == 0
+    slot = plain.slot_vectors(kv, np.zeros(1, np.int64), 1)[0]
+    assert np.array_equal(out.double().cpu().numpy(), np.broadcast_to(slot, (1, 40, 512)))
+    # scale log2(e), its product with the dot product, + log2(n), / log2(e): half a step each
+    # (log2(e) itself is the same fp32 number both times), and the steps of log2(n)
+    want = scale * q[0, :, 0].double().numpy() + np.log(n)
+    off = np.abs(lse[0].double().cpu().numpy() - want)
+    assert (off <= 2.5 * plain.STEP_F32 * np.abs(want) + 2.0 ** -19).all(), off
+
+
+@pytest.mark.parametrize("size", [1e10, -1e10, 1e20, -1e20, 1e35])
+@pytest.mark.parametrize("n", [2, 130, 900])
+def test_the_largest_of_large_scores_takes_all(kvc, n, size):
+    rng = np.random.default_rng(n)
+    best = n - 1 if size > 0 else 0
+    kv = np.concatenate([_equal_slots(rng, 3)] * -(-n // 64))
+    one = plain.random_cache(rng, 1)[0]
+    page, at = divmod(best, 64)
+    kv[page, at * TOKEN_STRIDE:(at + 1) * TOKEN_STRIDE] = one[:TOKEN_STRIDE]
+    kv[page, at * TOKEN_STRIDE] = 4 if size > 0 else 2
+    table = np.arange(len(kv), dtype=np.int32)[None]
+    q = _one_score(rng, 64, size)
+    out, lse = kvc.attend(q.cuda(), _cuda(kv), _cuda(table), torch.tensor([n], dtype=torch.int32, device="cuda"), 1.0)
+    assert _error(kvc) == 0
+    slot = plain.slot_vectors(kv, table[0], n)[best]
+    assert np.array_equal(out.double().cpu().numpy(), np.broadcast_to(slot, (1, 64, 512)))
+    want = slot[0] * q[0, :, 0].double().numpy()
+    assert (np.abs(lse[0].double().cpu().numpy() - want) <= 2.5 * plain.STEP_F32 * np.abs(want)).all()
