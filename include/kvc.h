@@ -340,9 +340,10 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
  * most 65535, num_kv_pages and num_reqs * max_pages_per_req * ceil(num_heads /
  * 64) below 2^31.  A pipeline wait that runs past its limit records
  * KVC_ERR_TIMEOUT; the call's rows and weights are then partly as they were.
- * Slots that hold infinities or NaN give what the sums above give, and so do
- * slots so large that their sum (each times exp(s_n - max), before the division)
- * leaves the fp32 range.  Allocates nothing.
+ * Slots that hold infinities or NaN give what the sums above give.  Finite
+ * slots give finite rows as long as the |k_n| of a request's slots sum up to less
+ * than 2^127 in every dim, whatever their scores; beyond that a sum may leave
+ * the fp32 range before it is divided.  Allocates nothing.
  */
 size_t kvc_attend_workspace_bytes(int64_t num_reqs, int32_t num_heads, int64_t max_pages_per_req,
                                   int32_t with_slot_weights);

@@ -21,7 +21,8 @@
 // P = 2^(s - m) goes to shared memory in bf16: its rounding is of the size of
 // the output's own, and the sum l that divides is taken before it.  m is a
 // column's reference, not its running maximum: any m serves as long as 2^(s - m)
-// stays in range, so O is rescaled only where a score exceeds m by 2^32.
+// and its products stay in range, so O is rescaled only where a score exceeds m
+// by 32, or at all on a page that holds values beyond 2^64.
 //
 // Warps of a CTA: 0..3 softmax and epilogue, one issues the products, one copies
 // the codes, one the queries, seven decode, one brings the RoPE words.  The codes
@@ -99,6 +100,11 @@ constexpr int kUndivided = 3;
 // more units; a run of five requests a lane).
 constexpr int kFewReqs = 160;
 constexpr float kRescaleAbove = 32.f;                   // log2
+// A page is large if a scale byte of it is above this, or a RoPE word not below
+// 2^65: all others' values are below 2^65, and 2^30 slots (more than a request
+// can have) of them times 2^32 stay in range.  On a large page the reference
+// follows the maximum, so that no value is multiplied by more than 1.
+constexpr uint32_t kLargeScale = 184;                   // 128 x 2^(184 - 127) = 2^64
 constexpr int kJoinThreads = kAttendThreads, kJoinCtasPerSm = 2;
 constexpr int kStatsPerLane = (kAttendCtas + 31) / 32;  // of a unit's parts
 
@@ -159,6 +165,7 @@ struct AttendShared {
   Barriers<N> bar;
   PageInfo info[kInfos];
   uint8_t bad[8];  // of the last segments: a page was outside the cache
+  uint8_t large[kInfos];  // of the pages in info
   int count, ctas, total, each;  // pages in all, and of a share that begins anew with every unit (0: equal shares)
   int start[4];  // request, length, unit and page of the share's first page
   Rows rows;     // of the last segment
@@ -399,6 +406,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// The larger magnitudes (with some sign).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -458,6 +471,7 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
         }
         const int valid = there ? min(kSlotsPerPage, w.length - (w.page + pg) * kSlotsPerPage) : 0;
         s.info[i % kInfos] = PageInfo{id, static_cast<int16_t>(valid), static_cast<int16_t>(pg + 1 == count)};
+        s.large[i % kInfos] = 0;
         dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], kScaleBytes);
         copy_bytes(s.scales[i % kScales], p.kv_cache + id * kPageBytes + kScaleBase, kScaleBytes,
                    &s.bar.info_full[i % kInfos]);
@@ -512,9 +526,10 @@ __device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
   }
 }
 
-// Eight times 16 codes and their scale bytes as 16 bf16.
+// Eight times 16 codes and their scale bytes as 16 bf16; sets *large if a scale
+// byte is.
 __device__ __forceinline__ void decode_rows(const uint4 (&raw)[8], const uint32_t (&scale)[8], uint4 (&lo)[8],
-                                            uint4 (&hi)[8]) {
+                                            uint4 (&hi)[8], uint8_t* large) {
   uint32_t most = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -525,7 +540,8 @@ __device__ __forceinline__ void decode_rows(const uint4 (&raw)[8], const uint32_
     decode4_bf16(raw[j].z, up, less, &hi[j].x, &hi[j].y);
     decode4_bf16(raw[j].w, up, less, &hi[j].z, &hi[j].w);
   }
-  if (__builtin_expect(__any_sync(0xFFFFFFFFu, most > 247u), 0)) {
+  if (__builtin_expect(__any_sync(0xFFFFFFFFu, most > kLargeScale), 0)) {
+    *large = 1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t more = (127u + max(scale[j], 247u) - 247u) * 0x00800080u;  // 2^(b - 247)
@@ -583,7 +599,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
     }
     // decoded before its place is free, so that only the stores are left then
     uint4 lo[8], hi[8];
-    decode_rows(raw, scale, lo, hi);
+    decode_rows(raw, scale, lo, hi, &s.large[i % kInfos]);
     if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit);
     if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
       s.abort = 1;
@@ -626,6 +642,20 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) 
 #pragma unroll
     for (int j = 0; j < 16; ++j)
       *reinterpret_cast<uint4*>(block + 512 * j + ((c ^ (r + 4 * (j & 1))) << 4)) = v[j];
+    // While the stores are on their way (before them: 128 requests x 1000 slots
+    // x 8 heads 38.3 us instead of 37.9), the largest word: an exponent's two
+    // highest bits are set from 2^65 on.  (A NaN is passed over; its slot's
+    // scores are NaN.)
+    uint32_t most[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      most[0] = max_abs_bf16x2(most[0], v[j].x);
+      most[1] = max_abs_bf16x2(most[1], v[j].y);
+      most[2] = max_abs_bf16x2(most[2], v[j].z);
+      most[3] = max_abs_bf16x2(most[3], v[j].w);
+    }
+    const uint32_t top = max_abs_bf16x2(max_abs_bf16x2(most[0], most[1]), max_abs_bf16x2(most[2], most[3]));
+    if (top & top << 1 & 0x40004000u) s.large[i % kInfos] = 1;
     fence_async_shared();
     __syncwarp();
     if (lane == 0) dev::mbar_arrive(&s.bar.half_full[stage][1]);
@@ -828,6 +858,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
       const int stage = i & 1;
       ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit));
       tc_fence_after();
+      const float above = s.large[i % kInfos] ? 0.f : kRescaleAbove;
       uint32_t v[2 * kCols];
       float x[2 * kCols];  // scores in powers of two
 #pragma unroll
@@ -864,7 +895,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
 #pragma unroll
       for (int j = 0; j < 2 * kCols; ++j)
         top = fmaxf(top, __fsub_rn(x[j], ref[(j >> 2) * 2 + (j & 1)]));
-      if (__builtin_expect(softmax_any(top > kRescaleAbove || !ok), 0)) {
+      if (__builtin_expect(softmax_any(top > above || !ok), 0)) {
         if (softmax_any(!ok)) {
           s.abort = 1;
           return;

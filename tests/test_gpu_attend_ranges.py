@@ -83,3 +83,47 @@ def test_the_largest_of_large_scores_takes_all(kvc, n, size):
     assert np.array_equal(out.double().cpu().numpy(), np.broadcast_to(slot, (1, 64, 512)))
     want = slot[0] * q[0, :, 0].double().numpy()
     assert (np.abs(lse[0].double().cpu().numpy() - want) <= 2.5 * plain.STEP_F32 * np.abs(want)).all()
+
+
+def _rising(rng, pages, rise, where, large):
+    """Pages of slots that a query of 1 in dim 448 scores 0, rise, 2 rise, ...
+    (in nats, before the slots' own spread of 1), whose values in the pages
+    `large` reach 2^112: as codes (where "codes") or as RoPE words ("rope")."""
+    kv = plain.random_cache(rng, pages)
+    rows = kv[:, :SCALE_BASE].reshape(pages, 64, TOKEN_STRIDE)
+    scales = kv[:, SCALE_BASE:].reshape(pages, 64, SCALE_DIM)
+    words = np.ascontiguousarray(rows[..., 448:]).view("<u2").reshape(pages, 64, 64).copy()
+    bits = lambda x: (np.asarray(x, np.float32).view(np.uint32) >> 16).astype("<u2")
+    if where == "codes":
+        scales[large, :, :7] = rng.integers(222, 233, scales[large, :, :7].shape, dtype=np.uint8)  # 2^95 .. 2^105
+    else:
+        words[large, :, 1:] = bits(rng.standard_normal((len(large), 64, 63)) * 2.0 ** rng.integers(95, 110, (len(large), 64, 63)))
+    words[..., 0] = bits(rise * np.arange(pages)[:, None] + rng.random((pages, 64)))
+    rows[..., 448:] = words.view(np.uint8).reshape(pages, 64, 128)
+    return kv
+
+
+@pytest.mark.parametrize("where", ["codes", "rope"])
+@pytest.mark.parametrize("H,n,rise,large,flags", [
+    (8, 128, 20.0, [0, 1], 1), (64, 128, 20.0, [1], 1), (24, 200, 9.0, [0, 3], 0), (64, 64 * 12 - 5, 7.0, list(range(12)), 1),
+    (16, 64 * 12 - 5, 20.0, [4, 5, 11], 2), (100, 64 * 12 - 5, -20.0, list(range(12)), 5), (64, 2500, 3.0, [10, 20, 39], 3),
+    (32, 2500, 0.0, list(range(40)), 0)])
+def test_values_near_the_end_of_the_range(kvc, where, H, n, rise, large, flags):
+    # Scores that rise by less than 2^32 (in weight) from page to page, under
+    # values whose sum stays in range: 40 pages of 64 values below 2^115 are
+    # below 2^127, and so is every sum of them times weights of at most 1.
+    rng = np.random.default_rng(H + n)
+    kv = _rising(rng, -(-n // 64), rise, where, large)
+    table = rng.permutation(len(kv)).astype(np.int32)[None]
+    kv[table[0]] = kv.copy()
+    q = torch.zeros((1, H, 512))
+    q[0, :, 448] = torch.from_numpy(rng.choice([-1.0, 0.5, 1.0, 1.0, 1.0625], H).astype(np.float32))
+    q = q.to(torch.bfloat16)
+    lengths = np.array([n], np.int32)
+    want = plain.attend(q.double().numpy(), kv, table, lengths, 1.0)
+    out, lse = kvc.attend(q.cuda(), _cuda(kv), _cuda(table), _cuda(lengths), 1.0, flags=flags)
+    assert _error(kvc) == 0
+    off = np.abs(out.double().cpu().numpy() - want[0])
+    assert np.isfinite(off).all()
+    assert (off <= want[3]).all()
+    assert (np.abs(lse.double().cpu().numpy() - want[1]) <= want[4]).all()
