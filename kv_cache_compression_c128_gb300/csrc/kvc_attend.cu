@@ -983,6 +983,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
           total = l * f + exp2_fast(sink - top);
         }
         if (!bad) p.lse[row0 + t] = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
+        if (p.row_stats != nullptr) p.row_stats[row0 + t] = make_float2(top, total == 0.f ? 0.f : 1.f / total);
         f = total == 0.f ? 0.f : f / total;
       } else {
         p.part_stats[part * N + t] = make_float2(m, l);
@@ -1306,9 +1307,10 @@ __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const
   return acc;
 }
 
-// Log-sum-exp (log2) of one head of a divided unit, by `with` threads of a warp.
-__device__ __forceinline__ float unit_lse(const AttendParams& p, int n, const Division& d, int col, int head,
-                                          int first, int with, int* skip) {
+// What the weights of one head of a divided unit are formed with, by `with`
+// threads of a warp: the reference (log2) and 1 / sum, 0 where there is no key.
+__device__ __forceinline__ float2 unit_stats(const AttendParams& p, int n, const Division& d, int col, int head,
+                                             int first, int with, int* skip) {
   const uint32_t who = 0xFFFFFFFFu >> (32 - with) << (threadIdx.x & 31 & ~(with - 1));
   float top = p.sinks == nullptr ? -FLT_MAX : fmaxf(p.sinks[head] * kLog2e, -FLT_MAX);
   float total = p.sinks == nullptr || first != 0 ? 0.f : exp2_fast(p.sinks[head] * kLog2e - top);
@@ -1328,7 +1330,7 @@ __device__ __forceinline__ float unit_lse(const AttendParams& p, int n, const Di
     top = next;
   }
   if (any) *skip = 1;
-  return total == 0.f ? -INFINITY : top + log2f(total);
+  return make_float2(top, total == 0.f ? 0.f : 1.f / total);
 }
 
 __device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row, int t, float4 v, float f, float lse) {
@@ -1350,7 +1352,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   __shared__ int warp_joins[kJoinThreads / 32];
   __shared__ float4 sums[kJoinThreads];
   __shared__ float part_weights[kJoinThreads / 32][32 * kStatsPerLane];
-  __shared__ __align__(16) float total[2 * 64];
+  __shared__ __align__(16) float tops[2 * 64], shares[2 * 64];
   __shared__ int skip;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1411,31 +1413,37 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
       continue;
     }
     if (p.weights_out == nullptr || length * sub / weight_ctas == length * (sub + 1) / weight_ctas) continue;
-    // the heads' log2-sum-exp, by column of the scores; +inf where there is no head or no key
+    // The heads' references and 1 / sums, by column of the scores: 0 where there is
+    // no head or no key.  (Not the log of the sum in their place: it is a number
+    // of the scores' size, and what its rounding loses would be a factor of every
+    // weight, 2 % at scores of 1e5.)
     if (t == 0) skip = 0;
     __syncthreads();
     {
       // a column to each kJoinThreads / score_cols threads (4 .. 32), which share its parts
       const int with = kJoinThreads / static_cast<int>(p.score_cols), col = t / with, first = t % with;
       const int unit = col / n, c = col % n, head = unit * p.group_heads + c;
-      float v = INFINITY;
+      float2 v = make_float2(0.f, 0.f);
       if (c < p.group_heads && head < p.num_heads) {
         const int2 parts = p.unit_parts[static_cast<int64_t>(r) * p.groups + unit];
         if (parts.x < 0) {
           if (parts.y) skip = 1;
-          v = p.lse[static_cast<int64_t>(r) * p.num_heads + head] * kLog2e;
+          v = p.row_stats[static_cast<int64_t>(r) * p.num_heads + head];
         } else {
-          v = unit_lse(p, n, Division{parts.x, parts.y}, c, head, first, with, &skip);
+          v = unit_stats(p, n, Division{parts.x, parts.y}, c, head, first, with, &skip);
         }
-        if (v == -INFINITY) v = INFINITY;
       }
-      if (first == 0) total[col] = v;
+      if (first == 0) {
+        tops[col] = v.x;
+        shares[col] = v.y;
+      }
     }
     __syncthreads();
     if (!skip) {
       // 4 columns a thread, `lanes` threads a slot
       const int lanes = static_cast<int>(p.score_cols) / 4, step = kJoinThreads / lanes;
-      const float4 l = *reinterpret_cast<const float4*>(total + 4 * (t % lanes));
+      const float4 m = *reinterpret_cast<const float4*>(tops + 4 * (t % lanes));
+      const float4 f = *reinterpret_cast<const float4*>(shares + 4 * (t % lanes));
       const float* const weights_in = p.weights_in == nullptr ? nullptr : p.weights_in + r * p.weights_in_row_stride;
       float* const weights_out = p.weights_out + r * p.weights_out_row_stride;
       const float4* const scores =
@@ -1447,14 +1455,14 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
         if (slot < end) {
           const float4 x = scores[static_cast<int64_t>(slot) * lanes];
           if (weights_in != nullptr) old = weights_in[slot];
-          sum = (l.x == INFINITY ? 0.f : exp2_fast(x.x - l.x)) + (l.y == INFINITY ? 0.f : exp2_fast(x.y - l.y)) +
-                (l.z == INFINITY ? 0.f : exp2_fast(x.z - l.z)) + (l.w == INFINITY ? 0.f : exp2_fast(x.w - l.w));
+          sum = (f.x == 0.f ? 0.f : exp2_fast(x.x - m.x) * f.x) + (f.y == 0.f ? 0.f : exp2_fast(x.y - m.y) * f.y) +
+                (f.z == 0.f ? 0.f : exp2_fast(x.z - m.z) * f.z) + (f.w == 0.f ? 0.f : exp2_fast(x.w - m.w) * f.w);
         }
         for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         if (slot < end && t % lanes == 0) weights_out[slot] = old + sum;
       }
     }
-    __syncthreads();  // total and skip are free again
+    __syncthreads();  // tops, shares and skip are free again
   }
 }
 

@@ -36,7 +36,7 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 // Byte offsets in an attention's workspace.
 struct AttendWorkspace {
-  size_t parts, stats, bad, units, joins, lse, scores, total;
+  size_t parts, stats, bad, units, joins, lse, rows, scores, total;
 };
 
 AttendWorkspace attend_workspace(int64_t num_reqs, int num_heads, int64_t max_pages, bool scores) {
@@ -55,6 +55,7 @@ AttendWorkspace attend_workspace(int64_t num_reqs, int num_heads, int64_t max_pa
   w.units = take(num_reqs * shape.groups * sizeof(int2));
   w.joins = take(kvc::kAttendCtas * sizeof(int4));
   w.lse = take(num_reqs * num_heads * sizeof(float));
+  w.rows = take(scores ? num_reqs * num_heads * sizeof(float2) : 0);
   w.scores = take(scores ? static_cast<size_t>(num_reqs) * max_pages * kvc::kSlotsPerPage * shape.groups *
                                shape.columns * sizeof(float)
                          : 0);
@@ -159,7 +160,10 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
   p.groups = shape.groups;
   p.group_heads = shape.group_heads;
   p.score_cols = static_cast<int64_t>(shape.groups) * shape.columns;
-  if (slot_weights != nullptr) p.scores = reinterpret_cast<float*>(base + at.scores);
+  if (slot_weights != nullptr) {
+    p.scores = reinterpret_cast<float*>(base + at.scores);
+    p.row_stats = reinterpret_cast<float2*>(base + at.rows);
+  }
   // one CTA per SM, fewer where the table cannot name a page for each
   int64_t ctas = sms < kvc::kAttendCtas ? sms : kvc::kAttendCtas;
   if (num_reqs * max_pages_per_req * shape.groups < ctas) ctas = num_reqs * max_pages_per_req * shape.groups;

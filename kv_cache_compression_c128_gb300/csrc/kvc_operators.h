@@ -44,6 +44,8 @@ struct AttendParams {
   float2* part_stats;    // [2 * ctas][columns]: their reference (log2) and sum
   int32_t* part_bad;     // [2 * ctas]: a page was outside the cache
   int2* unit_parts;      // [num_reqs * groups]: first part and last CTA; (-1, bad) if whole
+  float2* row_stats;     // [num_reqs, num_heads] of undivided units, for the weights: reference (log2) and
+                         // 1 / sum (0: no key), or null
   int4* joins;           // [ctas]: (request, group, first part, last CTA) to join, or (-1, ...)
   long long wait_limit;
   uint32_t* error;

@@ -127,3 +127,39 @@ def test_values_near_the_end_of_the_range(kvc, where, H, n, rise, large, flags):
     assert np.isfinite(off).all()
     assert (off <= want[3]).all()
     assert (np.abs(lse.double().cpu().numpy() - want[1]) <= want[4]).all()
+
+
+@pytest.mark.parametrize("size", [30.0, 1e5, 1e6, 1e10, 1e37, -1e5, -1e6, -1e10, -1e37])
+@pytest.mark.parametrize("H", [1, 8, 40, 100])
+@pytest.mark.parametrize("n,flags", [(1, 0), (2, 0), (64, 0), (200, 1), (3000, 0), (3000, 7)])
+def test_weights_of_equal_slots(kvc, n, flags, H, size):
+    # each of n equal slots gets 1 / n of every head, in undivided requests and in
+    # divided ones: half a step for the quotient and one for each head added
+    rng = np.random.default_rng(n)
+    kv = _equal_slots(rng, 1)
+    q = _one_score(rng, H, size)
+    table = torch.zeros((1, -(-n // 64)), dtype=torch.int32, device="cuda")
+    w = torch.full((1, n + 3), 7.0, device="cuda")
+    kvc.attend(q.cuda(), _cuda(kv), table, torch.tensor([n], dtype=torch.int32, device="cuda"), 0.7, slot_weights=w, flags=flags)
+    assert _error(kvc) == 0 and (w[0, n:] == 7).all()
+    off = np.abs(w[0, :n].double().cpu().numpy() - H / n)
+    assert (off <= (H + 1) / 2 * plain.STEP_F32 * H / n).all(), off.max() * n / H
+
+
+@pytest.mark.parametrize("lengths,flags", [([1, 64, 150], 0), ([3000], 0), ([700, 30], 3)])
+@pytest.mark.parametrize("spread", [1.0, 1e3, 1e6])
+def test_weights_of_a_request_sum_up_to_its_heads(kvc, lengths, flags, spread):
+    # Whatever rounding did to the scores, the weights and the sum that divides
+    # them are formed from the same ones: off by the steps of the exponentials
+    # (2 each), of the sums (one a slot, and one a head) and of the quotient.
+    rng = np.random.default_rng(len(lengths))
+    table, pool = plain.page_tables(rng, lengths)
+    H = 24
+    q = torch.from_numpy((spread * rng.standard_normal((len(lengths), H, 512))).astype(np.float32)).to(torch.bfloat16)
+    sinks = np.full(H, -np.inf, np.float32)
+    w = torch.zeros((len(lengths), max(lengths)), device="cuda")
+    kvc.attend(q.cuda(), _cuda(plain.random_cache(rng, pool)), _cuda(table), _cuda(np.array(lengths, np.int32)), sinks=_cuda(sinks),
+               slot_weights=w, flags=flags)
+    assert _error(kvc) == 0
+    got = w.double().sum(1).cpu().numpy()
+    assert (np.abs(got - H) <= H * (np.array(lengths) + H + 8) * plain.STEP_F32).all(), got
