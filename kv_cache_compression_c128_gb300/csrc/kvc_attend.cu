@@ -393,9 +393,13 @@ __device__ __forceinline__ void copy_bytes(void* dst, const void* src, uint32_t 
       : "memory");
 }
 
+// Slots and tables are read with ordinary loads, not the read-only path's
+// (.nc): this kernel may be resident while the one ahead of it on the stream
+// still writes them (an eviction moves slots in place, and releases its
+// dependents at its start), so they are not read-only for its lifetime.
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -460,7 +464,7 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
     int ids = 0;  // of 32 pages, one a lane
 #pragma unroll 1
     for (int pg = 0; ok && pg < count; ++pg, ++i) {
-      if ((pg & 31) == 0) ids = pg + lane < count ? __ldg(table + pg + lane) : 0;
+      if ((pg & 31) == 0) ids = pg + lane < count ? table[pg + lane] : 0;
       int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
       const bool there = static_cast<uint32_t>(id) < p.num_pages;
       if (!there) id = 0;
@@ -589,7 +593,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         raw[j] = load16(page + (r + 8 * j) * kTokenStride + g * kGroup + 16 * c);
-        scale[j] = __ldg(page + kScaleBase + (r + 8 * j) * kScaleDim + g);
+        scale[j] = page[kScaleBase + (r + 8 * j) * kScaleDim + g];
       }
     }
     if (__builtin_expect(info.valid < kSlotsPerPage, 0)) {  // code 0 in every place of the slots that do not count
