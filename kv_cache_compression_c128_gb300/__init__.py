@@ -720,8 +720,11 @@ class _on:
 def _run(call, device, stream):
     """call(raw stream), on the operator's device and stream."""
     cuda = _torch.cuda
-    if stream is None and cuda.current_device() == device:
-        return call(_torch._C._cuda_getCurrentRawStream(device))
+    if stream is None:
+        if cuda.current_device() == device:
+            return call(_torch._C._cuda_getCurrentRawStream(device))
+    elif stream.device.index != device:  # (its context would make the other device current)
+        raise ValueError(f"stream must be one of cuda:{device}, got one of {stream.device}")
     with _on(device, stream):
         return call(cuda.current_stream(device).cuda_stream)
 
