@@ -4,9 +4,12 @@
 // its out may hold anything.  A row whose parts all held none is zeros with
 // lse -inf.
 //
-// One warp per row of 512, 16 dims a lane, all parts of the row in flight;
-// sums in fp32, one rounding at the store for bf16 rows.  Bound by the bytes
-// of the parts and the result: 5 parts of 509 x 64 fp32 rows take 58 us, 6.9 TB/s.
+// One warp per row of 512, 16 dims a lane; sums in fp32, one rounding at the
+// store for bf16 rows.  A row's parts are read one after the other, each only
+// if its lse says that it holds keys: what is in flight beside them are other
+// rows.  Large calls are bound by the bytes of the parts and the result (5 parts
+// of 509 x 64 fp32 rows take 58 us, 6.9 TB/s), small ones by the latency of each
+// part in turn (2 parts of 8 x 64 rows 4.8 us).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
