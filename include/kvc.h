@@ -301,7 +301,10 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
  *   out[r, h] = sum_n exp(s_n - L) k_n,  lse[r, h] = L
  *   slot_weights[r, n] = slot_weights_in[r, n] + sum_h exp(s_n - L_h)
  * A row that sees no key (length 0 or every score -inf, and no sink) is zeros
- * with lse -inf and adds nothing to the weights.  Scores, sums and results
+ * with lse -inf and adds nothing to the weights.  The weights are shares of what a
+ * head gives to these slots and its sink: where the result is joined with
+ * attention over other tokens (kvc_join), a head that gives most of its weight
+ * to those still adds 1 to the slots' in all.  Scores, sums and results
  * are formed in fp32, scores and sinks in powers of two (beyond 2.3e38, where
  * s_n * log2(e) leaves the range, they count as infinite); the softmax weights
  * are rounded to bf16 for the product with the values, and out to bf16 at the

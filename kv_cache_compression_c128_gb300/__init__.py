@@ -743,11 +743,14 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
     Returns (out bf16 [R, H, 512], lse fp32 [R, H]).  With slot_weights (fp32
     [R, S]), entry [r, n] of every slot also receives slot_weights_in[r, n]
     (zero without it; may be the same tensor) plus the slot's softmax weight
-    summed over the heads: what `evict` goes by.  A request whose length or
-    pages are out of range keeps its rows as they were and raises the device
-    error word (kvc_get_device_error).  A workspace given by the caller
-    (kvc_attend_workspace_bytes) serves calls that do not overlap.  A serving
-    form: no gradient is recorded.
+    summed over the heads: what `evict` goes by.  They are shares among these
+    slots and the sink; what a head gives to tokens that are joined later does
+    not lower them.  A request whose length or pages are out of range keeps its
+    rows as they were (undefined in results that the call allocates) and raises
+    the device error word (kvc_get_device_error).  A workspace given by the
+    caller (kvc_attend_workspace_bytes) serves calls that do not overlap; with
+    slot_weights it holds a score for every slot of the page table's width and
+    every head.  A serving form: no gradient is recorded.
     """
     torch = _torch or _load_torch()
     device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
@@ -874,8 +877,11 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
     Returns (lengths_out int32 [R], kept int32 [R, keep]): the new lengths,
     and the former place of the slot at each place (-1 behind the new length).
     slot_weights_out and births_out, if given, receive those arrays in the new
-    order (entries behind the new length are left as they were).  lengths_out,
-    slot_weights_out and births_out may be the inputs themselves.
+    order; entries behind the new length are left as they were, so whoever adds a
+    slot there sets its weight and birth anew.  lengths_out, slot_weights_out and
+    births_out may be the inputs themselves.  A request whose length or pages are
+    out of range stays as it is, its rows of these results too (undefined in
+    results that the call allocates), and raises the device error word.
     """
     torch = _torch or _load_torch()
     device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
