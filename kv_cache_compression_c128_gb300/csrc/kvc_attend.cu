@@ -1032,9 +1032,9 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
 // Shares of `each` pages that begin anew with every unit: the fewest pages for
 // which the CTAs suffice, if not too many over an equal share (each 0: none).
 // An equal share of several units ends several times, some 4 us each at N = 64:
-// 32 requests of up to 4000 slots take 34.7 us with equal shares and 26.1 with
-// these, 96 of up to 1500 37.4 and 28.8 (64 heads); 32 of up to 4000 at 16 heads
-// 24.9 and 21.2.  Every warp tries a number; `own` and `before` are the finder's
+// 32 requests of up to 4000 slots take 33.7 us with equal shares and 25.8 with
+// these, 96 of up to 1500 35.6 and 28.2 (64 heads); 32 of up to 4000 at 16 heads
+// 24.3 and 21.0.  Every warp tries a number; `own` and `before` are the finder's
 // lanes'.  The search takes 1 us.
 struct Shares {
   int each, count, finder, own, before;

@@ -15,10 +15,11 @@
 // moves; a grid of warps then moves the slots, 584 bytes read and written each.
 // Up to 8192 slots a request the CTA keeps 32-bit keys in registers, 8 a
 // thread, and finds the keep-th largest two bits at a time by
-// counting: 16 rounds of one barrier each, whatever the weights are (a histogram
-// of digits took 24.7 us with its scans and its second pass over the keys on
-// 64 x 8192, this 23 us).  Longer requests go by digits, with the keys in
-// shared memory.  Where a request can move 64 slots at most (it has outgrown
+// counting: at most 16 rounds of one barrier each, fewer where a threshold is
+// met that exactly `keep` keys reach (a histogram of digits took 24.7 us with its
+// scans and its second pass over the keys on 64 x 8192, this 23 us).  Longer
+// requests go by digits, with the keys in shared memory (32 x 16384 to 8192:
+// 76.6 us).  Where a request can move 64 slots at most (it has outgrown
 // its share by less than a page), the selecting CTA moves them itself and the
 // second kernel is not launched.
 
