@@ -95,10 +95,26 @@ typedef enum {
 #define KVC_FLAG_ALL \
   (KVC_FLAG_GRID_MASK | KVC_FLAG_CLUSTER_MASK | KVC_FLAG_STREAM_K | KVC_FLAG_ROW_COPIES)
 
-/* Element types: of the state (kvc_compress_strided, kvc_query_launch_ex)
- * and of the output of kvc_dequantize. */
+/* Element types: of the state (kvc_compress_strided, kvc_query_launch_ex),
+ * of the output of kvc_dequantize, and of the tensors of kvc_join, kvc_store
+ * and kvc_rotate. */
 #define KVC_DTYPE_F32 0
 #define KVC_DTYPE_BF16 1
+
+/*
+ * Forms of a packed slot.  A page holds 64 slots: their payloads, then their
+ * scale records.
+ *   KVC_FORMAT_8BIT  what kvc_compress writes: 448 int8 codes in groups of 64,
+ *                    64 bf16 words, 8 scale bytes; a page is uint8 [37376].
+ *   KVC_FORMAT_4BIT  448 codes of 4 bits in groups of 32, 64 bf16 words, 16
+ *                    scale bytes (the last two zero): 352 + 16 bytes, a page is
+ *                    uint8 [23552].  A scale byte 8 e + m is the scale
+ *                    (1 + m / 8) 2^(e - 16); dim d is (u - 8) times the scale of
+ *                    group d / 32, u the 4 bits from bit 4 ((d % 8) / 2) + 16 (d % 2)
+ *                    on of the payload's little-endian 32-bit word d / 8.
+ */
+#define KVC_FORMAT_8BIT 0
+#define KVC_FORMAT_4BIT 1
 
 /*
  * Bytes of device workspace kvc_compress needs for num_outputs outputs on
@@ -292,6 +308,80 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
                           int32_t out_dtype, void* stream);
 
 /*
+ * kvc_dequantize for pages of either form.  A 4-bit slot's values are exact in
+ * fp32 and in bf16; out is 16-byte aligned for it.
+ */
+kvc_status kvc_dequantize_format(const uint8_t* kv_cache, int32_t kv_format, int64_t num_kv_pages,
+                                 const int64_t* slots, int64_t num_slots, void* out,
+                                 int32_t out_dtype, void* stream);
+
+/*
+ * Write vectors into packed slots as they come: row n of x goes to slot slots[n].
+ *   dims 0 .. 447, z = bf16(x), a = max |z| over a group of dims:
+ *     8-bit: e = ceil(log2(max(a, 1e-4) / 127)), code trunc(z 2^-e);
+ *     4-bit: s the smallest scale with 7 s >= a (the largest scale if there is
+ *            none), code z / s to the nearest whole number, halves away from
+ *            zero, at most 7 in size;
+ *   dims 448 .. 511: as they are, or turned by the row's positions (kvc_rotate),
+ *     in bf16.
+ * The 8-bit form stores what kvc_compress stores for the same vector.  A NaN
+ * counts as 0 among the codes, an infinity as the largest code.
+ *
+ * x            bf16 or fp32 (x_dtype) [num_rows, 512], row n at x + n *
+ *              x_row_stride (elements; a multiple of 16 bytes, >= 0), 16-byte
+ *              aligned, columns contiguous.
+ * kv_cache     uint8 pages of kv_format; only the bytes of the slots named are
+ *              written.
+ * slots        int64 [num_rows]; a negative slot skips its row.  No slot may be
+ *              named twice (its bytes would be of either row).
+ * positions, ... , num_positions   as for kvc_rotate; num_axes 0 (and
+ *              positions, pair_axes NULL): not turned.
+ *
+ * A slot beyond the last page, or a position outside the table, records
+ * KVC_ERR_BAD_INDEX and leaves the slot as it was; the other rows are written.
+ * Allocates nothing.
+ */
+kvc_status kvc_store(const void* x, int32_t x_dtype, int64_t x_row_stride, int64_t num_rows,
+                     uint8_t* kv_cache, int32_t kv_format, int64_t num_kv_pages,
+                     const int64_t* slots, const int64_t* positions,
+                     int64_t positions_row_stride, int64_t positions_axis_stride,
+                     int32_t num_axes, const uint8_t* pair_axes, const float* cos_sin_cache,
+                     int64_t num_positions, void* stream);
+
+/*
+ * Rotary positions with one to four axes (text; time, height and width of images
+ * and video): pair i < 32 of a row, dims 2 i and 2 i + 1, is turned by the angle
+ * of its axis' position p = positions[t, pair_axes[i]],
+ *   out[2 i]     = x[2 i] cos - x[2 i + 1] sin,
+ *   out[2 i + 1] = x[2 i + 1] cos + x[2 i] sin,
+ * cos = cos_sin_cache[p, i], sin = cos_sin_cache[p, 32 + i]; with inverse = 1 by
+ * the opposite angle.  It brings queries to their positions, and, inverted, turns
+ * attention's rows back (the rotated dims of a slot are values too); the inverse
+ * is also the map of its gradient.  fp32, rounded once at the end for bf16.
+ *
+ * x, out       bf16 or fp32 (dtype): row (t, h) of 64 elements at t *
+ *              token_stride + h * head_stride (elements; multiples of 16 bytes,
+ *              >= 0), 16-byte aligned.  The rows of out do not overlap; out may be
+ *              x itself, at the same strides.
+ * positions    int64, entry (t, axis) at t * positions_token_stride + axis *
+ *              positions_axis_stride (>= 0).
+ * num_axes     1 .. 4.
+ * pair_axes    HOST array of 32 axes, or NULL where there is one axis.
+ * cos_sin_cache  fp32 [num_positions, 64], 16-byte aligned.
+ * num_tokens at most 2^32, num_heads at most 65535.
+ *
+ * A position outside the table records KVC_ERR_BAD_INDEX and leaves the token's
+ * rows of out as they were; positions of axes that no pair has are not read.
+ * Allocates nothing.
+ */
+kvc_status kvc_rotate(const void* x, int32_t dtype, int64_t x_token_stride, int64_t x_head_stride,
+                      int64_t num_tokens, int32_t num_heads, const int64_t* positions,
+                      int64_t positions_token_stride, int64_t positions_axis_stride,
+                      int32_t num_axes, const uint8_t* pair_axes, const float* cos_sin_cache,
+                      int64_t num_positions, int32_t inverse, void* out,
+                      int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/*
  * Attention of one new token per request over the packed slots of its pages.
  * A slot's 512-vector k (decoded exactly, as kvc_dequantize does) is the key
  * and the value of every head.  For request r, head h and its slots
@@ -360,6 +450,18 @@ kvc_status kvc_attend(const void* q, int64_t q_req_stride, int64_t q_head_stride
                       float* slot_weights, int64_t slot_weights_row_stride, int64_t max_slots,
                       void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
 
+/* kvc_attend over pages of either form (the same workspace). */
+kvc_status kvc_attend_format(const void* q, int64_t q_req_stride, int64_t q_head_stride,
+                             int64_t num_reqs, int32_t num_heads,
+                             const uint8_t* kv_cache, int32_t kv_format, int64_t num_kv_pages,
+                             const int32_t* page_table, int64_t max_pages_per_req,
+                             int64_t page_table_row_stride, const int32_t* lengths,
+                             float scale, const float* sinks, void* out, float* lse,
+                             const float* slot_weights_in, int64_t slot_weights_in_row_stride,
+                             float* slot_weights, int64_t slot_weights_row_stride,
+                             int64_t max_slots, void* workspace, size_t workspace_bytes,
+                             uint32_t flags, void* stream);
+
 /*
  * Join of attention parts whose softmax ran over disjoint sets of keys (the
  * packed slots and the tokens not yet packed, or one cache with several
@@ -421,6 +523,18 @@ kvc_status kvc_evict(uint8_t* kv_cache, int64_t num_kv_pages, const int32_t* pag
                      float* slot_weights_out, int64_t slot_weights_out_row_stride,
                      int32_t* births_out, int64_t births_out_row_stride,
                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* kvc_evict over pages of either form (the same workspace); of 4-bit slots the
+ * 352 + 16 bytes move. */
+kvc_status kvc_evict_format(uint8_t* kv_cache, int32_t kv_format, int64_t num_kv_pages,
+                            const int32_t* page_table, int64_t num_reqs, int64_t max_pages_per_req,
+                            int64_t page_table_row_stride, const int32_t* lengths,
+                            const float* slot_weights, int64_t slot_weights_row_stride,
+                            int64_t max_slots, const int32_t* births, int64_t births_row_stride,
+                            int64_t keep, int64_t recent, int32_t* lengths_out, int32_t* kept,
+                            float* slot_weights_out, int64_t slot_weights_out_row_stride,
+                            int32_t* births_out, int64_t births_out_row_stride,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * kvc_compress without a workspace argument, for callers that cannot

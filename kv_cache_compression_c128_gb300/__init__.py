@@ -25,7 +25,8 @@ _INCLUDE = os.path.join(_ROOT, "include")
 _LIB_DIR = os.path.join(_HERE, "_lib")
 LIB_PATH = os.path.join(_LIB_DIR, "libkvc.so")
 _SOURCES = ["kvc_cluster.cu", "kvc_streamk.cu", "kvc_reader.cu", "kvc_api.cu", "kvc_static.cu",
-            "kvc_selftest.cu", "kvc_attend.cu", "kvc_join.cu", "kvc_evict.cu", "kvc_operators.cu"]
+            "kvc_selftest.cu", "kvc_attend.cu", "kvc_join.cu", "kvc_evict.cu", "kvc_operators.cu",
+            "kvc_store.cu", "kvc_rotate.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 KVC_OK = 0
@@ -38,6 +39,8 @@ KVC_ERR_SCRATCH_LIMIT = 6
 KVC_FLAG_GRID_MASK = 0xFFFF
 KVC_DTYPE_F32 = 0
 KVC_DTYPE_BF16 = 1
+KVC_FORMAT_8BIT = 0
+KVC_FORMAT_4BIT = 1
 KVC_FLAG_CLUSTER_SHIFT = 16
 KVC_FLAG_STREAM_K = 1 << 24
 KVC_FLAG_ROW_COPIES = 1 << 25
@@ -59,6 +62,8 @@ def make_flags(route: str = "auto", count: int = 0, cluster_size: int = 0,
 
 HEAD_DIM = 512
 KV_PAGE_BYTES = 64 * (576 + 8)
+KV4_PAGE_BYTES = 64 * (352 + 16)  # of 4-bit slots
+ROPE_DIM = 64
 
 _lock = threading.Lock()
 _lib = None
@@ -162,6 +167,10 @@ def lib():
                 P, I64, I64, I64, I32, P, I64, P, I64, I64, P, ctypes.c_float, P, P, P, P, I64,
                 P, I64, I64, P, ctypes.c_size_t, U32, P]
             L.kvc_attend.restype = ctypes.c_int
+            L.kvc_attend_format.argtypes = [
+                P, I64, I64, I64, I32, P, I32, I64, P, I64, I64, P, ctypes.c_float, P, P, P, P,
+                I64, P, I64, I64, P, ctypes.c_size_t, U32, P]
+            L.kvc_attend_format.restype = ctypes.c_int
             L.kvc_join.argtypes = [P, P, I32, I64, I32, P, P, P]
             L.kvc_join.restype = ctypes.c_int
             L.kvc_evict_workspace_bytes.argtypes = [I64, I64, I64]
@@ -170,6 +179,18 @@ def lib():
                 P, I64, P, I64, I64, I64, P, P, I64, I64, P, I64, I64, I64, P, P, P, I64, P, I64,
                 P, ctypes.c_size_t, P]
             L.kvc_evict.restype = ctypes.c_int
+            L.kvc_evict_format.argtypes = [
+                P, I32, I64, P, I64, I64, I64, P, P, I64, I64, P, I64, I64, I64, P, P, P, I64, P,
+                I64, P, ctypes.c_size_t, P]
+            L.kvc_evict_format.restype = ctypes.c_int
+            L.kvc_store.argtypes = [P, I32, I64, I64, P, I32, I64, P, P, I64, I64, I32,
+                                    ctypes.c_char_p, P, I64, P]
+            L.kvc_store.restype = ctypes.c_int
+            L.kvc_dequantize_format.argtypes = [P, I32, I64, P, I64, P, I32, P]
+            L.kvc_dequantize_format.restype = ctypes.c_int
+            L.kvc_rotate.argtypes = [P, I32, I64, I64, I64, I32, P, I64, I64, I32,
+                                     ctypes.c_char_p, P, I64, I32, P, I64, I64, P]
+            L.kvc_rotate.restype = ctypes.c_int
             L.kvc_query_launch.argtypes = [I64, I32, U32, P, P, P, P]
             L.kvc_query_launch.restype = ctypes.c_int
             L.kvc_query_launch_ex.argtypes = [I64, I32, I32, U32, P, P, P, P]
@@ -371,6 +392,35 @@ def kvc_dequantize(kv_cache, num_kv_pages, slots, num_slots, out, out_dtype, str
                                     int(out_dtype), v(stream)))
 
 
+def kvc_dequantize_format(kv_cache, kv_format, num_kv_pages, slots, num_slots, out, out_dtype,
+                          stream) -> int:
+    """Decode slots of either form (raw integer pointers); returns the status."""
+    return lib().kvc_dequantize_format(kv_cache, kv_format, num_kv_pages, slots, num_slots, out,
+                                       out_dtype, stream)
+
+
+def kvc_store(x, x_dtype, x_row_stride, num_rows, kv_cache, kv_format, num_kv_pages, slots,
+              positions, positions_row_stride, positions_axis_stride, num_axes, pair_axes,
+              cos_sin_cache, num_positions, stream) -> int:
+    """Vectors into packed slots (raw integer pointers; pair_axes 32 bytes or
+    None); returns the status."""
+    return lib().kvc_store(
+        x, x_dtype, x_row_stride, num_rows, kv_cache, kv_format, num_kv_pages, slots, positions,
+        positions_row_stride, positions_axis_stride, num_axes, pair_axes, cos_sin_cache,
+        num_positions, stream)
+
+
+def kvc_rotate(x, dtype, x_token_stride, x_head_stride, num_tokens, num_heads, positions,
+               positions_token_stride, positions_axis_stride, num_axes, pair_axes, cos_sin_cache,
+               num_positions, inverse, out, out_token_stride, out_head_stride, stream) -> int:
+    """Rotary positions (raw integer pointers; pair_axes 32 bytes or None);
+    returns the status."""
+    return lib().kvc_rotate(
+        x, dtype, x_token_stride, x_head_stride, num_tokens, num_heads, positions,
+        positions_token_stride, positions_axis_stride, num_axes, pair_axes, cos_sin_cache,
+        num_positions, inverse, out, out_token_stride, out_head_stride, stream)
+
+
 def kvc_attend_workspace_bytes(num_reqs: int, num_heads: int, max_pages_per_req: int,
                                with_slot_weights: bool = False) -> int:
     return int(lib().kvc_attend_workspace_bytes(int(num_reqs), int(num_heads),
@@ -386,6 +436,19 @@ def kvc_attend(q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, nu
     return lib().kvc_attend(
         q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, num_kv_pages, page_table,
         max_pages_per_req, page_table_row_stride, lengths, scale, sinks, out, lse,
+        slot_weights_in, slot_weights_in_row_stride, slot_weights, slot_weights_row_stride,
+        max_slots, workspace, workspace_bytes, flags, stream)
+
+
+def kvc_attend_format(q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, kv_format,
+                      num_kv_pages, page_table, max_pages_per_req, page_table_row_stride, lengths,
+                      scale, sinks, out, lse, slot_weights_in, slot_weights_in_row_stride,
+                      slot_weights, slot_weights_row_stride, max_slots, workspace,
+                      workspace_bytes, flags, stream) -> int:
+    """kvc_attend over pages of either form."""
+    return lib().kvc_attend_format(
+        q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, kv_format, num_kv_pages,
+        page_table, max_pages_per_req, page_table_row_stride, lengths, scale, sinks, out, lse,
         slot_weights_in, slot_weights_in_row_stride, slot_weights, slot_weights_row_stride,
         max_slots, workspace, workspace_bytes, flags, stream)
 
@@ -414,11 +477,26 @@ def kvc_evict(kv_cache, num_kv_pages, page_table, num_reqs, max_pages_per_req,
         births_out, births_out_row_stride, workspace, workspace_bytes, stream)
 
 
+def kvc_evict_format(kv_cache, kv_format, num_kv_pages, page_table, num_reqs, max_pages_per_req,
+                     page_table_row_stride, lengths, slot_weights, slot_weights_row_stride,
+                     max_slots, births, births_row_stride, keep, recent, lengths_out, kept,
+                     slot_weights_out, slot_weights_out_row_stride, births_out,
+                     births_out_row_stride, workspace, workspace_bytes, stream) -> int:
+    """kvc_evict over pages of either form."""
+    return lib().kvc_evict_format(
+        kv_cache, kv_format, num_kv_pages, page_table, num_reqs, max_pages_per_req,
+        page_table_row_stride, lengths, slot_weights, slot_weights_row_stride, max_slots, births,
+        births_row_stride, keep, recent, lengths_out, kept, slot_weights_out,
+        slot_weights_out_row_stride, births_out, births_out_row_stride, workspace,
+        workspace_bytes, stream)
+
+
 # ---- torch-facing wrappers ----------------------------------------------------
 
 def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
     """Read slots of a packed kv_cache back as [len(slots), 512] vectors
-    (torch.float32 or torch.bfloat16) on the cache's device."""
+    (torch.float32 or torch.bfloat16) on the cache's device.  Pages of 23552
+    bytes hold 4-bit slots, others 8-bit ones."""
     import torch
 
     dtype = torch.float32 if dtype is None else dtype
@@ -433,12 +511,15 @@ def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
     if out is None:
         out = torch.empty((M, HEAD_DIM), dtype=dtype, device=dev)
     _check(out, "out", dtype, dev)
+    four = kv_cache.dim() == 2 and kv_cache.shape[1] == KV4_PAGE_BYTES
+    if four and out.numel() < M * HEAD_DIM:
+        raise ValueError("out must hold len(slots) * 512 values")
     with torch.cuda.device(dev):
         s = stream if stream is not None else torch.cuda.current_stream(dev)
-        st = kvc_dequantize(kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), M,
-                            out.data_ptr(),
-                            KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32,
-                            int(s.cuda_stream))
+        st = kvc_dequantize_format(kv_cache.data_ptr(), KVC_FORMAT_4BIT if four else KVC_FORMAT_8BIT,
+                                   kv_cache.shape[0], slots.data_ptr(), M, out.data_ptr(),
+                                   KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32,
+                                   int(s.cuda_stream))
     if st != KVC_OK:
         raise KvcError(st, "kvc_dequantize")
     return out
@@ -671,7 +752,7 @@ def _rows(name, t, dtype, device):
         _refuse(name, t, dtype, 2, device)
     rows, cols = t.shape
     row, col = t.stride()
-    if col != 1 and cols > 1:
+    if col != 1 and cols > 1 and rows > 0:
         _refuse(name, t, dtype, 2, device)
     return rows, cols, row
 
@@ -684,19 +765,26 @@ def _dense(name, t, dtype, device, shape):
         raise ValueError(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _cache(kv_cache, page_table, lengths):
-    """(device index, pages, requests, page table columns, its row stride)"""
+def _pages(kv_cache):
+    """(device index, pages, their form)"""
     if not isinstance(kv_cache, _torch.Tensor) or not kv_cache.is_cuda:
         raise ValueError("kv_cache must be a CUDA tensor (there is no CPU path)")
     device = kv_cache.get_device()
     if kv_cache.dtype != _torch.uint8 or kv_cache.dim() != 2:
         _refuse("kv_cache", kv_cache, _torch.uint8, 2, device)
     pages, width = kv_cache.shape
-    if width != KV_PAGE_BYTES or not kv_cache.is_contiguous():
-        raise ValueError(f"kv_cache must be contiguous [num_pages, {KV_PAGE_BYTES}] uint8")
+    if (width != KV_PAGE_BYTES and width != KV4_PAGE_BYTES) or not kv_cache.is_contiguous():
+        raise ValueError(f"kv_cache must be contiguous [num_pages, {KV_PAGE_BYTES}] uint8, or "
+                         f"[num_pages, {KV4_PAGE_BYTES}] of 4-bit slots")
+    return device, pages, KVC_FORMAT_8BIT if width == KV_PAGE_BYTES else KVC_FORMAT_4BIT
+
+
+def _cache(kv_cache, page_table, lengths):
+    """(device index, pages, their form, requests, page table columns, its row stride)"""
+    device, pages, form = _pages(kv_cache)
     reqs, columns, row = _rows("page_table", page_table, _torch.int32, device)
     _dense("lengths", lengths, _torch.int32, device, (reqs,))
-    return device, pages, reqs, columns, row
+    return device, pages, form, reqs, columns, row
 
 
 class _on:
@@ -729,13 +817,132 @@ def _run(call, device, stream):
         return call(cuda.current_stream(device).cuda_stream)
 
 
+def _rotation(positions, cos_sin_cache, axes, rows, device):
+    """(positions, row stride, axis stride, axes, pair axes, table, its rows) of a
+    C call that turns `rows` rows."""
+    if not isinstance(positions, _torch.Tensor) or positions.dtype != _torch.int64 or positions.get_device() != device:
+        _refuse("positions", positions, _torch.int64, 2, device)
+    shape, stride = positions.shape, positions.stride()
+    count = 1
+    if len(shape) == 2:
+        count = shape[1]
+    elif len(shape) != 1:
+        raise ValueError("positions must be [rows] or [rows, axes]")
+    if shape[0] != rows:
+        raise ValueError("positions must have one row for each of x")
+    if not 1 <= count <= 4:
+        raise ValueError("positions must have 1 to 4 axes")
+    if axes is not None:
+        if type(axes) is not bytes:
+            axes = bytes(axes)
+        if len(axes) != 32 or max(axes) >= count:
+            raise ValueError("axes must name an axis of positions for each of the 32 pairs")
+    elif count > 1:
+        raise ValueError("positions of several axes need axes, one for each of the 32 pairs")
+    entries, width, _ = _rows("cos_sin_cache", cos_sin_cache, _torch.float32, device)
+    if width != ROPE_DIM or not cos_sin_cache.is_contiguous():
+        raise ValueError("cos_sin_cache must be contiguous [num_positions, 64]")
+    return (positions.data_ptr(), stride[0], stride[1] if len(shape) == 2 else 0, count, axes,
+            cos_sin_cache.data_ptr(), entries)
+
+
+def store(x, kv_cache, slots, *, positions=None, cos_sin_cache=None, axes=None, stream=None):
+    """Write vectors into packed slots as they come, in place.
+
+    x bf16 or fp32 [N, 512] (any row stride that is a multiple of 16 bytes,
+    columns contiguous); kv_cache uint8 [pages, 37376] of 8-bit slots or
+    [pages, 23552] of 4-bit ones; slots int64 [N], a negative one skips its row,
+    none may be named twice.  Dims 0..447 are rounded to bf16 and quantised: in
+    8 bits as the compressor does, in 4 bits to 15 levels with a scale for every
+    32 dims.  Dims 448..511 are kept in bf16, turned to `positions` if given
+    (with cos_sin_cache and axes as for `rotate`).
+
+    A slot beyond the cache or a position outside the table leaves its slot as
+    it was and raises the device error word (kvc_get_device_error).  Returns
+    kv_cache.  No gradient is recorded.
+    """
+    torch = _torch or _load_torch()
+    device, pages, form = _pages(kv_cache)
+    if not isinstance(x, torch.Tensor) or (x.dtype != torch.bfloat16 and x.dtype != torch.float32):
+        raise TypeError("x must be a tensor of dtype torch.float32 or torch.bfloat16")
+    N, D, row = _rows("x", x, x.dtype, device)
+    if D != HEAD_DIM:
+        raise ValueError("x must be [rows, 512]")
+    _dense("slots", slots, torch.int64, device, (N,))
+    turn = (None, 0, 0, 0, None, None, 0)
+    if positions is not None:
+        turn = _rotation(positions, cos_sin_cache, axes, N, device)
+    elif axes is not None or cos_sin_cache is not None:
+        raise ValueError("axes and cos_sin_cache need positions")
+
+    def call(raw):
+        return kvc_store(
+            x.data_ptr(), KVC_DTYPE_BF16 if x.dtype == torch.bfloat16 else KVC_DTYPE_F32, row if N > 1 else 0,
+            N, kv_cache.data_ptr(), form, pages, slots.data_ptr(), *turn, raw)
+
+    st = _run(call, device, stream)
+    if st != KVC_OK:
+        raise KvcError(st, "kvc_store")
+    return kv_cache
+
+
+def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out=None, stream=None):
+    """Rotary positions, with one axis or several.
+
+    x bf16 or fp32 [T, H, 64] or [T, 64] (any token and head strides that are
+    multiples of 16 bytes, columns contiguous: the last 64 dims of queries
+    [T, H, 512], for instance); positions int64 [T] or [T, 1..4 axes] (any
+    strides); cos_sin_cache fp32 [P, 64], cos in columns 0..31, sin 32..63.  Pair
+    i (dims 2 i, 2 i + 1) is turned by the angle in column i at the position of
+    axis axes[i]: 32 numbers (bytes are taken as they are), not needed for one
+    axis.
+
+    `inverse` turns by the opposite angles: attention's rows back, whose last 64
+    dims are sums of rotated ones, and the gradient with respect to x from the
+    one with respect to the result.  Returns `out`, which may be x itself (a new
+    contiguous tensor if None).  A position outside the table leaves its token's
+    rows of out as they were and raises the device error word.  No gradient is
+    recorded.
+    """
+    torch = _torch or _load_torch()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor (there is no CPU path)")
+    device, dtype, shape = x.get_device(), x.dtype, x.shape
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise TypeError("x must have dtype torch.float32 or torch.bfloat16")
+    if not 2 <= len(shape) <= 3 or shape[-1] != ROPE_DIM or (x.stride(-1) != 1 and x.numel() > 0):
+        raise ValueError("x must be [tokens, heads, 64] or [tokens, 64] with contiguous columns")
+    T, H = shape[0], shape[1] if len(shape) == 3 else 1
+    turn = _rotation(positions, cos_sin_cache, axes, T, device)
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != device or out.dim() != len(shape):
+            _refuse("out", out, dtype, len(shape), device)
+        if out.shape != shape or (out.stride(-1) != 1 and out.numel() > 0):
+            raise ValueError(f"out must be {tuple(shape)} with contiguous columns")
+
+    def call(raw):
+        nonlocal out
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=x.device)
+        xs, os = x.stride(), out.stride()
+        return kvc_rotate(
+            x.data_ptr(), KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32, xs[0] if T > 1 else 0,
+            xs[1] if H > 1 else 0, T, H, *turn, 1 if inverse else 0, out.data_ptr(), os[0] if T > 1 else 0,
+            os[1] if H > 1 else 0, raw)
+
+    st = _run(call, device, stream)
+    if st != KVC_OK:
+        raise KvcError(st, "kvc_rotate")
+    return out
+
+
 def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None, lse=None,
            slot_weights=None, slot_weights_in=None, flags: int = 0, stream=None, workspace=None):
     """Attention of one new token per request over its packed slots.
 
     q bf16 [R, H, 512] (any request and head strides that are multiples of 8
-    elements, columns contiguous; H up to 128); kv_cache uint8 [pages, 37376];
-    page_table int32 [R, max_pages] (any row stride), 64 slots to a page;
+    elements, columns contiguous; H up to 128); kv_cache uint8 [pages, 37376], or
+    [pages, 23552] of 4-bit slots; page_table int32 [R, max_pages] (any row stride), 64 slots to a page;
     lengths int32 [R], slots of each request.  A slot's decoded vector is the
     key and the value of every head; `scale` defaults to 512 ** -0.5; optional
     sinks fp32 [H] join the softmax as a score without a value.
@@ -753,7 +960,7 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
     every head.  A serving form: no gradient is recorded.
     """
     torch = _torch or _load_torch()
-    device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
+    device, pages, form, R, columns, row = _cache(kv_cache, page_table, lengths)
     if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.get_device() != device or q.dim() != 3:
         _refuse("q", q, torch.bfloat16, 3, device)
     shape = q.shape
@@ -803,9 +1010,9 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
         if workspace is None:
             workspace = torch.empty(kvc_attend_workspace_bytes(R, H, columns, slot_weights is not None),
                                     dtype=torch.uint8, device=kv_cache.device)
-        return kvc_attend(
-            q.data_ptr(), by_req, by_head, R, H, kv_cache.data_ptr(), pages, page_table.data_ptr(),
-            columns, row, lengths.data_ptr(), HEAD_DIM ** -0.5 if scale is None else scale,
+        return kvc_attend_format(
+            q.data_ptr(), by_req, by_head, R, H, kv_cache.data_ptr(), form, pages,
+            page_table.data_ptr(), columns, row, lengths.data_ptr(), HEAD_DIM ** -0.5 if scale is None else scale,
             None if sinks is None else sinks.data_ptr(), out.data_ptr(), lse.data_ptr(),
             None if slot_weights_in is None else slot_weights_in.data_ptr(), in_row,
             None if slot_weights is None else slot_weights.data_ptr(), weights_row, S,
@@ -866,7 +1073,8 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
           workspace=None):
     """Evict, in place, the slots that gathered the least attention.
 
-    Of the first lengths[r] slots of request r, min(keep, lengths[r]) stay:
+    Of the first lengths[r] slots of request r (of either form, as for attend),
+    min(keep, lengths[r]) stay:
     the `recent` newest by birth number (births int32 [R, S], needed if recent
     > 0), then those of largest slot_weights[r, n] (fp32 [R, S]), the lowest
     index first among equals, NaN last.  Slots that stay below the new length
@@ -884,7 +1092,7 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
     results that the call allocates), and raises the device error word.
     """
     torch = _torch or _load_torch()
-    device, pages, R, columns, row = _cache(kv_cache, page_table, lengths)
+    device, pages, form, R, columns, row = _cache(kv_cache, page_table, lengths)
     keep, recent = int(keep), int(recent)
     if keep < 0 or not 0 <= recent <= keep:
         raise ValueError("keep must be >= 0 and recent between 0 and keep")
@@ -928,8 +1136,8 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
         if workspace is None:
             workspace = torch.empty(kvc_evict_workspace_bytes(R, columns, keep), dtype=torch.uint8,
                                     device=kv_cache.device)
-        return kvc_evict(
-            kv_cache.data_ptr(), pages, page_table.data_ptr(), R, columns, row, lengths.data_ptr(),
+        return kvc_evict_format(
+            kv_cache.data_ptr(), form, pages, page_table.data_ptr(), R, columns, row, lengths.data_ptr(),
             slot_weights.data_ptr(), weights_row, S, None if births is None else births.data_ptr(),
             births_row, keep, recent, lengths_out.data_ptr(), kept.data_ptr() if keep else None,
             None if slot_weights_out is None else slot_weights_out.data_ptr(), weights_out_row,

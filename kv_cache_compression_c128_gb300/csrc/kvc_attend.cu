@@ -87,8 +87,12 @@ constexpr int kSoftmaxRegs = 168, kOtherRegs = 112;
 constexpr int kKeyBlock = kSlotsPerPage * 128;          // 64 slots x 64 dims, bf16
 constexpr int kKeyStage = 8 * kKeyBlock;                // a decoded page
 constexpr int kGroups = 7;                              // of 64 codes with one scale
-constexpr int kPieceBytes = kSlotsPerPage * kGroup;     // a page's codes of one group
-constexpr int kScaleBytes = kSlotsPerPage * kScaleDim;
+template <typename F>
+__host__ __device__ constexpr int group_bytes() { return F::kFour ? kGroup / 2 : kGroup; }  // a slot's codes of 64 dims
+template <typename F>
+__host__ __device__ constexpr int piece_bytes() { return kSlotsPerPage * group_bytes<F>(); }  // a page's
+template <typename F>
+__host__ __device__ constexpr int scale_bytes() { return kSlotsPerPage * F::kScales; }
 // Pages described at a time.  While the RoPE words of page j are not there, its
 // products are not issued, the decode is at page j + 2 at most, and the copies
 // at page j + 3 + depth(): a page's place here is taken again eight pages later.
@@ -113,14 +117,14 @@ constexpr int kStatsPerLane = (kAttendCtas + 31) / 32;  // of a unit's parts
 // loads its codes itself.  (Seven groups in turn on six places held the seventh
 // piece up behind the first one's store; half places asked for twice a page, or
 // loads a page ahead into registers, took longer.)
-template <int N>
-__host__ __device__ constexpr int ring_groups() { return N == 64 ? 6 : 7; }
+template <int N, typename F>
+__host__ __device__ constexpr int ring_groups() { return N == 64 && !F::kFour ? 6 : 7; }
 // Pages that the ring holds, and pages whose scales are kept for its groups:
 // page i's are asked for when all pieces of page i - 1 - depth() are read, and
 // their scales before them.
-template <int N>
-__host__ __device__ constexpr int depth() { return N == 64 ? 1 : 2; }
-template <int N>
+template <int N, typename F>
+__host__ __device__ constexpr int depth() { return N == 64 ? 1 : F::kFour ? 3 : 2; }
+template <int N, typename F>
 __host__ __device__ constexpr int scale_slots() { return N == 64 ? 2 : 4; }
 
 // A page on its way: its id (clamped), slots that count, whether it ends its segment.
@@ -129,7 +133,7 @@ struct PageInfo {
   int16_t valid, last;
 };
 
-template <int N>
+template <int N, typename F>
 struct Barriers {
   // Of a stage's halves of 256 dims, and of its chunks of 128.  A wait of the
   // issuer costs some 250 cycles even if nothing is to be waited for, since
@@ -137,7 +141,7 @@ struct Barriers {
   unsigned long long half_full[2][2], chunk_empty[2][4];
   unsigned long long s_full[2];
   unsigned long long p_full, q_full, q_empty, o_full, drain;
-  unsigned long long piece_full[depth<N>()][ring_groups<N>()], piece_empty[depth<N>()][ring_groups<N>()], info_full[kInfos];
+  unsigned long long piece_full[depth<N, F>()][ring_groups<N, F>()], piece_empty[depth<N, F>()][ring_groups<N, F>()], info_full[kInfos];
 };
 
 // What is left of a segment once its products are done: the rows of O, dims on
@@ -149,20 +153,20 @@ struct Rows {
   int whole;
 };
 
-template <int N>
+template <int N, typename F>
 struct AttendShared {
   alignas(1024) uint8_t keys[2][kKeyStage];
   alignas(1024) uint8_t q[N * 1024];
   alignas(1024) uint8_t p[kSlotsPerPage * 2 * N];
-  alignas(1024) uint8_t codes[depth<N>()][ring_groups<N>()][kPieceBytes];
-  alignas(16) uint8_t scales[scale_slots<N>()][kScaleBytes];
+  alignas(1024) uint8_t codes[depth<N, F>()][ring_groups<N, F>()][piece_bytes<F>()];
+  alignas(16) uint8_t scales[scale_slots<N, F>()][scale_bytes<F>()];
   union {
     float red[kSoftmaxWarps][N];
     int4 scan[kAttendThreads / 32];
   };
   float ref[N];
   alignas(8) float factor[N];
-  Barriers<N> bar;
+  Barriers<N, F> bar;
   PageInfo info[kInfos];
   uint8_t bad[8];  // of the last segments: a page was outside the cache
   uint8_t large[kInfos];  // of the pages in info
@@ -437,6 +441,19 @@ __device__ __forceinline__ void decode4_bf16(uint32_t word, uint32_t up, uint32_
   *hi = fma_bf16x2(mul_bf16x2(__byte_perm(u, 0, 0x4342), 0x7F007F00u), up, less);
 }
 
+// 8 codes of a 4-bit slot times its scale as four words of bf16, exactly.  A code
+// lies 8 above itself in its 4 bits, u; as the low bits of 128's bf16 it is
+// 128 + u, and one fused multiply-add by s less 136 s leaves (u - 8) s: s has 4
+// significant bits, 136 s = 17 x 8 s no more than 8, the result 7.
+__device__ __forceinline__ uint4 decode8_bf16(uint32_t word, uint32_t s, uint32_t less) {
+  uint4 v;
+  v.x = fma_bf16x2((word & 0x000F000Fu) | 0x43004300u, s, less);
+  v.y = fma_bf16x2((word >> 4 & 0x000F000Fu) | 0x43004300u, s, less);
+  v.z = fma_bf16x2((word >> 8 & 0x000F000Fu) | 0x43004300u, s, less);
+  v.w = fma_bf16x2((word >> 12 & 0x000F000Fu) | 0x43004300u, s, less);
+  return v;
+}
+
 // ---- the roles ------------------------------------------------------------------------
 
 template <int N>
@@ -450,9 +467,9 @@ __device__ __forceinline__ int heads_of(const AttendParams& p, int group) {
 // Copies the codes and scales of every page of the share: lane g the codes of
 // group g, lane 31 the scales.  (One lane after the other's wait, announcement
 // and copy took some 500 cycles a piece, 3500 a page, and held up all the rest.)
-template <int N>
-__device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
-  constexpr int kDepth = depth<N>(), kScales = scale_slots<N>(), kRing = ring_groups<N>();
+template <int N, typename F>
+__device__ void copy_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) {
+  constexpr int kDepth = depth<N, F>(), kScales = scale_slots<N, F>(), kRing = ring_groups<N, F>();
   const int lane = threadIdx.x & 31;
   int i = 0;       // pages begun
   int asked = 0;   // of this lane's pieces, or pages' scales
@@ -476,8 +493,8 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
         const int valid = there ? min(kSlotsPerPage, w.length - (w.page + pg) * kSlotsPerPage) : 0;
         s.info[i % kInfos] = PageInfo{id, static_cast<int16_t>(valid), static_cast<int16_t>(pg + 1 == count)};
         s.large[i % kInfos] = 0;
-        dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], kScaleBytes);
-        copy_bytes(s.scales[i % kScales], p.kv_cache + id * kPageBytes + kScaleBase, kScaleBytes,
+        dev::mbar_arrive_expect_tx(&s.bar.info_full[i % kInfos], scale_bytes<F>());
+        copy_bytes(s.scales[i % kScales], p.kv_cache + id * F::kPage + F::kScaleBase, scale_bytes<F>(),
                    &s.bar.info_full[i % kInfos]);
         ++asked;
       }
@@ -485,8 +502,8 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
       if (lane < kRing) {
         ok = turn == 0 || wait_for(&s.bar.piece_empty[place][lane], (turn - 1) & 1, p.wait_limit);
         if (ok) {
-          dev::mbar_arrive_expect_tx(&s.bar.piece_full[place][lane], kPieceBytes);
-          copy_box(s.codes[place][lane], &p.code_map, lane * kGroup, 0, id, &s.bar.piece_full[place][lane]);
+          dev::mbar_arrive_expect_tx(&s.bar.piece_full[place][lane], piece_bytes<F>());
+          copy_box(s.codes[place][lane], &p.code_map, lane * group_bytes<F>(), 0, id, &s.bar.piece_full[place][lane]);
           ++asked;
         }
       }
@@ -509,8 +526,8 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
 }
 
 // Copies each segment's queries, in the layout of the products' operand.
-template <int N>
-__device__ void query_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+template <int N, typename F>
+__device__ void query_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) {
 #pragma unroll 1
   for (int segment = 0; w.left > 0; ++segment) {
     bool ok = segment == 0 || wait_for(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit);
@@ -559,9 +576,9 @@ __device__ __forceinline__ void decode_rows(const uint4 (&raw)[8], const uint32_
 
 // Decodes group g of every page: 64 slots x 64 codes, 8 times 8 slots, lane l
 // slot l / 4 of the 8 and codes 16 (l % 4) .. + 15.
-template <int N>
-__device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, int count) {
-  constexpr int kDepth = depth<N>(), kScales = scale_slots<N>();
+template <int N, typename F>
+__device__ void decode_role(const AttendParams& p, AttendShared<N, F>& s, int g, int count) {
+  constexpr int kDepth = depth<N, F>(), kScales = scale_slots<N, F>();
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   uint32_t scale[8];
   uint4 raw[8];
@@ -572,7 +589,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
     ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
     // (what is not described, after a wait that ran out, is not an address)
     const PageInfo info = ok ? s.info[i % kInfos] : PageInfo{0, 0, 0};
-    if (g < ring_groups<N>()) {
+    if (g < ring_groups<N, F>()) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
       ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit);
@@ -589,7 +606,7 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
       const int arrives = __all_sync(0xFFFFFFFFu, all == 1u) ? 1 : 0;
       if (lane == arrives) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
     } else {
-      const uint8_t* page = p.kv_cache + info.id * kPageBytes;
+      const uint8_t* page = p.kv_cache + info.id * F::kPage;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         raw[j] = load16(page + (r + 8 * j) * kTokenStride + g * kGroup + 16 * c);
@@ -621,22 +638,77 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N>& s, int g, in
   }
 }
 
+// The same of 4-bit slots: 4 times 16 slots, lane l slot l / 2 of the 16 and codes
+// 32 (l % 2) .. + 31, which have one scale.
+template <int N, typename F>
+__device__ void decode4_role(const AttendParams& p, AttendShared<N, F>& s, int g, int count) {
+  constexpr int kDepth = depth<N, F>(), kScales = scale_slots<N, F>();
+  const int lane = threadIdx.x & 31, r = lane >> 1, c = lane & 1;
+  bool ok = true;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const int stage = i & 1, place = i % kDepth;
+    uint32_t scale[4];
+    uint4 raw[4];
+    ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
+    const int valid = ok ? s.info[i % kInfos].valid : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) scale[j] = s.scales[i % kScales][(r + 16 * j) * F::kScales + 2 * g + c];
+    ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[place][g] + (lane + 32 * j) * 16);
+    // given back once the values are there (see decode_role)
+    uint32_t all = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) all ^= raw[j].x ^ raw[j].w ^ scale[j];
+    const int arrives = __all_sync(0xFFFFFFFFu, all == 1u) ? 1 : 0;
+    if (lane == arrives) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
+    if (__builtin_expect(valid < kSlotsPerPage, 0)) {  // code 0 in every place of the slots that do not count
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r + 16 * j >= valid) raw[j] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u), scale[j] = 0;
+    }
+    uint4 v[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t up = scale[j] * 0x00100010u + kScale4Bits * 0x00010001u, less = mul_bf16x2(up, 0xC308C308u);
+      v[j][0] = decode8_bf16(raw[j].x, up, less);
+      v[j][1] = decode8_bf16(raw[j].y, up, less);
+      v[j][2] = decode8_bf16(raw[j].z, up, less);
+      v[j][3] = decode8_bf16(raw[j].w, up, less);
+    }
+    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit);
+    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+      s.abort = 1;
+      return;
+    }
+    uint8_t* const block = s.keys[stage] + g * kKeyBlock + r * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(block + 2048 * j + (((4 * c + k) ^ (r & 7)) << 4)) = v[j][k];
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(&s.bar.half_full[stage][g >> 2]);
+  }
+}
+
 // The RoPE words of every page, read into registers ahead (8 KB, which plain
 // loads can keep on their way) and stored once their place is free: lane l has
 // piece l % 8 of rows l / 8 + 4 j.
-template <int N>
-__device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) {
+template <int N, typename F>
+__device__ void rope_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
   const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7;
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1;
     bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
     const PageInfo info = ok ? s.info[i % kInfos] : PageInfo{0, 0, 0};
-    const uint8_t* src = p.kv_cache + info.id * kPageBytes + r * kTokenStride + kNopeDim + 16 * c;
+    const uint8_t* src = p.kv_cache + info.id * F::kPage + r * F::kStride + F::kCodes + 16 * c;
     uint4 v[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j)  // slots that do not count may hold anything, NaN too
-      v[j] = r + 4 * j < info.valid ? load16(src + 4 * j * kTokenStride) : make_uint4(0, 0, 0, 0);
+      v[j] = r + 4 * j < info.valid ? load16(src + 4 * j * F::kStride) : make_uint4(0, 0, 0, 0);
     if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][3], ((i >> 1) - 1) & 1, p.wait_limit);
     if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
       s.abort = 1;
@@ -672,8 +744,8 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N>& s, int count) 
 // short loop: the questions travel together and behind products already queued,
 // and every role's code has to stay in the instruction cache beside the others'.
 // (Questions by one lane instead of all: 137 us where this takes 125.)
-template <int N>
-__device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count) {
+template <int N, typename F>
+__device__ void issue_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
   constexpr uint32_t kFirst = instruction(64, N, false), kSecond = instruction(128, N, true);
   constexpr uint32_t kRows = operand_hi(1024, 2);
   constexpr uint32_t kProbs = operand_hi(16 * N, N == 64 ? 2 : N == 32 ? 4 : 6);
@@ -766,8 +838,8 @@ __device__ void issue_role(const AttendParams& p, AttendShared<N>& s, int count)
 }
 
 // Columns `from` .. `to` - 1 of the four chunks' 4 N, the lanes of a warp.
-template <int N>
-__device__ __forceinline__ void write_rows(const AttendParams& p, const AttendShared<N>& s, const Rows& rows, int from,
+template <int N, typename F>
+__device__ __forceinline__ void write_rows(const AttendParams& p, const AttendShared<N, F>& s, const Rows& rows, int from,
                                            int to) {
   constexpr int kWide = N == 16 ? 16 : 32;  // columns at a time
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -841,8 +913,8 @@ __device__ __forceinline__ void store_combined(const float (&v)[kCount], int lan
 
 // Softmax warps.  Warp w has slots 16 w .. 16 w + 15 of a page: thread t the
 // slots t / 4 and t / 4 + 8 of them, and columns 2 (t % 4) + {0, 1} of each 8.
-template <int N>
-__device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) {
+template <int N, typename F>
+__device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) {
   constexpr int kCols = N / 4;  // columns of a thread
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t tmem = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -1021,7 +1093,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N>& s, Walk w) 
       if (t == 0) s.rows = rows;
       return;
     }
-    write_rows<N>(p, s, rows, 0, 4 * N);
+    write_rows<N, F>(p, s, rows, 0, 4 * N);
     tc_fence_before();
     softmax_sync();  // s.red, s.factor and O are free again
     at += n;
@@ -1075,10 +1147,10 @@ __device__ __forceinline__ void write_empty(const AttendParams& p, int64_t r) {
   if (threadIdx.x < p.num_heads) p.lse[row0 + threadIdx.x] = p.sinks == nullptr ? -INFINITY : p.sinks[threadIdx.x];
 }
 
-template <int N>
+template <int N, typename F>
 __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(1024) uint8_t raw_shared[];
-  AttendShared<N>& s = *reinterpret_cast<AttendShared<N>*>(raw_shared);
+  AttendShared<N, F>& s = *reinterpret_cast<AttendShared<N, F>*>(raw_shared);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int cta = blockIdx.x;
   if (warp == kIssueWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
@@ -1093,7 +1165,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     dev::mbar_init(&s.bar.q_empty, 1);
     dev::mbar_init(&s.bar.o_full, 1);
     dev::mbar_init(&s.bar.drain, 1);
-    for (int i = 0; i < depth<N>() * ring_groups<N>(); ++i) {
+    for (int i = 0; i < depth<N, F>() * ring_groups<N, F>(); ++i) {
       dev::mbar_init(&s.bar.piece_full[0][0] + i, 1);
       dev::mbar_init(&s.bar.piece_empty[0][0] + i, 1);
     }
@@ -1211,20 +1283,23 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     w.left = count;
     if (warp < kSoftmaxWarps) {
       more_registers<kSoftmaxRegs>();
-      softmax_role<N>(p, s, w);
+      softmax_role<N, F>(p, s, w);
     } else {
       fewer_registers<kOtherRegs>();
       const int worker = 3 * (warp / 4 - 1) + warp % 4;  // of those not on the issuer's scheduler
       if (warp == kIssueWarp) {
-        issue_role<N>(p, s, count);
+        issue_role<N, F>(p, s, count);
       } else if (warp == kCopyWarp) {
-        copy_role<N>(p, s, w);
+        copy_role<N, F>(p, s, w);
       } else if (warp == kQueryWarp) {
-        query_role<N>(p, s, w);
+        query_role<N, F>(p, s, w);
       } else if (worker < kGroups) {
-        decode_role<N>(p, s, worker, count);
+        if constexpr (F::kFour)
+          decode4_role<N, F>(p, s, worker, count);
+        else
+          decode_role<N, F>(p, s, worker, count);
       } else if (worker == kGroups) {
-        rope_role<N>(p, s, count);
+        rope_role<N, F>(p, s, count);
       }
     }
   }
@@ -1232,7 +1307,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s.rows.heads > 0) write_rows<N>(p, s, s.rows, (warp >> 2) * N, (warp >> 2) * N + N);
+  if (s.rows.heads > 0) write_rows<N, F>(p, s, s.rows, (warp >> 2) * N, (warp >> 2) * N + N);
   if (p.alone) {
 #pragma unroll 1
     for (int r = cta; r < reqs; r += grid)
@@ -1470,11 +1545,11 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   }
 }
 
-template <int N>
+template <int N, typename F>
 cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(AttendShared<N>);
+  constexpr size_t smem = sizeof(AttendShared<N, F>);
   static_assert(smem <= 232448, "227 KB a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kvc_attend_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(kvc_attend_kernel<N, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1487,7 +1562,7 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N>, p);
+  e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N, F>, p);
   if (e != cudaSuccess || p.alone) return e;
   // as many as fit at once: they share the divided units' heads, then the requests,
   // one turn each (24 requests of up to 2050 slots, 32 heads: 22.6 us, in two turns 3 more)
@@ -1519,10 +1594,17 @@ bool attend_alone(const AttendParams& p, int ctas) {
 }
 
 cudaError_t launch_attend(const AttendParams& p, int columns, int ctas, cudaStream_t stream) {
+  if (p.four_bits) {
+    switch (columns) {
+      case 16: return launch_n<16, Slots4>(p, ctas, stream);
+      case 32: return launch_n<32, Slots4>(p, ctas, stream);
+      default: return launch_n<64, Slots4>(p, ctas, stream);
+    }
+  }
   switch (columns) {
-    case 16: return launch_n<16>(p, ctas, stream);
-    case 32: return launch_n<32>(p, ctas, stream);
-    default: return launch_n<64>(p, ctas, stream);
+    case 16: return launch_n<16, Slots8>(p, ctas, stream);
+    case 32: return launch_n<32, Slots8>(p, ctas, stream);
+    default: return launch_n<64, Slots8>(p, ctas, stream);
   }
 }
 

@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kvc_internal.h"
 #include "kvc_operators.h"
@@ -245,40 +246,44 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_long_kernel(const __
   }
 }
 
-// Eight moves by one warp: 8 x 36 pieces of 16 bytes are 9 a lane, and lanes
-// 0..7 have a move and its scale record each.
+// Eight moves by one warp: 8 x 36 pieces of 16 bytes are 9 a lane (8 x 22, up to
+// 6, of 4-bit slots), and lanes 0..7 have a move and its scale record each.
+template <typename F>
 __device__ __forceinline__ void move_eight(uint8_t* kv, longlong2 m, int count) {
+  constexpr int kPieces = F::kStride / 16, kTurns = (8 * kPieces + 31) / 32;
+  using Record = std::conditional_t<F::kScales == 16, uint4, uint2>;
   const int lane = threadIdx.x & 31;
   uint64_t dst = 0, src = 0;
-  uint2 scale = make_uint2(0, 0);
+  Record scale = {};
   uint8_t* scale_to = nullptr;
   if (lane < count) {
-    uint8_t* const to = kv + m.x / kSlotsPerPage * kPageBytes;
-    const uint8_t* const of = kv + m.y / kSlotsPerPage * kPageBytes;
+    uint8_t* const to = kv + m.x / kSlotsPerPage * F::kPage;
+    const uint8_t* const of = kv + m.y / kSlotsPerPage * F::kPage;
     const int p = static_cast<int>(m.x % kSlotsPerPage), q = static_cast<int>(m.y % kSlotsPerPage);
-    dst = reinterpret_cast<uint64_t>(to + p * kTokenStride);
-    src = reinterpret_cast<uint64_t>(of + q * kTokenStride);
-    scale_to = to + kScaleBase + p * kScaleDim;
-    scale = *reinterpret_cast<const uint2*>(of + kScaleBase + q * kScaleDim);
+    dst = reinterpret_cast<uint64_t>(to + p * F::kStride);
+    src = reinterpret_cast<uint64_t>(of + q * F::kStride);
+    scale_to = to + F::kScaleBase + p * F::kScales;
+    scale = *reinterpret_cast<const Record*>(of + F::kScaleBase + q * F::kScales);
   }
-  uint4 v[9];
+  uint4 v[kTurns];
 #pragma unroll
-  for (int k = 0; k < 9; ++k) {
-    const int slot = (32 * k + lane) / 36, piece = (32 * k + lane) - 36 * slot;
+  for (int k = 0; k < kTurns; ++k) {
+    const int slot = (32 * k + lane) / kPieces, piece = (32 * k + lane) - kPieces * slot;
     const uint64_t from = __shfl_sync(0xFFFFFFFFu, src, slot);
     if (slot < count) v[k] = *reinterpret_cast<const uint4*>(from + 16 * piece);
   }
 #pragma unroll
-  for (int k = 0; k < 9; ++k) {
-    const int slot = (32 * k + lane) / 36, piece = (32 * k + lane) - 36 * slot;
+  for (int k = 0; k < kTurns; ++k) {
+    const int slot = (32 * k + lane) / kPieces, piece = (32 * k + lane) - kPieces * slot;
     const uint64_t to = __shfl_sync(0xFFFFFFFFu, dst, slot);
     if (slot < count) *reinterpret_cast<uint4*>(to + 16 * piece) = v[k];
   }
-  if (lane < count) *reinterpret_cast<uint2*>(scale_to) = scale;
+  if (lane < count) *reinterpret_cast<Record*>(scale_to) = scale;
 }
 
 // The moves of a request by the warps of grid.y CTAs, which are all resident:
 // a warp asks for its next moves before it makes the present ones.
+template <typename F>
 __global__ void __launch_bounds__(kMoveWarps * 32, kMoveCtasPerSm) kvc_evict_move_kernel(
     const __grid_constant__ EvictParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, kMoveCtasPerSm) kvc_evict_mov
   for (; i < moves; i += step) {
     longlong2 next = make_longlong2(0, 0);
     if (lane < 8 && i + step + lane < moves) next = list[i + step + lane];
-    move_eight(p.kv_cache, m, min(8, moves - i));
+    move_eight<F>(p.kv_cache, m, min(8, moves - i));
     m = next;
   }
 }
@@ -337,7 +342,7 @@ __device__ uint32_t rank_slots(const bool* first, const bool* second, uint32_t* 
   return total;
 }
 
-template <bool kMoves>
+template <bool kMoves, typename F>
 __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint8_t raw_shared[];
   ShortShared& s = *reinterpret_cast<ShortShared*>(raw_shared);
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kSelectThreads) kvc_evict_short_kernel(const _
     if (moves == 0) return;
     for (int i = 8 * warp; i < moves; i += 8 * kSelectWarps) {
       const int of_list = min(i + (lane & 7), moves - 1);
-      move_eight(p.kv_cache, move_of(table, s.holes[of_list], s.movers[of_list]), min(8, moves - i));
+      move_eight<F>(p.kv_cache, move_of(table, s.holes[of_list], s.movers[of_list]), min(8, moves - i));
     }
   }
 }
@@ -487,26 +492,31 @@ cudaError_t launch(Kernel kernel, dim3 grid, int threads, size_t smem, const Evi
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-}  // namespace
-
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+template <typename F>
+cudaError_t launch_evict_of(const EvictParams& p, cudaStream_t stream) {
   const dim3 reqs(static_cast<unsigned>(p.num_reqs));
   cudaError_t e;
   if (p.max_slots > kShortSlots) {
     const size_t smem = sizeof(uint32_t) * (p.max_slots < kCachedKeys ? p.max_slots : kCachedKeys);
     e = launch(kvc_evict_long_kernel, reqs, kSelectThreads, smem, p, stream);
   } else if (p.move_stride <= kFewMoves) {
-    return launch(kvc_evict_short_kernel<true>, reqs, kSelectThreads, sizeof(ShortShared), p, stream);
-  } else {
-    e = launch(kvc_evict_short_kernel<false>, reqs, kSelectThreads, sizeof(ShortShared), p, stream);
+    return launch(kvc_evict_short_kernel<true, F>, reqs, kSelectThreads, sizeof(ShortShared), p, stream);
+  } else {  // (moves nothing: the same for both forms of slots)
+    e = launch(kvc_evict_short_kernel<false, Slots8>, reqs, kSelectThreads, sizeof(ShortShared), p, stream);
   }
   if (e != cudaSuccess || p.move_stride == 0) return e;
   // as many CTAs as fit at once, shared out evenly over the requests, and no
   // more than all the moves there can be need
   const int64_t wide = (p.move_stride + 8 * kMoveWarps - 1) / (8 * kMoveWarps);
   const int64_t share = kMoveCtasPerSm * 152 / p.num_reqs, most = share > 0 ? share : 1;
-  return launch(kvc_evict_move_kernel, dim3(reqs.x, static_cast<unsigned>(wide < most ? wide : most)),
+  return launch(kvc_evict_move_kernel<F>, dim3(reqs.x, static_cast<unsigned>(wide < most ? wide : most)),
                 kMoveWarps * 32, 0, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+  return p.four_bits ? launch_evict_of<Slots4>(p, stream) : launch_evict_of<Slots8>(p, stream);
 }
 
 }  // namespace kvc
