@@ -309,7 +309,8 @@ kvc_status kvc_dequantize(const uint8_t* kv_cache, int64_t num_kv_pages,
 
 /*
  * kvc_dequantize for pages of either form.  A 4-bit slot's values are exact in
- * fp32 and in bf16; out is 16-byte aligned for it.
+ * fp32 and in bf16; out is 16-byte aligned for it, num_slots at most 2^32 and
+ * num_kv_pages below 2^31.
  */
 kvc_status kvc_dequantize_format(const uint8_t* kv_cache, int32_t kv_format, int64_t num_kv_pages,
                                  const int64_t* slots, int64_t num_slots, void* out,
@@ -336,6 +337,8 @@ kvc_status kvc_dequantize_format(const uint8_t* kv_cache, int32_t kv_format, int
  *              named twice (its bytes would be of either row).
  * positions, ... , num_positions   as for kvc_rotate; num_axes 0 (and
  *              positions, pair_axes NULL): not turned.
+ *
+ * num_rows at most 2^32, num_kv_pages below 2^31.
  *
  * A slot beyond the last page, or a position outside the table, records
  * KVC_ERR_BAD_INDEX and leaves the slot as it was; the other rows are written.
@@ -368,7 +371,7 @@ kvc_status kvc_store(const void* x, int32_t x_dtype, int64_t x_row_stride, int64
  * num_axes     1 .. 4.
  * pair_axes    HOST array of 32 axes, or NULL where there is one axis.
  * cos_sin_cache  fp32 [num_positions, 64], 16-byte aligned.
- * num_tokens at most 2^32, num_heads at most 65535.
+ * num_tokens below 2^31, num_heads at most 65535.
  *
  * A position outside the table records KVC_ERR_BAD_INDEX and leaves the token's
  * rows of out as they were; positions of axes that no pair has are not read.

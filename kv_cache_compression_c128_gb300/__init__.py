@@ -129,6 +129,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def lib():
     """The loaded libkvc.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -497,29 +499,33 @@ def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
     """Read slots of a packed kv_cache back as [len(slots), 512] vectors
     (torch.float32 or torch.bfloat16) on the cache's device.  Pages of 23552
     bytes hold 4-bit slots, others 8-bit ones."""
-    import torch
-
+    torch = _torch or _load_torch()
     dtype = torch.float32 if dtype is None else dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype not in _dtype_codes:
         raise TypeError("dtype must be torch.float32 or torch.bfloat16")
-    dev = kv_cache.device
-    if dev.type != "cuda":
+    if not kv_cache.is_cuda:
         raise ValueError("kv_cache must be a CUDA tensor (there is no CPU path)")
-    _check(kv_cache, "kv_cache", torch.uint8, dev)
-    _check(slots, "slots", torch.int64, dev)
+    device = kv_cache.get_device()
+    if not _is_flat(kv_cache, torch.uint8, device):
+        _check(kv_cache, "kv_cache", torch.uint8, kv_cache.device)
+    if not _is_flat(slots, torch.int64, device):
+        _check(slots, "slots", torch.int64, kv_cache.device)
     M = slots.numel()
-    if out is None:
-        out = torch.empty((M, HEAD_DIM), dtype=dtype, device=dev)
-    _check(out, "out", dtype, dev)
-    four = kv_cache.dim() == 2 and kv_cache.shape[1] == KV4_PAGE_BYTES
-    if four and out.numel() < M * HEAD_DIM:
+    if out is not None and not _is_flat(out, dtype, device):
+        _check(out, "out", dtype, kv_cache.device)
+    shape = kv_cache.shape
+    four = len(shape) == 2 and shape[1] == KV4_PAGE_BYTES
+    if four and out is not None and out.numel() < M * HEAD_DIM:
         raise ValueError("out must hold len(slots) * 512 values")
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        st = kvc_dequantize_format(kv_cache.data_ptr(), KVC_FORMAT_4BIT if four else KVC_FORMAT_8BIT,
-                                   kv_cache.shape[0], slots.data_ptr(), M, out.data_ptr(),
-                                   KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32,
-                                   int(s.cuda_stream))
+
+    def call(raw):
+        nonlocal out
+        if out is None:
+            out = torch.empty((M, HEAD_DIM), dtype=dtype, device=kv_cache.device)
+        return kvc_dequantize_format(kv_cache.data_ptr(), KVC_FORMAT_4BIT if four else KVC_FORMAT_8BIT, shape[0],
+                                     slots.data_ptr(), M, out.data_ptr(), _dtype_codes[dtype], raw)
+
+    st = _run(call, device, stream)
     if st != KVC_OK:
         raise KvcError(st, "kvc_dequantize")
     return out
@@ -722,6 +728,7 @@ def compress_layers(state_caches, token_to_req, positions, boundary_token_indice
 # the checks below read each attribute once and make no objects in passing.
 
 _torch = None
+_dtype_codes = {}  # of the element types, KVC_DTYPE_*
 
 
 def _load_torch():
@@ -729,8 +736,13 @@ def _load_torch():
     if _torch is None:
         import torch
 
+        _dtype_codes.update({torch.float32: KVC_DTYPE_F32, torch.bfloat16: KVC_DTYPE_BF16})
         _torch = torch
     return _torch
+
+
+def _is_flat(t, dtype, device):
+    return isinstance(t, _torch.Tensor) and t.dtype == dtype and t.get_device() == device and t.is_contiguous()
 
 
 def _refuse(name, t, dtype, dim, device):
@@ -809,7 +821,7 @@ def _run(call, device, stream):
     """call(raw stream), on the operator's device and stream."""
     cuda = _torch.cuda
     if stream is None:
-        if cuda.current_device() == device:
+        if _torch._C._cuda_getDevice() == device:  # (a tensor of the device is there: CUDA is up)
             return call(_torch._C._cuda_getCurrentRawStream(device))
     elif stream.device.index != device:  # (its context would make the other device current)
         raise ValueError(f"stream must be one of cuda:{device}, got one of {stream.device}")
@@ -817,33 +829,47 @@ def _run(call, device, stream):
         return call(cuda.current_stream(device).cuda_stream)
 
 
+_known_axes = {None: (1, None)}  # of what `axes` was found right for: (axes that positions have at least, bytes)
+
+
+def _axes(axes):
+    """(axes that positions have at least, the 32 bytes of a C call)"""
+    pairs = bytes(axes)
+    if len(pairs) != 32:
+        raise ValueError("axes must name an axis of positions for each of the 32 pairs")
+    known = (max(pairs) + 1, pairs)
+    if len(_known_axes) < 64:
+        _known_axes[pairs] = known
+    return known
+
+
 def _rotation(positions, cos_sin_cache, axes, rows, device):
     """(positions, row stride, axis stride, axes, pair axes, table, its rows) of a
     C call that turns `rows` rows."""
-    if not isinstance(positions, _torch.Tensor) or positions.dtype != _torch.int64 or positions.get_device() != device:
-        _refuse("positions", positions, _torch.int64, 2, device)
+    int64, float32 = _torch.int64, _torch.float32
+    if not isinstance(positions, _torch.Tensor) or positions.dtype != int64 or positions.get_device() != device:
+        _refuse("positions", positions, int64, 2, device)
     shape, stride = positions.shape, positions.stride()
-    count = 1
+    count, apart = 1, 0
     if len(shape) == 2:
-        count = shape[1]
+        count, apart = shape[1], stride[1]
     elif len(shape) != 1:
         raise ValueError("positions must be [rows] or [rows, axes]")
     if shape[0] != rows:
         raise ValueError("positions must have one row for each of x")
     if not 1 <= count <= 4:
         raise ValueError("positions must have 1 to 4 axes")
-    if axes is not None:
-        if type(axes) is not bytes:
-            axes = bytes(axes)
-        if len(axes) != 32 or max(axes) >= count:
-            raise ValueError("axes must name an axis of positions for each of the 32 pairs")
-    elif count > 1:
+    least, pairs = (_known_axes.get(axes) if axes is None or type(axes) is bytes else None) or _axes(axes)
+    if least > count:
+        raise ValueError("axes must name an axis of positions for each of the 32 pairs")
+    if pairs is None and count > 1:
         raise ValueError("positions of several axes need axes, one for each of the 32 pairs")
-    entries, width, _ = _rows("cos_sin_cache", cos_sin_cache, _torch.float32, device)
-    if width != ROPE_DIM or not cos_sin_cache.is_contiguous():
+    if not _is_flat(cos_sin_cache, float32, device) or cos_sin_cache.dim() != 2:
+        _refuse("cos_sin_cache", cos_sin_cache, float32, 2, device)
+    entries, width = cos_sin_cache.shape
+    if width != ROPE_DIM:
         raise ValueError("cos_sin_cache must be contiguous [num_positions, 64]")
-    return (positions.data_ptr(), stride[0], stride[1] if len(shape) == 2 else 0, count, axes,
-            cos_sin_cache.data_ptr(), entries)
+    return positions.data_ptr(), stride[0], apart, count, pairs, cos_sin_cache.data_ptr(), entries
 
 
 def store(x, kv_cache, slots, *, positions=None, cos_sin_cache=None, axes=None, stream=None):
@@ -863,9 +889,10 @@ def store(x, kv_cache, slots, *, positions=None, cos_sin_cache=None, axes=None, 
     """
     torch = _torch or _load_torch()
     device, pages, form = _pages(kv_cache)
-    if not isinstance(x, torch.Tensor) or (x.dtype != torch.bfloat16 and x.dtype != torch.float32):
+    if not isinstance(x, torch.Tensor) or x.dtype not in _dtype_codes:
         raise TypeError("x must be a tensor of dtype torch.float32 or torch.bfloat16")
-    N, D, row = _rows("x", x, x.dtype, device)
+    dtype = x.dtype
+    N, D, row = _rows("x", x, dtype, device)
     if D != HEAD_DIM:
         raise ValueError("x must be [rows, 512]")
     _dense("slots", slots, torch.int64, device, (N,))
@@ -876,9 +903,8 @@ def store(x, kv_cache, slots, *, positions=None, cos_sin_cache=None, axes=None, 
         raise ValueError("axes and cos_sin_cache need positions")
 
     def call(raw):
-        return kvc_store(
-            x.data_ptr(), KVC_DTYPE_BF16 if x.dtype == torch.bfloat16 else KVC_DTYPE_F32, row if N > 1 else 0,
-            N, kv_cache.data_ptr(), form, pages, slots.data_ptr(), *turn, raw)
+        return kvc_store(x.data_ptr(), _dtype_codes[dtype], row if N > 1 else 0, N, kv_cache.data_ptr(), form, pages,
+                         slots.data_ptr(), *turn, raw)
 
     st = _run(call, device, stream)
     if st != KVC_OK:
@@ -894,8 +920,7 @@ def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out
     [T, H, 512], for instance); positions int64 [T] or [T, 1..4 axes] (any
     strides); cos_sin_cache fp32 [P, 64], cos in columns 0..31, sin 32..63.  Pair
     i (dims 2 i, 2 i + 1) is turned by the angle in column i at the position of
-    axis axes[i]: 32 numbers (bytes are taken as they are), not needed for one
-    axis.
+    axis axes[i]: 32 numbers (quickest as bytes), not needed for one axis.
 
     `inverse` turns by the opposite angles: attention's rows back, whose last 64
     dims are sums of rotated ones, and the gradient with respect to x from the
@@ -907,28 +932,33 @@ def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out
     torch = _torch or _load_torch()
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA tensor (there is no CPU path)")
-    device, dtype, shape = x.get_device(), x.dtype, x.shape
-    if dtype != torch.bfloat16 and dtype != torch.float32:
+    device, dtype, shape, strides = x.get_device(), x.dtype, x.shape, x.stride()
+    code = _dtype_codes.get(dtype)
+    if code is None:
         raise TypeError("x must have dtype torch.float32 or torch.bfloat16")
-    if not 2 <= len(shape) <= 3 or shape[-1] != ROPE_DIM or (x.stride(-1) != 1 and x.numel() > 0):
+    T, H, D, by_token, by_head, by_dim = 0, 1, 0, 0, 0, 0
+    if len(shape) == 3:
+        T, H, D = shape
+        by_token, by_head, by_dim = strides
+    elif len(shape) == 2:
+        T, D = shape
+        by_token, by_dim = strides
+    if D != ROPE_DIM or (by_dim != 1 and T * H > 0):
         raise ValueError("x must be [tokens, heads, 64] or [tokens, 64] with contiguous columns")
-    T, H = shape[0], shape[1] if len(shape) == 3 else 1
     turn = _rotation(positions, cos_sin_cache, axes, T, device)
     if out is not None:
-        if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != device or out.dim() != len(shape):
+        if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != device:
             _refuse("out", out, dtype, len(shape), device)
-        if out.shape != shape or (out.stride(-1) != 1 and out.numel() > 0):
+        if out.shape != shape or (out.stride(-1) != 1 and T * H > 0):
             raise ValueError(f"out must be {tuple(shape)} with contiguous columns")
 
     def call(raw):
         nonlocal out
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=x.device)
-        xs, os = x.stride(), out.stride()
-        return kvc_rotate(
-            x.data_ptr(), KVC_DTYPE_BF16 if dtype == torch.bfloat16 else KVC_DTYPE_F32, xs[0] if T > 1 else 0,
-            xs[1] if H > 1 else 0, T, H, *turn, 1 if inverse else 0, out.data_ptr(), os[0] if T > 1 else 0,
-            os[1] if H > 1 else 0, raw)
+        to = out.stride()
+        return kvc_rotate(x.data_ptr(), code, by_token if T > 1 else 0, by_head if H > 1 else 0, T, H, *turn,
+                          1 if inverse else 0, out.data_ptr(), to[0] if T > 1 else 0, to[1] if H > 1 else 0, raw)
 
     st = _run(call, device, stream)
     if st != KVC_OK:

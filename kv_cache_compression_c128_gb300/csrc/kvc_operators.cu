@@ -357,7 +357,7 @@ kvc_status kvc_store(const void* x, int32_t x_dtype, int64_t x_row_stride, int64
   if (num_axes == 0 && (positions != nullptr || pair_axes != nullptr)) return KVC_ERR_INVALID_ARG;
   if (num_rows == 0) return KVC_OK;
   p.x_f32 = x_dtype == KVC_DTYPE_F32;
-  if (x == nullptr || kv_cache == nullptr || slots == nullptr || num_kv_pages <= 0 || !aligned(x, 16) ||
+  if (x == nullptr || kv_cache == nullptr || slots == nullptr || num_kv_pages <= 0 || num_kv_pages > INT32_MAX || !aligned(x, 16) ||
       !aligned(kv_cache, 16) || !aligned(slots, 8) || x_row_stride < 0 ||
       x_row_stride % (p.x_f32 ? 4 : 8) != 0)
     return KVC_ERR_INVALID_ARG;
@@ -384,7 +384,7 @@ kvc_status kvc_dequantize_format(const uint8_t* kv_cache, int32_t kv_format, int
   if (num_slots < 0 || num_slots > kMaxRows || (out_dtype != KVC_DTYPE_F32 && out_dtype != KVC_DTYPE_BF16))
     return KVC_ERR_INVALID_ARG;
   if (num_slots == 0) return KVC_OK;
-  if (kv_cache == nullptr || slots == nullptr || out == nullptr || num_kv_pages <= 0 || !aligned(kv_cache, 16) ||
+  if (kv_cache == nullptr || slots == nullptr || out == nullptr || num_kv_pages <= 0 || num_kv_pages > INT32_MAX || !aligned(kv_cache, 16) ||
       !aligned(slots, 8) || !aligned(out, 16))
     return KVC_ERR_INVALID_ARG;
   int sms = 0;
@@ -419,8 +419,7 @@ kvc_status kvc_rotate(const void* x, int32_t dtype, int64_t x_token_stride, int6
       x_head_stride % piece != 0 || out_token_stride % piece != 0 || out_head_stride % piece != 0 ||
       !heads_apart(num_tokens, out_token_stride, num_heads, out_head_stride))
     return KVC_ERR_INVALID_ARG;
-  // (as many CTAs as a launch can have; 2^38 rows of 64)
-  if (num_tokens * ((num_heads + 3) / 4) > int64_t{1} << 35) return KVC_ERR_UNSUPPORTED;
+  if (num_tokens > INT32_MAX) return KVC_ERR_UNSUPPORTED;  // (a launch has no more CTAs)
   int sms = 0;
   long long wait_limit = 0;
   const kvc_status st = kvc::operator_device(&sms, &p.error, &wait_limit);

@@ -10,67 +10,54 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kvc_operators.h"
 
 namespace kvc {
 
-// Of pairs first .. first + kCount - 1 (first a multiple of kCount).
+__device__ __forceinline__ int pair_axis(const Rotation& r, int pair) {
+  return static_cast<int>(r.axes >> (2 * pair)) & 3;
+}
+
+// (cos, sin) of a pair at a position that lies in the table.
+__device__ __forceinline__ float2 pair_angle(const Rotation& r, int64_t position, int pair) {
+  const float* const entry = r.table + position * kRopeDim + pair;
+  return make_float2(entry[0], entry[kPairs]);
+}
+
+// The angles of pairs first .. first + kCount - 1 (first a multiple of kCount) of a
+// row; false if a position lies outside the table.
 template <int kCount>
-struct Angles {
-  float cos[kCount], sin[kCount];
-
-  // False if a position lies outside the table; the angles are then 0.
-  __device__ __forceinline__ bool load(const Rotation& r, int64_t row, int first) {
-    const int64_t* const at = r.positions + row * r.row_stride;
-    const uint32_t axes = static_cast<uint32_t>(r.axes >> (2 * first)) & ((1u << (2 * kCount)) - 1);
-    bool ok = true;
-    // one axis for all of them: its number in every place
-    if (axes == (axes & 3u) * (((1u << (2 * kCount)) - 1) / 3)) {
-      int64_t pos = at[(axes & 3u) * r.axis_stride];
-      ok = static_cast<uint64_t>(pos) < static_cast<uint64_t>(r.num_positions);
-      const float* const entry = r.table + (ok ? pos : 0) * kRopeDim + first;
-      load_run(entry, cos);
-      load_run(entry + kPairs, sin);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCount; ++i) {
-        const int64_t pos = at[(axes >> (2 * i) & 3u) * r.axis_stride];
-        const bool in = static_cast<uint64_t>(pos) < static_cast<uint64_t>(r.num_positions);
-        const float* const entry = r.table + (in ? pos : 0) * kRopeDim + first + i;
-        cos[i] = entry[0];
-        sin[i] = entry[kPairs];
-        ok = ok && in;
-      }
-    }
-    return ok;
-  }
-
-  __device__ __forceinline__ void invert() {
-#pragma unroll
-    for (int i = 0; i < kCount; ++i) sin[i] = -sin[i];
-  }
-
-  __device__ __forceinline__ void turn(float* x) const {
+__device__ __forceinline__ bool load_angles(const Rotation& r, int64_t row, int first, float (&cos)[kCount], float (&sin)[kCount]) {
+  static_assert(kCount == 2 || kCount == 4, "pairs in 16 bytes of a row");
+  using Run = std::conditional_t<kCount == 4, float4, float2>;
+  const int64_t* const at = r.positions + row * r.row_stride;
+  const uint32_t axes = static_cast<uint32_t>(r.axes >> (2 * first)) & ((1u << (2 * kCount)) - 1);
+  bool ok = true;
+  if (axes == (axes & 3u) * (((1u << (2 * kCount)) - 1) / 3)) {  // one axis: its number in every place
+    const int64_t position = at[(axes & 3u) * r.axis_stride];
+    ok = static_cast<uint64_t>(position) < static_cast<uint64_t>(r.num_positions);
+    const float* const entry = r.table + (ok ? position : 0) * kRopeDim + first;
+    *reinterpret_cast<Run*>(cos) = *reinterpret_cast<const Run*>(entry);
+    *reinterpret_cast<Run*>(sin) = *reinterpret_cast<const Run*>(entry + kPairs);
+  } else {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = __fsub_rn(__fmul_rn(a, cos[i]), __fmul_rn(b, sin[i]));
-      x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cos[i]), __fmul_rn(a, sin[i]));
+      const int64_t position = at[(axes >> (2 * i) & 3u) * r.axis_stride];
+      const bool in = static_cast<uint64_t>(position) < static_cast<uint64_t>(r.num_positions);
+      const float2 angle = pair_angle(r, in ? position : 0, first + i);
+      cos[i] = angle.x;
+      sin[i] = angle.y;
+      ok = ok && in;
     }
   }
+  return ok;
+}
 
- private:
-  __device__ __forceinline__ static void load_run(const float* src, float* dst) {
-    if constexpr (kCount == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      dst[0] = v.x, dst[1] = v.y, dst[2] = v.z, dst[3] = v.w;
-    } else {
-      static_assert(kCount == 2, "pairs in 16 bytes of a row");
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      dst[0] = v.x, dst[1] = v.y;
-    }
-  }
-};
+__device__ __forceinline__ float2 turn_pair(float2 x, float cos, float sin) {
+  return make_float2(__fsub_rn(__fmul_rn(x.x, cos), __fmul_rn(x.y, sin)),
+                     __fadd_rn(__fmul_rn(x.y, cos), __fmul_rn(x.x, sin)));
+}
 
 }  // namespace kvc

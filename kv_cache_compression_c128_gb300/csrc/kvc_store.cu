@@ -9,9 +9,14 @@
 //     positions, one rounding per operation in fp32, then bf16.
 // The 8-bit form is what the compressor stores for the same vector.
 //
-// A warp has a row: lane l dims 8 l .. + 7 and 256 + 8 l .. + 7, so that every load
-// and store covers one run of the row, a scale group is 4 or 8 lanes, and lanes
-// 24 .. 31 of the second half hold the rotated dims.
+// A warp has a row: lane l dims 8 l .. + 7, 256 + 8 l .. + 7 and pair l of the rotated
+// ones, so that every load and store covers one run of the row, a scale group is 4 or
+// 8 lanes, and each lane asks for one angle.  Large calls are bound by the rows in and
+// the slots out: 65537 fp32 rows to 8-bit slots take 25.8 us (99 % of the copy
+// bandwidth), to 4-bit ones turned to one axis 26.9 (97 %); bf16 rows to 4 bits with
+// three axes 19.1 (85 %), which is near what its instructions take to issue.  (Two rows
+// a warp: 29.8, 30.1, 21.7.  Codes by division, angles by the eight lanes of the
+// rotated dims: 340 instructions a row, 26.7 us for the last.)
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -19,6 +24,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "kvc_codes.cuh"
 #include "kvc_device.cuh"
 #include "kvc_internal.h"
 #include "kvc_operators.h"
@@ -28,48 +34,91 @@ namespace kvc {
 namespace {
 
 constexpr int kWarps = 8;
+// Slots to read up to which a warp has one: with more, the card is full of warps.
+constexpr int64_t kFewRows = 152 * 64;
 
-// 8 values as 4 words of bf16.
-__device__ __forceinline__ uint4 round8(const float (&x)[8]) {
-  uint32_t w[4];
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// ---- codes: 8 values of a lane -----------------------------------------------------
+
+// The largest magnitudes of each lane's two runs of 8 as bits of bf16, whose order
+// is that of the values, infinities and NaN above all: the first's in the low half.
+__device__ __forceinline__ uint32_t most_of(const uint4& v) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs));
+}
+template <int kLanes>
+__device__ __forceinline__ uint32_t most_of_groups(const uint4& v, const uint4& w) {
+  const uint32_t a = most_of(v), b = most_of(w);
+  uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  return m;
+}
+
+// Each half of the words in magnitude at most `most` (bits of bf16), NaN as 0.
+__device__ __noinline__ uint4 bring_in(uint4 v, uint32_t most) {
+  uint32_t* const words = &v.x;
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    uint32_t out = 0;
+    for (int h = 0; h < 32; h += 16) {
+      const uint32_t x = words[i] >> h & 0xFFFFu, size = x & 0x7FFFu;
+      out |= (size > 0x7F80u ? 0u : (x & 0x8000u) | min(size, most)) << h;
+    }
+    words[i] = out;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return v;
 }
 
-// The largest magnitude of 8 values, NaN passed over.
-__device__ __forceinline__ float most8(const float (&z)[8]) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(z[i]));
-  return a;
-}
+// 7 times the largest scale of 4-bit slots, as bf16: 105 x 2^12.
+constexpr uint32_t kMost4 = 0x48D2;
 
-// The scale byte of a group whose largest magnitude is a.  Where 7 s = a holds, a / 7
-// in fp32 is s; elsewhere it is 2^-9 of s or more away from every s (both are
-// multiples of the same power of two), so rounding up to 4 significant bits is exact.
+// The scale byte of a 4-bit group, a <= 7 times the largest scale.  A bf16 a that is
+// not 7 s lies 2^-9 of s or more from it (both are multiples of one power of two), so
+// a little less than a / 7, rounded up to 4 significant bits, is the scale sought.
 __device__ __forceinline__ uint32_t scale_byte(float a) {
-  const uint32_t up = (__float_as_uint(__fdiv_rn(a, 7.f)) + 0xFFFFFu) >> 20;  // 8 exponent + 3 mantissa bits
+  const uint32_t up = (__float_as_uint(__fmul_rn(a, (1.f - 0x1p-16f) / 7.f)) + 0xFFFFFu) >> 20;
   constexpr int kLeast = (127 - 16) * 8;
-  return static_cast<uint32_t>(max(0, min(255, static_cast<int>(up) - kLeast)));
+  return static_cast<uint32_t>(max(0, static_cast<int>(up) - kLeast));
 }
 
-// 8 codes of the group with scale s, 8 above themselves.
-__device__ __forceinline__ uint32_t codes4(const float (&z)[8], float s) {
+// 8 codes of 4 bits, each 8 above itself.  z / s is a half or 2^-10 and more from
+// one, by the same argument, so z times a little more than 1 / s, rounded to the
+// nearest whole number by the sum with 2^23, has its halves rounded away from zero.
+__device__ __forceinline__ uint32_t codes4(const uint4& w, uint32_t byte) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float((byte << 20) + ((127 - 16) << 23))));
+  r = __fmul_rn(r, 1.f + 0x1p-16f);
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
   uint32_t word = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // |z| / s is exact at halves, and 2^-9 or more away from them elsewhere
-    const float size = fminf(floorf(__fdiv_rn(fabsf(z[i]), s) + 0.5f), 7.f);
-    const int q = z[i] == z[i] ? static_cast<int>(copysignf(size, z[i])) : 0;
-    word |= static_cast<uint32_t>(q + 8) << (4 * (i >> 1) + 16 * (i & 1));
+  for (int i = 3; i >= 0; --i) {
+    const uint32_t even = __float_as_uint(__fmaf_rn(dev::bf16_lo(words[i]), r, 8388616.f));
+    const uint32_t odd = __float_as_uint(__fmaf_rn(dev::bf16_hi(words[i]), r, 8388616.f));
+    word = word * 16 + __byte_perm(even, odd, 0x5410);  // below 2^23 the sum's bits are the number
   }
   return word;
 }
 
+// 8 codes of 8 bits with the scale 2^e: z 2^-e is exact, and at most 127 in size unless
+// it is infinite.
+__device__ __forceinline__ uint2 codes8(const uint4& w, int e) {
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  uint32_t two[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int lo = max(-127, min(127, __float2int_rz(__fmul_rn(dev::bf16_lo(words[i]), inv))));
+    const int hi = max(-127, min(127, __float2int_rz(__fmul_rn(dev::bf16_hi(words[i]), inv))));
+    two[i] = __byte_perm(lo, hi, 0x0040);
+  }
+  return make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410));
+}
+
+// Lane l has dims 8 l .. + 7, if l < 24 256 + 8 l .. + 7, and pair l of the rotated ones.
 template <typename F, bool kF32>
 __global__ void __launch_bounds__(kWarps * 32) kvc_store_kernel(const __grid_constant__ StoreParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -78,145 +127,183 @@ __global__ void __launch_bounds__(kWarps * 32) kvc_store_kernel(const __grid_con
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (row >= p.num_rows) return;
   const int64_t slot = p.slots[row];
-  if (slot < 0) return;
-  const int64_t page = slot / kSlotsPerPage;
-  const int place = static_cast<int>(slot % kSlotsPerPage);
-  float x[2][8];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t at = row * p.x_row_stride + 256 * k + 8 * lane;
-    if constexpr (kF32) {
-      const float4* const src = reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + at);
-      const float4 a = src[0], b = src[1];
-      x[k][0] = a.x, x[k][1] = a.y, x[k][2] = a.z, x[k][3] = a.w;
-      x[k][4] = b.x, x[k][5] = b.y, x[k][6] = b.z, x[k][7] = b.w;
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + at);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[k][2 * i] = dev::bf16_lo(w[i]), x[k][2 * i + 1] = dev::bf16_hi(w[i]);
+  const bool turns = p.rotation.positions != nullptr;
+  int64_t at = 0;
+  if (turns) at = p.rotation.positions[row * p.rotation.row_stride + pair_axis(p.rotation, lane) * p.rotation.axis_stride];
+  uint4 v, w = make_uint4(0, 0, 0, 0);
+  float2 pair;
+  if constexpr (kF32) {
+    const float* const src = static_cast<const float*>(p.x) + row * p.x_row_stride;
+    const float4 a = reinterpret_cast<const float4*>(src)[2 * lane], b = reinterpret_cast<const float4*>(src)[2 * lane + 1];
+    v = make_uint4(round2(a.x, a.y), round2(a.z, a.w), round2(b.x, b.y), round2(b.z, b.w));
+    if (lane < 24) {
+      const float4 c = reinterpret_cast<const float4*>(src)[64 + 2 * lane], d = reinterpret_cast<const float4*>(src)[65 + 2 * lane];
+      w = make_uint4(round2(c.x, c.y), round2(c.z, c.w), round2(d.x, d.y), round2(d.z, d.w));
     }
+    pair = reinterpret_cast<const float2*>(src)[kNopeDim / 2 + lane];
+  } else {
+    const uint16_t* const src = static_cast<const uint16_t*>(p.x) + row * p.x_row_stride;
+    v = reinterpret_cast<const uint4*>(src)[lane];
+    if (lane < 24) w = reinterpret_cast<const uint4*>(src)[32 + lane];
+    const uint32_t two = reinterpret_cast<const uint32_t*>(src)[kNopeDim / 2 + lane];
+    pair = make_float2(dev::bf16_lo(two), dev::bf16_hi(two));
   }
-  const bool rope = lane >= 24;  // of the second half
-  bool ok = page < p.num_pages;
-  if (p.rotation.positions != nullptr && rope) {
-    Angles<4> angles;
-    ok = angles.load(p.rotation, row, 4 * (lane - 24)) && ok;
-    angles.turn(x[1]);
+  if (slot < 0) return;
+  bool ok = slot < p.num_pages * kSlotsPerPage;
+  if (turns) {
+    const bool in = static_cast<uint64_t>(at) < static_cast<uint64_t>(p.rotation.num_positions);
+    const float2 angle = pair_angle(p.rotation, in ? at : 0, lane);
+    pair = turn_pair(pair, angle.x, angle.y);
+    ok = ok && in;
   }
   if (!__all_sync(0xFFFFFFFFu, ok)) {
     if (lane == 0) dev::record_error(p.error, dev::kErrBadIndex);
     return;
   }
-  uint8_t* const base = p.kv_cache + page * F::kPage;
+  const uint32_t place = static_cast<uint32_t>(slot) % kSlotsPerPage;
+  uint8_t* const base = p.kv_cache + static_cast<uint64_t>(static_cast<uint32_t>(slot / kSlotsPerPage)) * F::kPage;
   uint8_t* const payload = base + place * F::kStride;
   uint8_t* const scales = base + F::kScaleBase + place * F::kScales;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint4 w = round8(x[k]);
-    if (k == 1 && rope) *reinterpret_cast<uint4*>(payload + F::kCodes + 16 * (lane - 24)) = w;
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) z[2 * i] = dev::bf16_lo(words[i]), z[2 * i + 1] = dev::bf16_hi(words[i]);
-    float a = most8(z);
-    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-    if constexpr (F::kFour) {
-      const uint32_t byte = k == 1 && rope ? 0u : scale_byte(a);  // (two bytes behind the 14 scales are zero)
-      if (!(k == 1 && rope))
-        *reinterpret_cast<uint32_t*>(payload + 4 * (32 * k + lane)) =
-            codes4(z, __uint_as_float((byte + (127 - 16) * 8) << 20));
-      if ((lane & 3) == 0) scales[8 * k + lane / 4] = static_cast<uint8_t>(byte);
-    } else {
-      a = fmaxf(fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 4)), 1.0e-4f);
-      const int e = dev::scale_exponent(a);
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
-      uint32_t code[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int q = max(-127, min(127, __float2int_rz(__fmul_rn(z[i], inv))));
-        code[i >> 2] |= static_cast<uint32_t>(q & 0xFF) << (8 * (i & 3));
-      }
-      if (!(k == 1 && rope)) *reinterpret_cast<uint2*>(payload + 8 * (32 * k + lane)) = make_uint2(code[0], code[1]);
-      if ((lane & 7) == 0) scales[4 * k + lane / 8] = static_cast<uint8_t>(k == 1 && rope ? 0 : e + 127);
+  reinterpret_cast<uint32_t*>(payload + F::kCodes)[lane] = round2(pair.x, pair.y);
+  constexpr int kLanes = F::kFour ? 4 : 8;
+  constexpr uint32_t kMost = F::kFour ? kMost4 : 0x7F80u;
+  uint32_t m = most_of_groups<kLanes>(v, w);
+  // above what a scale holds, or NaN (8 bits: infinities stay as they are)
+  if (__any_sync(0xFFFFFFFFu, (m & 0xFFFFu) > kMost || m >> 16 > kMost)) {
+    v = bring_in(v, kMost);
+    w = bring_in(w, kMost);
+    m = most_of_groups<kLanes>(v, w);
+  }
+  const float a = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
+  if constexpr (F::kFour) {
+    // (two bytes behind the 14 scales are zero: lanes 24 .. 31 hold no second run)
+    const uint32_t byte0 = scale_byte(a), byte1 = scale_byte(b);
+    reinterpret_cast<uint32_t*>(payload)[lane] = codes4(v, byte0);
+    if (lane < 24) reinterpret_cast<uint32_t*>(payload)[32 + lane] = codes4(w, byte1);
+    if ((lane & 3) == 0) {
+      scales[lane / 4] = static_cast<uint8_t>(byte0);
+      scales[8 + lane / 4] = static_cast<uint8_t>(byte1);
+    }
+  } else {
+    const int e0 = dev::scale_exponent(fmaxf(a, 1.0e-4f)), e1 = dev::scale_exponent(fmaxf(b, 1.0e-4f));
+    reinterpret_cast<uint2*>(payload)[lane] = codes8(v, e0);
+    if (lane < 24) reinterpret_cast<uint2*>(payload)[32 + lane] = codes8(w, e1);
+    if ((lane & 7) == 0) {
+      scales[lane / 8] = static_cast<uint8_t>(e0 + 127);
+      scales[4 + lane / 8] = static_cast<uint8_t>(lane < 24 ? e1 + 127 : 0);
     }
   }
 }
 
-// A warp has a slot: lane l dims 4 l + 128 k .. + 3, k < 4, so that every store of
-// fp32 values covers one run.
-template <bool kBf16>
+// ---- 4-bit slots back ---------------------------------------------------------------
+
+// A warp has kSlots slots, all loads of all of them ahead of the first store.  Where
+// bf16 is asked for, lane l has dims 8 l .. + 7 and 256 + 8 l .. + 7 of each; of fp32
+// values dims 4 l + 128 k .. + 3, k < 4: every store covers one run.
+template <bool kBf16, int kSlots>
 __global__ void __launch_bounds__(kWarps * 32) kvc_dequantize4_kernel(const uint8_t* kv, int64_t num_pages,
                                                                       const int64_t* slots, int64_t num_slots, void* out,
                                                                       uint32_t* err) {
   using F = Slots4;
+  constexpr int kParts = kBf16 ? 2 : 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (m >= num_slots) return;
-  const int64_t slot = slots[m], page = slot / kSlotsPerPage;
-  const bool there = slot >= 0 && page < num_pages;
-  if (slot >= 0 && !there && lane == 0) dev::record_error(err, dev::kErrBadIndex);
-  const uint8_t* const base = kv + (there ? page : 0) * F::kPage;
-  const int place = there ? static_cast<int>(slot % kSlotsPerPage) : 0;
-  const uint8_t* const payload = base + place * F::kStride;
-  const uint8_t* const scales = base + F::kScaleBase + place * F::kScales;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kSlots;
+  if (first >= num_slots) return;
+  const bool rope = lane >= (kBf16 ? 24 : 16);  // of the last part
+  int64_t slot[kSlots];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (there && k == 3 && lane >= 16) {
-      const uint2 w = *reinterpret_cast<const uint2*>(payload + F::kCodes + 8 * (lane - 16));
-      v[0] = dev::bf16_lo(w.x), v[1] = dev::bf16_hi(w.x), v[2] = dev::bf16_lo(w.y), v[3] = dev::bf16_hi(w.y);
-    } else if (there) {
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(payload + 4 * (16 * k + lane / 2)) >> (8 * (lane & 1));
-      const float s = __uint_as_float((scales[4 * k + lane / 8] + (127u - 16u) * 8u) << 20);
+  for (int u = 0; u < kSlots; ++u) slot[u] = first + u < num_slots ? slots[first + u] : -1;
+  uint32_t words[kSlots][kParts];
+  uint4 tail[kSlots], scale[kSlots];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = (static_cast<int>(word >> (4 * (i >> 1) + 16 * (i & 1)) & 15u) - 8) * s;
+  for (int u = 0; u < kSlots; ++u) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) words[u][k] = 0x88888888u;  // zeros
+    tail[u] = scale[u] = make_uint4(0, 0, 0, 0);
+    if (slot[u] < 0) continue;
+    if (slot[u] >= num_pages * kSlotsPerPage) {
+      if (lane == 0) dev::record_error(err, dev::kErrBadIndex);
+      continue;
     }
-    const int64_t at = m * kHeadDim + 128 * k + 4 * lane;
-    if constexpr (kBf16) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    const uint8_t* const base = kv + slot[u] / kSlotsPerPage * F::kPage;
+    const int place = static_cast<int>(slot[u] % kSlotsPerPage);
+    const uint8_t* const payload = base + place * F::kStride;
+    scale[u] = *reinterpret_cast<const uint4*>(base + F::kScaleBase + place * F::kScales);
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      if (k < kParts - 1 || !rope) {
+        words[u][k] = *reinterpret_cast<const uint32_t*>(payload + (kBf16 ? 4 * (32 * k + lane) : 4 * (16 * k + lane / 2)));
+      } else if constexpr (kBf16) {
+        tail[u] = *reinterpret_cast<const uint4*>(payload + F::kCodes + 16 * (lane - 24));
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(payload + F::kCodes + 8 * (lane - 16));
+        tail[u].x = v.x, tail[u].y = v.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kSlots; ++u) {
+    if (first + u >= num_slots) break;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      // the scale byte of group 8 k + l / 4, or 4 k + l / 8
+      uint32_t record;
+      if constexpr (kBf16)
+        record = k == 0 ? (lane < 16 ? scale[u].x : scale[u].y) : (lane < 16 ? scale[u].z : scale[u].w);
+      else
+        record = k == 0 ? scale[u].x : k == 1 ? scale[u].y : k == 2 ? scale[u].z : scale[u].w;
+      const uint32_t byte = record >> (8 * (kBf16 ? lane / 4 & 3 : lane / 8)) & 0xFFu;
+      const uint32_t s = byte * 0x00100010u + kScale4Bits * 0x00010001u, less = mul_bf16x2(s, 0xC308C308u);
+      const bool tails = k == kParts - 1 && rope;
+      if constexpr (kBf16) {
+        uint4 v = decode8_bf16(words[u][k], s, less);
+        if (tails) v = tail[u];
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (first + u) * kHeadDim)[32 * k + lane] = v;
+      } else {
+        const uint32_t half = words[u][k] >> (8 * (lane & 1));  // of a word's 8 dims
+        uint32_t a = fma_bf16x2((half & 0x000F000Fu) | 0x43004300u, s, less);
+        uint32_t b = fma_bf16x2((half >> 4 & 0x000F000Fu) | 0x43004300u, s, less);
+        if (tails) a = tail[u].x, b = tail[u].y;
+        reinterpret_cast<float4*>(static_cast<float*>(out) + (first + u) * kHeadDim)[32 * k + lane] =
+            make_float4(dev::bf16_lo(a), dev::bf16_hi(a), dev::bf16_lo(b), dev::bf16_hi(b));
+      }
     }
   }
 }
 
-cudaLaunchConfig_t warp_per_row(int64_t rows, cudaStream_t stream, cudaLaunchAttribute* attr) {
-  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr->val.programmaticStreamSerializationAllowed = 1;
+template <typename... Params, typename... Args>
+cudaError_t launch_rows(void (*kernel)(Params...), int64_t rows, int each, cudaStream_t stream, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps * each - 1) / (kWarps * each)));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cfg;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
 cudaError_t launch_store(const StoreParams& p, bool four_bits, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = warp_per_row(p.num_rows, stream, attr);
   if (four_bits)
-    return p.x_f32 ? cudaLaunchKernelEx(&cfg, kvc_store_kernel<Slots4, true>, p)
-                   : cudaLaunchKernelEx(&cfg, kvc_store_kernel<Slots4, false>, p);
-  return p.x_f32 ? cudaLaunchKernelEx(&cfg, kvc_store_kernel<Slots8, true>, p)
-                 : cudaLaunchKernelEx(&cfg, kvc_store_kernel<Slots8, false>, p);
+    return p.x_f32 ? launch_rows(kvc_store_kernel<Slots4, true>, p.num_rows, 1, stream, p)
+                   : launch_rows(kvc_store_kernel<Slots4, false>, p.num_rows, 1, stream, p);
+  return p.x_f32 ? launch_rows(kvc_store_kernel<Slots8, true>, p.num_rows, 1, stream, p)
+                 : launch_rows(kvc_store_kernel<Slots8, false>, p.num_rows, 1, stream, p);
 }
 
 cudaError_t launch_dequantize4(const uint8_t* kv, int64_t num_pages, const int64_t* slots, int64_t num_slots, void* out,
                                int out_bf16, uint32_t* err, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = warp_per_row(num_slots, stream, attr);
-  return out_bf16 ? cudaLaunchKernelEx(&cfg, kvc_dequantize4_kernel<true>, kv, num_pages, slots, num_slots, out, err)
-                  : cudaLaunchKernelEx(&cfg, kvc_dequantize4_kernel<false>, kv, num_pages, slots, num_slots, out, err);
+  if (num_slots <= kFewRows)
+    return out_bf16 ? launch_rows(kvc_dequantize4_kernel<true, 1>, num_slots, 1, stream, kv, num_pages, slots, num_slots, out, err)
+                    : launch_rows(kvc_dequantize4_kernel<false, 1>, num_slots, 1, stream, kv, num_pages, slots, num_slots, out, err);
+  return out_bf16 ? launch_rows(kvc_dequantize4_kernel<true, 4>, num_slots, 4, stream, kv, num_pages, slots, num_slots, out, err)
+                  : launch_rows(kvc_dequantize4_kernel<false, 4>, num_slots, 4, stream, kv, num_pages, slots, num_slots, out, err);
 }
 
 }  // namespace kvc
