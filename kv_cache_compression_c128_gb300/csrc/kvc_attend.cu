@@ -24,7 +24,7 @@
 // and its products stay in range, so O is rescaled only where a score exceeds m
 // by 32, or at all on a page that holds values beyond 2^64.
 //
-// Warps of a CTA: 0..3 softmax and epilogue, one issues the products, one copies
+// Warps of a CTA: 0..3 softmax and epilogue, two issue the products, one copies
 // the codes, one the queries, seven decode, one brings the RoPE words.  The codes
 // of a page come by TMA, a piece of 64 slots x 64 bytes for each scale group,
 // through a ring: 24 KB (N 64) or 56 KB stay on their way whatever the decode
@@ -77,9 +77,9 @@ using dev::smem_addr;
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-// Every fourth warp shares a scheduler: the products' issuer sits with the two
-// copying warps, which mostly wait, apart from the decode and its long loop.
-constexpr int kIssueWarp = 7, kCopyWarp = 11, kQueryWarp = 15;
+// Every fourth warp shares a scheduler: the products' two issuers sit with the warp
+// that copies codes, which mostly waits, apart from the decode and its long loop.
+constexpr int kFirstWarp = 7, kCopyWarp = 11, kSecondWarp = 15, kQueryWarp = 14;
 constexpr int kAttendThreads = 16 * 32;
 // Registers of a thread by group of four warps: 512 x 128 at launch, shared
 // out anew so that no role spills (the cache that a spill would sit in is
@@ -120,6 +120,11 @@ constexpr int kStatsPerLane = (kAttendCtas + 31) / 32;  // of a unit's parts
 // loads a page ahead into registers, took longer.)
 template <int N, typename F>
 __host__ __device__ constexpr int ring_groups() { return N == 64 && !F::kFour ? 6 : 7; }
+// Pages whose softmax weights have a place.  With two, those of the next page are
+// stored while the second products still read; where shared memory leaves one (8-bit
+// slots from 17 heads on) they wait for them.
+template <int N, typename F>
+__host__ __device__ constexpr int weight_places() { return F::kFour || N == 16 ? 2 : 1; }
 // Pages that the ring holds, and pages whose scales are kept for its groups:
 // page i's are asked for when all pieces of page i - 1 - depth() are read, and
 // their scales before them.
@@ -141,7 +146,7 @@ struct Barriers {
   // the products' operands keep shared memory busy: two a page, not eight.
   unsigned long long half_full[2][2], chunk_empty[2][4];
   unsigned long long s_full[2];
-  unsigned long long p_full, q_full, q_empty, o_full, drain;
+  unsigned long long p_full[weight_places<N, F>()], q_full, q_empty, o_full, drain[2];
   unsigned long long piece_full[depth<N, F>()][ring_groups<N, F>()], piece_empty[depth<N, F>()][ring_groups<N, F>()], info_full[kInfos];
 };
 
@@ -158,7 +163,7 @@ template <int N, typename F>
 struct AttendShared {
   alignas(1024) uint8_t keys[2][kKeyStage];
   alignas(1024) uint8_t q[N * 1024];
-  alignas(1024) uint8_t p[kSlotsPerPage * 2 * N];
+  alignas(1024) uint8_t p[weight_places<N, F>()][kSlotsPerPage * 2 * N];
   alignas(1024) uint8_t codes[depth<N, F>()][ring_groups<N, F>()][piece_bytes<F>()];
   alignas(16) uint8_t scales[scale_slots<N, F>()][scale_bytes<F>()];
   union {
@@ -715,103 +720,104 @@ __device__ void rope_role(const AttendParams& p, AttendShared<N, F>& s, int coun
   }
 }
 
-// The products of every page: whatever can be issued next, a page's second
-// product, which frees the place of the page after next, before a half of the
-// next page's first.  The whole warp walks, one elected thread issues.  One
-// short loop: the questions travel together and behind products already queued,
-// and every role's code has to stay in the instruction cache beside the others'.
-// (Questions by one lane instead of all: 137 us where this takes 125.)
+// No product may run on when the CTA's memory is given back.
 template <int N, typename F>
-__device__ void issue_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
-  constexpr uint32_t kFirst = instruction(64, N, false), kSecond = instruction(128, N, true);
-  constexpr uint32_t kRows = operand_hi(1024, 2);
-  constexpr uint32_t kProbs = operand_hi(16 * N, N == 64 ? 2 : N == 32 ? 4 : 6);
+__device__ __forceinline__ void drain_products(AttendShared<N, F>& s, int which) {
+  if (elect_one()) tc_commit(&s.bar.drain[which]);
+  __syncwarp();
+  wait_for(&s.bar.drain[which], 0, kDefaultWaitLimitCycles);
+}
+
+// The first products of every page, a half of the dims at a time.  The whole warp
+// waits, one elected thread issues.  First and second products have a warp each: a
+// question of a barrier takes 250 to 450 cycles beside the products' operands, and an
+// issue as long as the products before it, so that one warp for both left the tensor
+// core without work for 400 cycles four times in two pages.  Nothing but barriers
+// orders the two: a page's first products need its keys, which are decoded into their
+// place once the second products of two pages before have read it, and those followed
+// the softmax of that page.
+template <int N, typename F>
+__device__ void first_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
+  constexpr uint32_t kFirst = instruction(64, N, false), kRows = operand_hi(1024, 2);
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s.tmem, 0);
   const uint32_t q = operand_lo(smem_addr(s.q), 16), all_keys = smem_addr(s.keys);
-  const uint32_t probs = operand_lo(smem_addr(s.p), 16);
-  int halves = 0, done = 0;      // halves of first products and whole second products issued
-  int segment = 0;               // segments begun
-  bool begins = true;            // the next half begins a segment
-  bool ends[2] = {true, false};  // the page of each stage ends its segment
-  bool fresh = true;             // the next second product is its segment's first
-  bool ok = true, idle = false;
-  long long since = 0;  // idle
+  int segment = 0;     // segments begun
+  bool begins = true;  // the next page begins a segment
+  bool ok = true;
 #pragma unroll 1
-  while (done < count) {
-    const int i = halves >> 1, half = halves & 1, stage = i & 1;
-    const uint32_t parity = (i >> 1) & 1;
-    // asked all at once: an answer takes long while products keep shared memory busy
-    bool first = dev::mbar_test_wait(&s.bar.half_full[stage][half], parity);
-    const bool other = dev::mbar_test_wait(&s.bar.half_full[stage][1], parity);
-    const bool second = dev::mbar_test_wait(&s.bar.p_full, done & 1);
-    if (begins) first = first && dev::mbar_test_wait(&s.bar.q_full, segment & 1);
-    if (done < i && __all_sync(0xFFFFFFFFu, second)) {
+  for (int i = 0; i < count; ++i) {
+    const int stage = i & 1;
+    const uint32_t parity = (i >> 1) & 1, into = tmem + 4 * N + stage * N;
+    if (begins) ok = wait_for(&s.bar.q_full, segment++ & 1, p.wait_limit);
+    ok = ok && wait_for(&s.bar.half_full[stage][0], parity, p.wait_limit);
+    // asked before the first half is issued: an answer takes long while products run
+    const bool other = __all_sync(0xFFFFFFFFu, dev::mbar_test_wait(&s.bar.half_full[stage][1], parity));
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !other) ok = ok && wait_for(&s.bar.half_full[stage][1], parity, p.wait_limit);
+      if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) break;
       tc_fence_after();
-      const int of = done & 1;
-      const bool last = of == 0 ? ends[0] : ends[1];
-      const uint32_t keys = operand_lo(all_keys + of * kKeyStage, kKeyBlock);
+      const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + h * (4 * kKeyBlock), 16);
+      const uint32_t queries = q + h * (4 * N * 128 / 16);
       if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
-                                           probs + k * 32 * N / 16, !fresh || k > 0);
-          tc_commit(&s.bar.chunk_empty[of][c]);  // the decode of page i + 2 follows chunk by chunk
-        }
-        if (last) tc_commit(&s.bar.o_full);
+            tc_mma<kRows, kRows, kFirst>(into, keys + (b * kKeyBlock + 32 * k) / 16,
+                                         queries + (b * (N * 128) + 32 * k) / 16, h + b + k > 0);
       }
       __syncwarp();
-      fresh = last;
-      ++done;
-    } else if (i < count && __all_sync(0xFFFFFFFFu, first)) {
-      tc_fence_after();
-      const uint32_t into = tmem + 4 * N + stage * N;
-      const int to = half == 1 || __all_sync(0xFFFFFFFFu, other) ? 2 : 1;
-#pragma unroll 1
-      for (int h = half; h < to; ++h) {
-        const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + h * (4 * kKeyBlock), 16);
-        const uint32_t queries = q + h * (4 * N * 128 / 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma<kRows, kRows, kFirst>(into, keys + (b * kKeyBlock + 32 * k) / 16,
-                                           queries + (b * (N * 128) + 32 * k) / 16, h + b + k > 0);
-        }
-        __syncwarp();
-      }
-      segment += begins;
-      begins = false;
-      if (to == 2) {
-        begins = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
-        ends[0] = stage == 0 ? begins : ends[0];
-        ends[1] = stage == 1 ? begins : ends[1];
-        if (elect_one()) {
-          tc_commit(&s.bar.s_full[stage]);
-          if (begins) tc_commit(&s.bar.q_empty);
-        }
-        __syncwarp();
-      }
-      halves += to - half;
-    } else {
-      const long long now = clock64();
-      if (!idle) since = now;
-      idle = true;
-      if (__any_sync(0xFFFFFFFFu, now - since > p.wait_limit || s.abort)) {
-        ok = false;
-        break;
-      }
-      continue;
     }
-    idle = false;
+    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+      s.abort = 1;
+      break;
+    }
+    begins = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
+    if (elect_one()) {
+      tc_commit(&s.bar.s_full[stage]);
+      if (begins) tc_commit(&s.bar.q_empty);
+    }
+    __syncwarp();
   }
-  if (!ok) s.abort = 1;
-  // no product may run on when the CTA's memory is given back
-  if (elect_one()) tc_commit(&s.bar.drain);
-  __syncwarp();
-  wait_for(&s.bar.drain, 0, kDefaultWaitLimitCycles);
+  drain_products(s, 0);
+}
+
+// The second products of every page.
+template <int N, typename F>
+__device__ void second_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
+  constexpr int kPlaces = weight_places<N, F>();
+  constexpr uint32_t kSecond = instruction(128, N, true), kRows = operand_hi(1024, 2);
+  constexpr uint32_t kProbs = operand_hi(16 * N, N == 64 ? 2 : N == 32 ? 4 : 6);
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s.tmem, 0), all_keys = smem_addr(s.keys);
+  bool fresh = true;  // the segment's first page
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const int stage = i & 1;
+    const bool ok = wait_for(&s.bar.p_full[i % kPlaces], (i / kPlaces) & 1, p.wait_limit);
+    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+      s.abort = 1;
+      break;
+    }
+    tc_fence_after();
+    const bool last = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
+    const uint32_t keys = operand_lo(all_keys + stage * kKeyStage, kKeyBlock);
+    const uint32_t probs = operand_lo(smem_addr(s.p[i % kPlaces]), 16);
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma<kRows, kProbs, kSecond>(tmem + c * N, keys + (2 * c * kKeyBlock + 2048 * k) / 16,
+                                         probs + k * 32 * N / 16, !fresh || k > 0);
+        tc_commit(&s.bar.chunk_empty[stage][c]);  // the decode of page i + 2 follows chunk by chunk
+      }
+      if (last) tc_commit(&s.bar.o_full);
+    }
+    __syncwarp();
+    fresh = last;
+  }
+  drain_products(s, 1);
 }
 
 // Columns `from` .. `to` - 1 of the four chunks' 4 N, the lanes of a warp.
@@ -997,19 +1003,19 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
         sum[col + 1] += b;
         pair[j] = __floats2bfloat162_rn(a, b);
       }
-      if (i > 0)  // the products of the page before have read its P
+      if (weight_places<N, F>() == 1 && i > 0)  // the products of the page before have read its P
         ok = __all_sync(0xFFFFFFFFu,
                         ok && wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const uint32_t off = (row + 8 * (j & 1)) * (2 * N) + 16 * (j >> 1) + 4 * (lane & 3);
         constexpr uint32_t kMask = N / 8 - 1;  // 16-byte pieces of a row
-        *reinterpret_cast<__nv_bfloat162*>(s.p + (off ^ (((off >> 7) & kMask) << 4))) = pair[j];
+        *reinterpret_cast<__nv_bfloat162*>(s.p[i % weight_places<N, F>()] + (off ^ (((off >> 7) & kMask) << 4))) = pair[j];
       }
       fence_async_shared();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&s.bar.p_full);
+      if (lane == 0) dev::mbar_arrive(&s.bar.p_full[i % weight_places<N, F>()]);
     }
     // the segment's end: columns' sums, then the rows of O
     combine_rows(sum, lane, [](float a, float b) { return a + b; });
@@ -1130,18 +1136,18 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   AttendShared<N, F>& s = *reinterpret_cast<AttendShared<N, F>*>(raw_shared);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int cta = blockIdx.x;
-  if (warp == kIssueWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
+  if (warp == kFirstWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
   if (t == 0) {
     for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) dev::mbar_init(&s.bar.half_full[i][j], 4);
       for (int j = 0; j < 4; ++j) dev::mbar_init(&s.bar.chunk_empty[i][j], 1);
       dev::mbar_init(&s.bar.s_full[i], 1);
     }
-    dev::mbar_init(&s.bar.p_full, kSoftmaxWarps);
+    for (int i = 0; i < weight_places<N, F>(); ++i) dev::mbar_init(&s.bar.p_full[i], kSoftmaxWarps);
     dev::mbar_init(&s.bar.q_full, 1);
     dev::mbar_init(&s.bar.q_empty, 1);
     dev::mbar_init(&s.bar.o_full, 1);
-    dev::mbar_init(&s.bar.drain, 1);
+    for (int i = 0; i < 2; ++i) dev::mbar_init(&s.bar.drain[i], 1);
     for (int i = 0; i < depth<N, F>() * ring_groups<N, F>(); ++i) {
       dev::mbar_init(&s.bar.piece_full[0][0] + i, 1);
       dev::mbar_init(&s.bar.piece_empty[0][0] + i, 1);
@@ -1263,9 +1269,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
       softmax_role<N, F>(p, s, w);
     } else {
       fewer_registers<kOtherRegs>();
-      const int worker = 3 * (warp / 4 - 1) + warp % 4;  // of those not on the issuer's scheduler
-      if (warp == kIssueWarp) {
-        issue_role<N, F>(p, s, count);
+      const int worker = 3 * (warp / 4 - 1) + warp % 4;  // of those not on the issuers' scheduler
+      if (warp == kFirstWarp) {
+        first_role<N, F>(p, s, count);
+      } else if (warp == kSecondWarp) {
+        second_role<N, F>(p, s, count);
       } else if (warp == kCopyWarp) {
         copy_role<N, F>(p, s, w);
       } else if (warp == kQueryWarp) {
@@ -1297,7 +1305,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_free(s.tmem, tmem_columns<N>());
+  if (warp == kFirstWarp) tmem_free(s.tmem, tmem_columns<N>());
 }
 
 // ---- joining kernel -----------------------------------------------------------------
