@@ -12,8 +12,11 @@ from a KernelGen Optimization" (KernelGen Challenge 8 write-up), section
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import subprocess
+import sysconfig
 import threading
 from concurrent.futures import ThreadPoolExecutor
 from typing import Optional
@@ -24,6 +27,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _INCLUDE = os.path.join(_ROOT, "include")
 _LIB_DIR = os.path.join(_HERE, "_lib")
 LIB_PATH = os.path.join(_LIB_DIR, "libkvc.so")
+_CALL_PATH = os.path.join(_LIB_DIR, "_kvc_call.so")
 _SOURCES = ["kvc_cluster.cu", "kvc_streamk.cu", "kvc_reader.cu", "kvc_api.cu", "kvc_static.cu",
             "kvc_selftest.cu", "kvc_attend.cu", "kvc_join.cu", "kvc_evict.cu", "kvc_operators.cu",
             "kvc_store.cu", "kvc_rotate.cu"]
@@ -67,6 +71,7 @@ ROPE_DIM = 64
 
 _lock = threading.Lock()
 _lib = None
+_entries = None
 
 
 class KvcError(RuntimeError):
@@ -118,17 +123,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+    _build_call()
     os.replace(tmp, LIB_PATH)
     if verbose:
         print("".join(logs))
     return LIB_PATH
 
 
+def _build_call() -> None:
+    """Compile csrc/kvc_call.c, the operators' entry points as the interpreter's own
+    functions.  Without the interpreter's headers the calls go through ctypes."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        if os.path.exists(_CALL_PATH):
+            os.remove(_CALL_PATH)
+        return
+    tmp = _CALL_PATH + f".tmp{os.getpid()}"
+    r = subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-I", include,
+                        os.path.join(_CSRC, "kvc_call.c"), "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for kvc_call.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, _CALL_PATH)
+
+
 # ---- loading -----------------------------------------------------------------
 
 def lib():
     """The loaded libkvc.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _entries
     if _lib is not None:
         return _lib
     with _lock:
@@ -211,8 +233,28 @@ def lib():
             L.kvc_error_string.restype = ctypes.c_char_p
             L.kvc_version.argtypes = []
             L.kvc_version.restype = ctypes.c_char_p
+            _entries = _load_entries(L)
             _lib = L
     return _lib
+
+
+def _load_entries(L):
+    """The operators' entry points: kvc_call.c's functions, or ctypes' own."""
+    if not os.path.exists(_CALL_PATH):
+        return L
+    loader = importlib.machinery.ExtensionFileLoader("_kvc_call", _CALL_PATH)
+    call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvc_call", loader))
+    loader.exec_module(call)
+    call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.kvc_attend_format, L.kvc_evict_format, L.kvc_store, L.kvc_dequantize_format, L.kvc_rotate)])
+    return call
+
+
+def _entry():
+    """What the operators call the library through (lib() with quicker calls)."""
+    if _entries is None:
+        lib()
+    return _entries
 
 
 # ---- the C ABI, one Python function per entry point ---------------------------
@@ -397,7 +439,7 @@ def kvc_dequantize(kv_cache, num_kv_pages, slots, num_slots, out, out_dtype, str
 def kvc_dequantize_format(kv_cache, kv_format, num_kv_pages, slots, num_slots, out, out_dtype,
                           stream) -> int:
     """Decode slots of either form (raw integer pointers); returns the status."""
-    return lib().kvc_dequantize_format(kv_cache, kv_format, num_kv_pages, slots, num_slots, out,
+    return _entry().kvc_dequantize_format(kv_cache, kv_format, num_kv_pages, slots, num_slots, out,
                                        out_dtype, stream)
 
 
@@ -406,7 +448,7 @@ def kvc_store(x, x_dtype, x_row_stride, num_rows, kv_cache, kv_format, num_kv_pa
               cos_sin_cache, num_positions, stream) -> int:
     """Vectors into packed slots (raw integer pointers; pair_axes 32 bytes or
     None); returns the status."""
-    return lib().kvc_store(
+    return _entry().kvc_store(
         x, x_dtype, x_row_stride, num_rows, kv_cache, kv_format, num_kv_pages, slots, positions,
         positions_row_stride, positions_axis_stride, num_axes, pair_axes, cos_sin_cache,
         num_positions, stream)
@@ -417,7 +459,7 @@ def kvc_rotate(x, dtype, x_token_stride, x_head_stride, num_tokens, num_heads, p
                num_positions, inverse, out, out_token_stride, out_head_stride, stream) -> int:
     """Rotary positions (raw integer pointers; pair_axes 32 bytes or None);
     returns the status."""
-    return lib().kvc_rotate(
+    return _entry().kvc_rotate(
         x, dtype, x_token_stride, x_head_stride, num_tokens, num_heads, positions,
         positions_token_stride, positions_axis_stride, num_axes, pair_axes, cos_sin_cache,
         num_positions, inverse, out, out_token_stride, out_head_stride, stream)
@@ -448,7 +490,7 @@ def kvc_attend_format(q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_ca
                       slot_weights, slot_weights_row_stride, max_slots, workspace,
                       workspace_bytes, flags, stream) -> int:
     """kvc_attend over pages of either form."""
-    return lib().kvc_attend_format(
+    return _entry().kvc_attend_format(
         q, q_req_stride, q_head_stride, num_reqs, num_heads, kv_cache, kv_format, num_kv_pages,
         page_table, max_pages_per_req, page_table_row_stride, lengths, scale, sinks, out, lse,
         slot_weights_in, slot_weights_in_row_stride, slot_weights, slot_weights_row_stride,
@@ -485,7 +527,7 @@ def kvc_evict_format(kv_cache, kv_format, num_kv_pages, page_table, num_reqs, ma
                      slot_weights_out, slot_weights_out_row_stride, births_out,
                      births_out_row_stride, workspace, workspace_bytes, stream) -> int:
     """kvc_evict over pages of either form."""
-    return lib().kvc_evict_format(
+    return _entry().kvc_evict_format(
         kv_cache, kv_format, num_kv_pages, page_table, num_reqs, max_pages_per_req,
         page_table_row_stride, lengths, slot_weights, slot_weights_row_stride, max_slots, births,
         births_row_stride, keep, recent, lengths_out, kept, slot_weights_out,
@@ -522,7 +564,7 @@ def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
         nonlocal out
         if out is None:
             out = torch.empty((M, HEAD_DIM), dtype=dtype, device=kv_cache.device)
-        return kvc_dequantize_format(kv_cache.data_ptr(), KVC_FORMAT_4BIT if four else KVC_FORMAT_8BIT, shape[0],
+        return _entry().kvc_dequantize_format(kv_cache.data_ptr(), KVC_FORMAT_4BIT if four else KVC_FORMAT_8BIT, shape[0],
                                      slots.data_ptr(), M, out.data_ptr(), _dtype_codes[dtype], raw)
 
     st = _run(call, device, stream)
@@ -903,7 +945,7 @@ def store(x, kv_cache, slots, *, positions=None, cos_sin_cache=None, axes=None, 
         raise ValueError("axes and cos_sin_cache need positions")
 
     def call(raw):
-        return kvc_store(x.data_ptr(), _dtype_codes[dtype], row if N > 1 else 0, N, kv_cache.data_ptr(), form, pages,
+        return _entry().kvc_store(x.data_ptr(), _dtype_codes[dtype], row if N > 1 else 0, N, kv_cache.data_ptr(), form, pages,
                          slots.data_ptr(), *turn, raw)
 
     st = _run(call, device, stream)
@@ -945,7 +987,7 @@ def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out
         by_token, by_dim = strides
     if D != ROPE_DIM or (by_dim != 1 and T * H > 0):
         raise ValueError("x must be [tokens, heads, 64] or [tokens, 64] with contiguous columns")
-    turn = _rotation(positions, cos_sin_cache, axes, T, device)
+    at, at_row, at_axis, axis_count, pairs, table, entries = _rotation(positions, cos_sin_cache, axes, T, device)
     if out is not None:
         if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != device:
             _refuse("out", out, dtype, len(shape), device)
@@ -957,8 +999,9 @@ def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=x.device)
         to = out.stride()
-        return kvc_rotate(x.data_ptr(), code, by_token if T > 1 else 0, by_head if H > 1 else 0, T, H, *turn,
-                          1 if inverse else 0, out.data_ptr(), to[0] if T > 1 else 0, to[1] if H > 1 else 0, raw)
+        return _entry().kvc_rotate(
+            x.data_ptr(), code, by_token if T > 1 else 0, by_head if H > 1 else 0, T, H, at, at_row, at_axis, axis_count,
+            pairs, table, entries, 1 if inverse else 0, out.data_ptr(), to[0] if T > 1 else 0, to[1] if H > 1 else 0, raw)
 
     st = _run(call, device, stream)
     if st != KVC_OK:
@@ -1040,7 +1083,7 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
         if workspace is None:
             workspace = torch.empty(kvc_attend_workspace_bytes(R, H, columns, slot_weights is not None),
                                     dtype=torch.uint8, device=kv_cache.device)
-        return kvc_attend_format(
+        return _entry().kvc_attend_format(
             q.data_ptr(), by_req, by_head, R, H, kv_cache.data_ptr(), form, pages,
             page_table.data_ptr(), columns, row, lengths.data_ptr(), HEAD_DIM ** -0.5 if scale is None else scale,
             None if sinks is None else sinks.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -1166,7 +1209,7 @@ def evict(kv_cache, page_table, lengths, slot_weights, keep, *, recent: int = 0,
         if workspace is None:
             workspace = torch.empty(kvc_evict_workspace_bytes(R, columns, keep), dtype=torch.uint8,
                                     device=kv_cache.device)
-        return kvc_evict_format(
+        return _entry().kvc_evict_format(
             kv_cache.data_ptr(), form, pages, page_table.data_ptr(), R, columns, row, lengths.data_ptr(),
             slot_weights.data_ptr(), weights_row, S, None if births is None else births.data_ptr(),
             births_row, keep, recent, lengths_out.data_ptr(), kept.data_ptr() if keep else None,
