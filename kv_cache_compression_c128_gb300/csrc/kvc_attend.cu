@@ -77,9 +77,15 @@ using dev::smem_addr;
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-// Every fourth warp shares a scheduler: the products' two issuers sit with the warp
-// that copies codes, which mostly waits, apart from the decode and its long loop.
-constexpr int kFirstWarp = 7, kCopyWarp = 11, kSecondWarp = 15, kQueryWarp = 14;
+constexpr int kFirstWarp = 7, kSecondWarp = 15;
+// Every fourth warp shares a scheduler.  Of 8-bit slots, whose decode takes more
+// instructions, one of the seven warps that decode sits beside the two that issue the
+// products and two on each other scheduler; of 4-bit slots the copying warp sits
+// there, and none that decodes.  (64 requests x 8192 slots, 64 and 16 heads, and 32 x
+// up to 4099, 16 heads, us: 8 bits 119.6, 83.8, 17.5 and the other way 122.0, 83.5,
+// 17.9; 4 bits 107.9, 80.7, 17.1 and the other way 108.6, 83.3, 17.1.)
+template <typename F>
+__host__ __device__ constexpr int copy_warp() { return F::kFour ? 11 : 12; }
 constexpr int kAttendThreads = 16 * 32;
 // Registers of a thread by group of four warps: 512 x 128 at launch, shared
 // out anew so that no role spills (the cache that a spill would sit in is
@@ -286,6 +292,14 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Four 8 x 8 matrices of 16 bits, two neighbours in a row a lane and word; lane l
+// gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_matrices(void* row, const uint32_t* v) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_addr(row)), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -304,14 +318,16 @@ __device__ __forceinline__ void fewer_registers() {
 // dev::mbar_wait_bounded in line (a call would have its registers counted
 // against every role), and with the clock read only if the phase is not
 // complete at once: read at every wait it took 270 cycles of the issuing
-// thread each, 9 times a page.
-__device__ __forceinline__ bool wait_for(unsigned long long* bar, uint32_t parity, long long limit) {
+// thread each, 9 times a page.  For the same reason nobody looks whether another
+// role has given up (`abort`) but here.
+__device__ __forceinline__ bool wait_for(unsigned long long* bar, uint32_t parity, long long limit,
+                                         const volatile int* abort) {
   const bool poll = limit < dev::kPollBelowCycles;
   if (!poll && dev::mbar_try_wait(bar, parity)) return true;
   const long long start = clock64();
   do {
     if (poll ? dev::mbar_test_wait(bar, parity) : dev::mbar_try_wait(bar, parity)) return true;
-  } while (clock64() - start <= limit);
+  } while (clock64() - start <= limit && (abort == nullptr || *abort == 0));
   return false;
 }
 
@@ -482,14 +498,14 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) 
       }
       const int place = i % kDepth, turn = i / kDepth;
       if (lane < kRing) {
-        ok = turn == 0 || wait_for(&s.bar.piece_empty[place][lane], (turn - 1) & 1, p.wait_limit);
+        ok = turn == 0 || wait_for(&s.bar.piece_empty[place][lane], (turn - 1) & 1, p.wait_limit, &s.abort);
         if (ok) {
           dev::mbar_arrive_expect_tx(&s.bar.piece_full[place][lane], piece_bytes<F>());
           copy_box(s.codes[place][lane], &p.code_map, lane * group_bytes<F>(), 0, id, &s.bar.piece_full[place][lane]);
           ++asked;
         }
       }
-      ok = __all_sync(0xFFFFFFFFu, ok && !s.abort);
+      ok = __all_sync(0xFFFFFFFFu, ok);
     }
     w.advance(p, count);
   }
@@ -498,35 +514,13 @@ __device__ void copy_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) 
   if (lane < kRing) {
 #pragma unroll 1
     for (int j = max(0, asked - kDepth); j < asked; ++j)
-      wait_for(&s.bar.piece_full[j % kDepth][lane], (j / kDepth) & 1, kDefaultWaitLimitCycles);
+      wait_for(&s.bar.piece_full[j % kDepth][lane], (j / kDepth) & 1, kDefaultWaitLimitCycles, nullptr);
   } else if (lane == 31) {
 #pragma unroll 1
     for (int j = max(0, asked - kInfos); j < asked; ++j)
-      wait_for(&s.bar.info_full[j % kInfos], (j / kInfos) & 1, kDefaultWaitLimitCycles);
+      wait_for(&s.bar.info_full[j % kInfos], (j / kInfos) & 1, kDefaultWaitLimitCycles, nullptr);
   }
   __syncwarp();
-}
-
-// Copies each segment's queries, in the layout of the products' operand.
-template <int N, typename F>
-__device__ void query_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) {
-#pragma unroll 1
-  for (int segment = 0; w.left > 0; ++segment) {
-    bool ok = segment == 0 || wait_for(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit);
-    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
-      s.abort = 1;
-      return;
-    }
-    if (elect_one()) {
-      dev::mbar_arrive_expect_tx(&s.bar.q_full, N * 1024);
-#pragma unroll 1
-      for (int b = 0; b < 8; ++b)
-        copy_box(s.q + b * (N * 128), &p.q_map, 64 * b, w.group * p.group_heads, p.q_shared ? 0 : w.req, &s.bar.q_full);
-    }
-    __syncwarp();
-    wait_for(&s.bar.q_full, segment & 1, kDefaultWaitLimitCycles);
-    w.advance(p, w.segment());
-  }
 }
 
 // Eight times 16 codes and their scale bytes as 16 bf16; sets *large if a scale
@@ -568,13 +562,13 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N, F>& s, int g,
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1, place = i % kDepth;
-    ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
+    ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit, &s.abort);
     // (what is not described, after a wait that ran out, is not an address)
     const PageInfo info = ok ? s.info[i % kInfos] : PageInfo{0, 0, 0};
     if (g < ring_groups<N, F>()) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) scale[j] = s.scales[i % kScales][(r + 8 * j) * kScaleDim + g];
-      ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit);
+      ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit, &s.abort);
 #pragma unroll
       for (int j = 0; j < 8; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[place][g] + (lane + 32 * j) * 16);
       // The place is given back once the values are there, not once they have
@@ -603,8 +597,8 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N, F>& s, int g,
     // decoded before its place is free, so that only the stores are left then
     uint4 lo[8], hi[8];
     decode_rows(raw, scale, lo, hi, &s.large[i % kInfos]);
-    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit);
-    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit, &s.abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
       s.abort = 1;
       return;
     }
@@ -621,7 +615,8 @@ __device__ void decode_role(const AttendParams& p, AttendShared<N, F>& s, int g,
 }
 
 // The same of 4-bit slots: 4 times 16 slots, lane l slot l / 2 of the 16 and codes
-// 32 (l % 2) .. + 31, which have one scale.
+// 32 (l % 2) .. + 31, which have one scale.  (The next page's codes asked for before
+// this one's wait for their place: level.)
 template <int N, typename F>
 __device__ void decode4_role(const AttendParams& p, AttendShared<N, F>& s, int g, int count) {
   constexpr int kDepth = depth<N, F>(), kScales = scale_slots<N, F>();
@@ -632,17 +627,17 @@ __device__ void decode4_role(const AttendParams& p, AttendShared<N, F>& s, int g
     const int stage = i & 1, place = i % kDepth;
     uint32_t scale[4];
     uint4 raw[4];
-    ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
-    const int valid = ok ? s.info[i % kInfos].valid : 0;
+    ok = ok && wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit, &s.abort);
+    const int valid = s.info[i % kInfos].valid;
 #pragma unroll
     for (int j = 0; j < 4; ++j) scale[j] = s.scales[i % kScales][(r + 16 * j) * F::kScales + 2 * g + c];
-    ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit);
+    ok = ok && wait_for(&s.bar.piece_full[place][g], (i / kDepth) & 1, p.wait_limit, &s.abort);
 #pragma unroll
     for (int j = 0; j < 4; ++j) raw[j] = *reinterpret_cast<const uint4*>(s.codes[place][g] + (lane + 32 * j) * 16);
     // given back once the values are there (see decode_role)
     uint32_t all = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) all ^= raw[j].x ^ raw[j].w ^ scale[j];
+    for (int j = 0; j < 4; ++j) all ^= raw[j].x ^ scale[j];
     const int arrives = __all_sync(0xFFFFFFFFu, all == 1u) ? 1 : 0;
     if (lane == arrives) dev::mbar_arrive(&s.bar.piece_empty[place][g]);
     if (__builtin_expect(valid < kSlotsPerPage, 0)) {  // code 0 in every place of the slots that do not count
@@ -659,8 +654,8 @@ __device__ void decode4_role(const AttendParams& p, AttendShared<N, F>& s, int g
       v[j][2] = decode8_bf16(raw[j].z, up, less);
       v[j][3] = decode8_bf16(raw[j].w, up, less);
     }
-    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit);
-    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][g >> 1], ((i >> 1) - 1) & 1, p.wait_limit, &s.abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
       s.abort = 1;
       return;
     }
@@ -675,24 +670,26 @@ __device__ void decode4_role(const AttendParams& p, AttendShared<N, F>& s, int g
   }
 }
 
-// The RoPE words of every page, read into registers ahead (8 KB, which plain
+// The RoPE words of every other page, read into registers ahead (8 KB, which plain
 // loads can keep on their way) and stored once their place is free: lane l has
-// piece l % 8 of rows l / 8 + 4 j.
+// piece l % 8 of rows l / 8 + 4 j.  Two warps take turns: one for all pages asked for
+// a page's words when it had stored those before, and waited for them some 1600
+// cycles of a page's 2700 at N = 16.
 template <int N, typename F>
-__device__ void rope_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
+__device__ void rope_role(const AttendParams& p, AttendShared<N, F>& s, int from, int count) {
   const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7;
 #pragma unroll 1
-  for (int i = 0; i < count; ++i) {
+  for (int i = from; i < count; i += 2) {
     const int stage = i & 1;
-    bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit);
+    bool ok = wait_for(&s.bar.info_full[i % kInfos], (i / kInfos) & 1, p.wait_limit, &s.abort);
     const PageInfo info = ok ? s.info[i % kInfos] : PageInfo{0, 0, 0};
     const uint8_t* src = p.kv_cache + info.id * F::kPage + r * F::kStride + F::kCodes + 16 * c;
     uint4 v[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j)  // slots that do not count may hold anything, NaN too
       v[j] = r + 4 * j < info.valid ? load16(src + 4 * j * F::kStride) : make_uint4(0, 0, 0, 0);
-    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][3], ((i >> 1) - 1) & 1, p.wait_limit);
-    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+    if (i >= 2) ok = ok && wait_for(&s.bar.chunk_empty[stage][3], ((i >> 1) - 1) & 1, p.wait_limit, &s.abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
       s.abort = 1;
       return;
     }
@@ -725,7 +722,7 @@ template <int N, typename F>
 __device__ __forceinline__ void drain_products(AttendShared<N, F>& s, int which) {
   if (elect_one()) tc_commit(&s.bar.drain[which]);
   __syncwarp();
-  wait_for(&s.bar.drain[which], 0, kDefaultWaitLimitCycles);
+  wait_for(&s.bar.drain[which], 0, kDefaultWaitLimitCycles, nullptr);
 }
 
 // The first products of every page, a half of the dims at a time.  The whole warp
@@ -737,7 +734,7 @@ __device__ __forceinline__ void drain_products(AttendShared<N, F>& s, int which)
 // place once the second products of two pages before have read it, and those followed
 // the softmax of that page.
 template <int N, typename F>
-__device__ void first_role(const AttendParams& p, AttendShared<N, F>& s, int count) {
+__device__ void first_role(const AttendParams& p, AttendShared<N, F>& s, Walk w, int count) {
   constexpr uint32_t kFirst = instruction(64, N, false), kRows = operand_hi(1024, 2);
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s.tmem, 0);
   const uint32_t q = operand_lo(smem_addr(s.q), 16), all_keys = smem_addr(s.keys);
@@ -748,14 +745,25 @@ __device__ void first_role(const AttendParams& p, AttendShared<N, F>& s, int cou
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1;
     const uint32_t parity = (i >> 1) & 1, into = tmem + 4 * N + stage * N;
-    if (begins) ok = wait_for(&s.bar.q_full, segment++ & 1, p.wait_limit);
-    ok = ok && wait_for(&s.bar.half_full[stage][0], parity, p.wait_limit);
-    // asked before the first half is issued: an answer takes long while products run
-    const bool other = __all_sync(0xFFFFFFFFu, dev::mbar_test_wait(&s.bar.half_full[stage][1], parity));
+    if (begins) {  // the segment's queries, in the layout of the products' operand
+      ok = segment == 0 || wait_for(&s.bar.q_empty, (segment - 1) & 1, p.wait_limit, &s.abort);
+      if (__all_sync(0xFFFFFFFFu, ok)) {
+        if (elect_one()) {
+          dev::mbar_arrive_expect_tx(&s.bar.q_full, N * 1024);
+#pragma unroll 1
+          for (int b = 0; b < 8; ++b)
+            copy_box(s.q + b * (N * 128), &p.q_map, 64 * b, w.group * p.group_heads, p.q_shared ? 0 : w.req, &s.bar.q_full);
+        }
+        __syncwarp();
+        wait_for(&s.bar.q_full, segment & 1, kDefaultWaitLimitCycles, nullptr);
+      }
+      ++segment;
+    }
+    ok = ok && wait_for(&s.bar.half_full[stage][0], parity, p.wait_limit, &s.abort);
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
-      if (h == 1 && !other) ok = ok && wait_for(&s.bar.half_full[stage][1], parity, p.wait_limit);
-      if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) break;
+      if (h == 1) ok = ok && wait_for(&s.bar.half_full[stage][1], parity, p.wait_limit, &s.abort);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
       const uint32_t keys = operand_lo(all_keys + stage * kKeyStage + h * (4 * kKeyBlock), 16);
       const uint32_t queries = q + h * (4 * N * 128 / 16);
@@ -769,7 +777,7 @@ __device__ void first_role(const AttendParams& p, AttendShared<N, F>& s, int cou
       }
       __syncwarp();
     }
-    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
       s.abort = 1;
       break;
     }
@@ -779,6 +787,7 @@ __device__ void first_role(const AttendParams& p, AttendShared<N, F>& s, int cou
       if (begins) tc_commit(&s.bar.q_empty);
     }
     __syncwarp();
+    if (begins) w.advance(p, w.segment());
   }
   drain_products(s, 0);
 }
@@ -794,13 +803,12 @@ __device__ void second_role(const AttendParams& p, AttendShared<N, F>& s, int co
 #pragma unroll 1
   for (int i = 0; i < count; ++i) {
     const int stage = i & 1;
-    const bool ok = wait_for(&s.bar.p_full[i % kPlaces], (i / kPlaces) & 1, p.wait_limit);
-    if (!__all_sync(0xFFFFFFFFu, ok && !s.abort)) {
+    const bool ok = wait_for(&s.bar.p_full[i % kPlaces], (i / kPlaces) & 1, p.wait_limit, &s.abort);
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
       s.abort = 1;
       break;
     }
     tc_fence_after();
-    const bool last = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
     const uint32_t keys = operand_lo(all_keys + stage * kKeyStage, kKeyBlock);
     const uint32_t probs = operand_lo(smem_addr(s.p[i % kPlaces]), 16);
     if (elect_one()) {
@@ -812,10 +820,11 @@ __device__ void second_role(const AttendParams& p, AttendShared<N, F>& s, int co
                                          probs + k * 32 * N / 16, !fresh || k > 0);
         tc_commit(&s.bar.chunk_empty[stage][c]);  // the decode of page i + 2 follows chunk by chunk
       }
-      if (last) tc_commit(&s.bar.o_full);
     }
     __syncwarp();
-    fresh = last;
+    fresh = __any_sync(0xFFFFFFFFu, s.info[i % kInfos].last);
+    if (fresh && elect_one()) tc_commit(&s.bar.o_full);
+    __syncwarp();
   }
   drain_products(s, 1);
 }
@@ -915,7 +924,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
 #pragma unroll 1
     for (int pg = 0; pg < n; ++pg, ++i) {
       const int stage = i & 1;
-      ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit));
+      ok = __all_sync(0xFFFFFFFFu, ok && wait_for(&s.bar.s_full[stage], (i >> 1) & 1, p.wait_limit, &s.abort));
       tc_fence_after();
       const float above = s.large[i % kInfos] ? 0.f : kRescaleAbove;
       uint32_t v[2 * kCols];
@@ -954,7 +963,28 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
 #pragma unroll
       for (int j = 0; j < 2 * kCols; ++j)
         top = fmaxf(top, __fsub_rn(x[j], ref[(j >> 2) * 2 + (j & 1)]));
-      if (__builtin_expect(softmax_any(top > above || !ok), 0)) {
+      // The weights by the reference as it is, and then the question whether it moves:
+      // asked first, the slowest warp's answer was waited for.  If it does, they are
+      // formed again; on the first page it always does.
+      float was[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) was[j] = sum[j];
+      uint32_t pair[kCols];
+#pragma unroll 1
+      for (bool moved = false;; moved = true) {
+        if (moved || pg > 0) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {  // columns of j / 2, rows of j % 2
+            const int col = j & ~1;
+            const float a = exp2_fast(__fsub_rn(x[2 * j], ref[col]));
+            const float b = exp2_fast(__fsub_rn(x[2 * j + 1], ref[col + 1]));
+            sum[col] += a;
+            sum[col + 1] += b;
+            const __nv_bfloat162 both = __floats2bfloat162_rn(a, b);
+            pair[j] = *reinterpret_cast<const uint32_t*>(&both);
+          }
+          if (moved || !softmax_any(top > above || !ok)) break;
+        }
         if (softmax_any(!ok)) {
           s.abort = 1;
           return;
@@ -972,13 +1002,13 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
           const float next = fmaxf(fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
                                          fmaxf(s.red[2][col], s.red[3][col])), ref[j]);
           const float f = exp2_fast(ref[j] - next);
-          sum[j] *= f;
+          sum[j] = was[j] * f;
           ref[j] = next;
           if (warp == 0 && lane < 4) s.factor[col] = f;
         }
         softmax_sync();
         if (pg > 0) {  // bring what is summed up so far to the new reference
-          ok = __all_sync(0xFFFFFFFFu, wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
+          ok = __all_sync(0xFFFFFFFFu, wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit, &s.abort));
           tc_fence_after();
 #pragma unroll 1
           for (int b = 0; b < 4 * N; b += 16) {
@@ -993,24 +1023,15 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
           tmem_wait_st();
         }
       }
-      __nv_bfloat162 pair[kCols];
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) {  // columns of j / 2, rows of j % 2
-        const int col = j & ~1;
-        const float a = exp2_fast(__fsub_rn(x[2 * j], ref[col]));
-        const float b = exp2_fast(__fsub_rn(x[2 * j + 1], ref[col + 1]));
-        sum[col] += a;
-        sum[col + 1] += b;
-        pair[j] = __floats2bfloat162_rn(a, b);
-      }
       if (weight_places<N, F>() == 1 && i > 0)  // the products of the page before have read its P
         ok = __all_sync(0xFFFFFFFFu,
-                        ok && wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit));
+                        ok && wait_for(&s.bar.chunk_empty[stage ^ 1][3], ((i - 1) >> 1) & 1, p.wait_limit, &s.abort));
+      // pairs 2 b, 2 b + 1 of the lanes are 8 slots each x the 16 bytes of columns 8 b .. + 7
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) {
-        const uint32_t off = (row + 8 * (j & 1)) * (2 * N) + 16 * (j >> 1) + 4 * (lane & 3);
+      for (int j = 0; j < kCols; j += 4) {
+        const uint32_t off = (warp * 16 + (lane & 15)) * (2 * N) + 16 * ((j >> 1) + (lane >> 4));
         constexpr uint32_t kMask = N / 8 - 1;  // 16-byte pieces of a row
-        *reinterpret_cast<__nv_bfloat162*>(s.p[i % weight_places<N, F>()] + (off ^ (((off >> 7) & kMask) << 4))) = pair[j];
+        store_matrices(s.p[i % weight_places<N, F>()] + (off ^ (((off >> 7) & kMask) << 4)), pair + j);
       }
       fence_async_shared();
       tc_fence_before();
@@ -1064,7 +1085,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
         }
       }
     }
-    ok = ok && wait_for(&s.bar.o_full, segment & 1, p.wait_limit);
+    ok = ok && wait_for(&s.bar.o_full, segment & 1, p.wait_limit, &s.abort);
     if (softmax_any(!ok)) {  // also makes s.factor visible
       s.abort = 1;
       return;
@@ -1269,22 +1290,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
       softmax_role<N, F>(p, s, w);
     } else {
       fewer_registers<kOtherRegs>();
-      const int worker = 3 * (warp / 4 - 1) + warp % 4;  // of those not on the issuers' scheduler
+      const int worker = warp - kSoftmaxWarps - (warp > kFirstWarp) - (warp > copy_warp<F>());
       if (warp == kFirstWarp) {
-        first_role<N, F>(p, s, count);
+        first_role<N, F>(p, s, w, count);
       } else if (warp == kSecondWarp) {
         second_role<N, F>(p, s, count);
-      } else if (warp == kCopyWarp) {
+      } else if (warp == copy_warp<F>()) {
         copy_role<N, F>(p, s, w);
-      } else if (warp == kQueryWarp) {
-        query_role<N, F>(p, s, w);
       } else if (worker < kGroups) {
         if constexpr (F::kFour)
           decode4_role<N, F>(p, s, worker, count);
         else
           decode_role<N, F>(p, s, worker, count);
-      } else if (worker == kGroups) {
-        rope_role<N, F>(p, s, count);
+      } else {
+        rope_role<N, F>(p, s, worker - kGroups, count);
       }
     }
   }
