@@ -71,7 +71,7 @@ ROPE_DIM = 64
 
 _lock = threading.Lock()
 _lib = None
-_entries = None
+_quick = None
 
 
 class KvcError(RuntimeError):
@@ -116,14 +116,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with ThreadPoolExecutor(len(_SOURCES)) as ex:
+    with ThreadPoolExecutor(len(_SOURCES) + 1) as ex:
+        calls = ex.submit(_build_call)
         logs = list(ex.map(compile_one, zip(_SOURCES, objs)))
+        calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, "-shared"] + ARCH_FLAGS + objs + ["-o", tmp],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    _build_call()
     os.replace(tmp, LIB_PATH)
     if verbose:
         print("".join(logs))
@@ -131,18 +132,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def _build_call() -> None:
-    """Compile csrc/kvc_call.c, the operators' entry points as the interpreter's own
-    functions.  Without the interpreter's headers the calls go through ctypes."""
-    include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
+    """Compile csrc/kvc_call.cpp, the operators' calls as the interpreter's own functions.
+    Without the interpreter's or torch's headers the calls go through ctypes."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"), cuda]
+    needed = ["Python.h", os.path.join("torch", "csrc", "autograd", "python_variable.h"), "cuda_runtime.h"]
+    if not all(os.path.exists(os.path.join(d, f)) for d, f in zip(includes, needed)):
         if os.path.exists(_CALL_PATH):
             os.remove(_CALL_PATH)
         return
+    libs = os.path.join(root, "lib")
     tmp = _CALL_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-I", include,
-                        os.path.join(_CSRC, "kvc_call.c"), "-o", tmp], capture_output=True, text=True)
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    cmd += [f"-I{d}" for d in includes] + [os.path.join(_CSRC, "kvc_call.cpp"), "-o", tmp, "-L" + libs]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for kvc_call.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for kvc_call.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, _CALL_PATH)
 
 
@@ -150,7 +159,7 @@ def _build_call() -> None:
 
 def lib():
     """The loaded libkvc.so (raises if it has not been built)."""
-    global _lib, _entries
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -233,28 +242,29 @@ def lib():
             L.kvc_error_string.restype = ctypes.c_char_p
             L.kvc_version.argtypes = []
             L.kvc_version.restype = ctypes.c_char_p
-            _entries = _load_entries(L)
             _lib = L
     return _lib
 
 
-def _load_entries(L):
-    """The operators' entry points: kvc_call.c's functions, or ctypes' own."""
-    if not os.path.exists(_CALL_PATH):
-        return L
-    loader = importlib.machinery.ExtensionFileLoader("_kvc_call", _CALL_PATH)
-    call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvc_call", loader))
-    loader.exec_module(call)
-    call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.kvc_attend_format, L.kvc_evict_format, L.kvc_store, L.kvc_dequantize_format, L.kvc_rotate)])
-    return call
+def _load_quick():
+    """kvc_call.cpp's functions, where they were built (torch is loaded)."""
+    global _quick
+    if _quick is None and os.path.exists(LIB_PATH) and os.path.exists(_CALL_PATH):
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_kvc_call", _CALL_PATH)
+            call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvc_call", loader))
+            loader.exec_module(call)
+        except ImportError:  # built beside another torch
+            return
+        L = lib()
+        call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.kvc_attend_format, L.kvc_evict_format, L.kvc_store, L.kvc_dequantize_format, L.kvc_rotate)])
+        _quick = call
 
 
 def _entry():
-    """What the operators call the library through (lib() with quicker calls)."""
-    if _entries is None:
-        lib()
-    return _entries
+    """What the operators call the library through: lib(), or the same with quicker calls."""
+    return _quick or lib()
 
 
 # ---- the C ABI, one Python function per entry point ---------------------------
@@ -543,6 +553,12 @@ def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
     bytes hold 4-bit slots, others 8-bit ones."""
     torch = _torch or _load_torch()
     dtype = torch.float32 if dtype is None else dtype
+    if out is not None and stream is None and _quick is not None and isinstance(out, torch.Tensor) and out.dtype == dtype:
+        st = _quick.dequantize(kv_cache, slots, out)
+        if st == KVC_OK:
+            return out
+        if st is not None:
+            raise KvcError(st, "kvc_dequantize")
     if dtype not in _dtype_codes:
         raise TypeError("dtype must be torch.float32 or torch.bfloat16")
     if not kv_cache.is_cuda:
@@ -780,6 +796,7 @@ def _load_torch():
 
         _dtype_codes.update({torch.float32: KVC_DTYPE_F32, torch.bfloat16: KVC_DTYPE_BF16})
         _torch = torch
+        _load_quick()
     return _torch
 
 
@@ -930,6 +947,12 @@ def store(x, kv_cache, slots, *, positions=None, cos_sin_cache=None, axes=None, 
     kv_cache.  No gradient is recorded.
     """
     torch = _torch or _load_torch()
+    if stream is None and _quick is not None:
+        st = _quick.store(x, kv_cache, slots, positions, cos_sin_cache, axes)
+        if st == KVC_OK:
+            return kv_cache
+        if st is not None:
+            raise KvcError(st, "kvc_store")
     device, pages, form = _pages(kv_cache)
     if not isinstance(x, torch.Tensor) or x.dtype not in _dtype_codes:
         raise TypeError("x must be a tensor of dtype torch.float32 or torch.bfloat16")
@@ -972,6 +995,12 @@ def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out
     recorded.
     """
     torch = _torch or _load_torch()
+    if out is not None and stream is None and _quick is not None:
+        st = _quick.rotate(x, positions, cos_sin_cache, axes, inverse, out)
+        if st == KVC_OK:
+            return out
+        if st is not None:
+            raise KvcError(st, "kvc_rotate")
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA tensor (there is no CPU path)")
     device, dtype, shape, strides = x.get_device(), x.dtype, x.shape, x.stride()
@@ -1033,6 +1062,12 @@ def attend(q, kv_cache, page_table, lengths, scale=None, *, sinks=None, out=None
     every head.  A serving form: no gradient is recorded.
     """
     torch = _torch or _load_torch()
+    if workspace is not None and stream is None and _quick is not None:  # (out and lse are looked at there)
+        st = _quick.attend(q, kv_cache, page_table, lengths, scale, sinks, out, lse, slot_weights, slot_weights_in, flags, workspace)
+        if st == KVC_OK:
+            return out, lse
+        if st is not None:
+            raise KvcError(st, "kvc_attend")
     device, pages, form, R, columns, row = _cache(kv_cache, page_table, lengths)
     if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.get_device() != device or q.dim() != 3:
         _refuse("q", q, torch.bfloat16, 3, device)

@@ -1346,7 +1346,13 @@ __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const
   const float4* const parts = reinterpret_cast<const float4*>(p.parts) + col * (kHeadDim / 4) + t;
   const int64_t apart = static_cast<int64_t>(n) * (kHeadDim / 4);
   const float sink = p.sinks == nullptr ? -INFINITY : p.sinks[head] * kLog2e;
-  float2 ml[kStatsPerLane];  // all at once: one latency, not one for each
+  // all at once, and the first parts with them: one latency, not one for each
+  constexpr int kFirst = 2;
+  float4 o[kFirst];
+#pragma unroll
+  for (int k = 0; k < kFirst; ++k)
+    if (from + k * step < count) o[k] = parts[d.part(from + k * step) * apart];
+  float2 ml[kStatsPerLane];
   int any = 0;
 #pragma unroll
   for (int k = 0; k < kStatsPerLane; ++k) {
@@ -1377,15 +1383,17 @@ __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const
   *lse = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
   __syncwarp();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float f, const float4& part) {
+    acc.x += f * part.x;
+    acc.y += f * part.y;
+    acc.z += f * part.z;
+    acc.w += f * part.w;
+  };
+#pragma unroll
+  for (int k = 0; k < kFirst; ++k)
+    if (from + k * step < count) add(w[from + k * step], o[k]);
 #pragma unroll 4
-  for (int j = from; j < count; j += step) {
-    const float f = w[j];
-    const float4 o = parts[d.part(j) * apart];
-    acc.x += f * o.x;
-    acc.y += f * o.y;
-    acc.z += f * o.z;
-    acc.w += f * o.w;
-  }
+  for (int j = from + kFirst * step; j < count; j += step) add(w[j], parts[d.part(j) * apart]);
   __syncwarp();  // w is free again
   return acc;
 }
@@ -1399,7 +1407,7 @@ __device__ __forceinline__ float2 unit_stats(const AttendParams& p, int n, const
   float total = p.sinks == nullptr || first != 0 ? 0.f : exp2_fast(p.sinks[head] * kLog2e - top);
   const int count = d.count();
   int any = 0;
-#pragma unroll 8
+#pragma unroll 4
   for (int j = first; j < count; j += with) {
     const float2 ml = p.part_stats[d.part(j) * n + col];
     any |= p.part_bad[d.part(j)];
@@ -1424,19 +1432,108 @@ __device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row,
   if (t == 0) p.lse[row] = lse;
 }
 
+// The weights of slots [length * sub / subs, length * (sub + 1) / subs) of request r.
+// What does not depend on anything read is asked for first, the scores beside the
+// parts' stats: two latencies.
+struct WeightsShared {
+  __align__(16) float tops[2 * 64], shares[2 * 64];
+  int skip;
+};
+__device__ __forceinline__ void form_weights(const AttendParams& p, WeightsShared& s, int n, int r, int sub, int subs) {
+  constexpr int kAhead = 4;  // slots of a thread on their way
+  const int t = threadIdx.x;
+  // The heads' references and 1 / sums, by column of the scores: 0 where there is
+  // no head or no key.  (Not the log of the sum in their place: it is a number
+  // of the scores' size, and what its rounding loses would be a factor of every
+  // weight, 2 % at scores of 1e5.)
+  // A column to each kJoinThreads / score_cols threads (4 .. 32), which share its parts.
+  const int with = kJoinThreads / static_cast<int>(p.score_cols), col = t / with, first = t % with;
+  const int unit = col / n, c = col % n, head = unit * p.group_heads + c;
+  const bool is_head = c < p.group_heads && head < p.num_heads;
+  const int64_t length = p.lengths[r];
+  int2 parts = make_int2(-1, 0);
+  float2 whole = make_float2(0.f, 0.f);
+  if (is_head) {
+    parts = p.unit_parts[static_cast<int64_t>(r) * p.groups + unit];
+    whole = p.row_stats[static_cast<int64_t>(r) * p.num_heads + head];
+  }
+  if (length < 0 || length > p.max_slots) return;
+  if (length == 0) {
+    if (sub == 0) write_empty(p, r);
+    return;
+  }
+  const int begin = static_cast<int>(length * sub / subs), end = static_cast<int>(length * (sub + 1) / subs);
+  if (begin == end) return;
+  // 4 columns a thread, `lanes` threads a slot
+  const int lanes = static_cast<int>(p.score_cols) / 4, step = kJoinThreads / lanes;
+  const float* const weights_in = p.weights_in == nullptr ? nullptr : p.weights_in + r * p.weights_in_row_stride;
+  float* const weights_out = p.weights_out + r * p.weights_out_row_stride;
+  const float4* const scores =
+      reinterpret_cast<const float4*>(p.scores + r * p.max_pages * kSlotsPerPage * p.score_cols) + t % lanes;
+  float4 x[kAhead];
+  float old[kAhead];
+  auto fetch = [&](int from) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int slot = from + k * step + t / lanes;
+      old[k] = 0.f;
+      if (slot < end) {
+        x[k] = scores[static_cast<int64_t>(slot) * lanes];
+        if (weights_in != nullptr) old[k] = weights_in[slot];
+      }
+    }
+  };
+  fetch(begin);
+  if (t == 0) s.skip = 0;
+  __syncthreads();
+  float2 v = make_float2(0.f, 0.f);
+  if (is_head) {
+    if (parts.x < 0) {
+      if (parts.y) s.skip = 1;
+      v = whole;
+    } else {
+      v = unit_stats(p, n, Division{parts.x, parts.y}, c, head, first, with, &s.skip);
+    }
+  }
+  if (first == 0) {
+    s.tops[col] = v.x;
+    s.shares[col] = v.y;
+  }
+  __syncthreads();
+  if (!s.skip) {
+    const float4 m = *reinterpret_cast<const float4*>(s.tops + 4 * (t % lanes));
+    const float4 f = *reinterpret_cast<const float4*>(s.shares + 4 * (t % lanes));
+    for (int from = begin; from < end; from += kAhead * step) {  // a warp stays together
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int slot = from + k * step + t / lanes;
+        float sum = 0.f;
+        if (slot < end)
+          sum = (f.x == 0.f ? 0.f : exp2_fast(x[k].x - m.x) * f.x) + (f.y == 0.f ? 0.f : exp2_fast(x[k].y - m.y) * f.y) +
+                (f.z == 0.f ? 0.f : exp2_fast(x[k].z - m.z) * f.z) + (f.w == 0.f ? 0.f : exp2_fast(x[k].w - m.w) * f.w);
+        for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if (slot < end && t % lanes == 0) weights_out[slot] = old[k] + sum;
+      }
+      fetch(from + kAhead * step);
+    }
+  }
+  __syncthreads();  // s is free again
+}
+
 // Joins the divided units, zeroes the rows without slots, forms the weights.
 // An item is a head of a divided unit, 128 threads' work if that fills the grid.
 // Else it is a CTA's, whose four groups of 128 take a quarter of the parts each,
 // or, where that leaves CTAs without work, 2 or 4 CTAs', each for a part of the
-// dims and with as many more groups.
+// dims and with as many more groups.  Where weights are wanted as well, half of the
+// CTAs form them meanwhile: neither needs what the other makes, and both are chains
+// of latencies more than anything else.
+template <bool kWeights>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_kernel(const __grid_constant__ AttendParams p,
-                                                                        int n, int ctas, int weight_ctas) {
+                                                                        int n, int ctas) {
   __shared__ int4 joins[kAttendCtas];
   __shared__ int warp_joins[kJoinThreads / 32];
   __shared__ float4 sums[kJoinThreads];
   __shared__ float part_weights[kJoinThreads / 32][32 * kStatsPerLane];
-  __shared__ __align__(16) float tops[2 * 64], shares[2 * 64];
-  __shared__ int skip;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1452,100 +1549,52 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
     if (i < warp) before += warp_joins[i];
     divided += warp_joins[i];
   }
-  if (mine.x >= 0) joins[before] = mine;
-  __syncthreads();
-  const int heads = divided * p.group_heads, grid = static_cast<int>(gridDim.x);
-  const bool apart = heads >= 2 * grid;  // a head to each 128 threads
-  const int cuts = 4 * heads <= grid ? 4 : 2 * heads <= grid ? 2 : 1, size = 128 / cuts;
-  const int group = t / size, groups = kJoinThreads / size, items = heads * cuts;
-  for (int item = apart ? 4 * static_cast<int>(blockIdx.x) + group : static_cast<int>(blockIdx.x); item < items;
-       item += apart ? 4 * grid : grid) {
-    const int unit = item / cuts, at = item % cuts * size + t % size;
-    const int4 join = joins[unit / p.group_heads];
-    const int col = unit % p.group_heads, head = join.y * p.group_heads + col;
-    if (head >= p.num_heads) continue;
-    float f, lse;
-    bool bad;
-    float4 v = join_parts(p, n, Division{join.z, join.w}, col, head, at, apart ? 0 : group, apart ? 1 : groups,
-                          part_weights[warp], &f, &lse, &bad);
-    if (!apart) {
-      sums[t] = v;
-      __syncthreads();
-      if (group == 0) {
-        for (int g = 1; g < groups; ++g) {
-          const float4 o = sums[g * size + t];
-          v.x += o.x;
-          v.y += o.y;
-          v.z += o.z;
-          v.w += o.w;
+  const int block = static_cast<int>(blockIdx.x), all = static_cast<int>(gridDim.x);
+  const int grid = !kWeights ? all : divided == 0 ? 0 : all / 2;  // that join
+  if (block < grid) {
+    if (mine.x >= 0) joins[before] = mine;
+    __syncthreads();
+    const int heads = divided * p.group_heads;
+    const bool apart = heads >= 2 * grid;  // a head to each 128 threads
+    const int cuts = 4 * heads <= grid ? 4 : 2 * heads <= grid ? 2 : 1, size = 128 / cuts;
+    const int group = t / size, groups = kJoinThreads / size, items = heads * cuts;
+    for (int item = apart ? 4 * block + group : block; item < items; item += apart ? 4 * grid : grid) {
+      const int unit = item / cuts, at = item % cuts * size + t % size;
+      const int4 join = joins[unit / p.group_heads];
+      const int col = unit % p.group_heads, head = join.y * p.group_heads + col;
+      if (head >= p.num_heads) continue;
+      float f, lse;
+      bool bad;
+      float4 v = join_parts(p, n, Division{join.z, join.w}, col, head, at, apart ? 0 : group, apart ? 1 : groups,
+                            part_weights[warp], &f, &lse, &bad);
+      if (!apart) {
+        sums[t] = v;
+        __syncthreads();
+        if (group == 0) {
+          for (int g = 1; g < groups; ++g) {
+            const float4 o = sums[g * size + t];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
+      if (!bad && (apart || group == 0))
+        store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, at, v, f, lse);
     }
-    if (!bad && (apart || group == 0))
-      store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, at, v, f, lse);
   }
-  // requests: `weight_ctas` CTAs for each
-  for (int item = blockIdx.x; item < p.num_reqs * weight_ctas; item += grid) {
-    const int r = item / weight_ctas, sub = item % weight_ctas;
-    const int64_t length = p.lengths[r];
-    if (length < 0 || length > p.max_slots) continue;
-    if (length == 0) {
-      if (sub != 0) continue;
-      write_empty(p, r);
-      continue;
-    }
-    if (p.weights_out == nullptr || length * sub / weight_ctas == length * (sub + 1) / weight_ctas) continue;
-    // The heads' references and 1 / sums, by column of the scores: 0 where there is
-    // no head or no key.  (Not the log of the sum in their place: it is a number
-    // of the scores' size, and what its rounding loses would be a factor of every
-    // weight, 2 % at scores of 1e5.)
-    if (t == 0) skip = 0;
-    __syncthreads();
-    {
-      // a column to each kJoinThreads / score_cols threads (4 .. 32), which share its parts
-      const int with = kJoinThreads / static_cast<int>(p.score_cols), col = t / with, first = t % with;
-      const int unit = col / n, c = col % n, head = unit * p.group_heads + c;
-      float2 v = make_float2(0.f, 0.f);
-      if (c < p.group_heads && head < p.num_heads) {
-        const int2 parts = p.unit_parts[static_cast<int64_t>(r) * p.groups + unit];
-        if (parts.x < 0) {
-          if (parts.y) skip = 1;
-          v = p.row_stats[static_cast<int64_t>(r) * p.num_heads + head];
-        } else {
-          v = unit_stats(p, n, Division{parts.x, parts.y}, c, head, first, with, &skip);
-        }
-      }
-      if (first == 0) {
-        tops[col] = v.x;
-        shares[col] = v.y;
-      }
-    }
-    __syncthreads();
-    if (!skip) {
-      // 4 columns a thread, `lanes` threads a slot
-      const int lanes = static_cast<int>(p.score_cols) / 4, step = kJoinThreads / lanes;
-      const float4 m = *reinterpret_cast<const float4*>(tops + 4 * (t % lanes));
-      const float4 f = *reinterpret_cast<const float4*>(shares + 4 * (t % lanes));
-      const float* const weights_in = p.weights_in == nullptr ? nullptr : p.weights_in + r * p.weights_in_row_stride;
-      float* const weights_out = p.weights_out + r * p.weights_out_row_stride;
-      const float4* const scores =
-          reinterpret_cast<const float4*>(p.scores + r * p.max_pages * kSlotsPerPage * p.score_cols) + t % lanes;
-      const int begin = static_cast<int>(length * sub / weight_ctas), end = static_cast<int>(length * (sub + 1) / weight_ctas);
-#pragma unroll 4
-      for (int slot = begin + t / lanes; slot < end + t / lanes; slot += step) {  // a warp stays together
-        float sum = 0.f, old = 0.f;
-        if (slot < end) {
-          const float4 x = scores[static_cast<int64_t>(slot) * lanes];
-          if (weights_in != nullptr) old = weights_in[slot];
-          sum = (f.x == 0.f ? 0.f : exp2_fast(x.x - m.x) * f.x) + (f.y == 0.f ? 0.f : exp2_fast(x.y - m.y) * f.y) +
-                (f.z == 0.f ? 0.f : exp2_fast(x.z - m.z) * f.z) + (f.w == 0.f ? 0.f : exp2_fast(x.w - m.w) * f.w);
-        }
-        for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (slot < end && t % lanes == 0) weights_out[slot] = old + sum;
-      }
-    }
-    __syncthreads();  // tops, shares and skip are free again
+  if constexpr (!kWeights) {
+    for (int r = block; r < p.num_reqs; r += all)
+      if (p.lengths[r] == 0) write_empty(p, r);
+  } else if (block >= grid) {
+    __shared__ WeightsShared weights;
+    // as many CTAs to a request as there are for all at once, and pages for each
+    const int with = all - grid, pages = static_cast<int>((p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage);
+    const int subs = max(1, min(pages, with / static_cast<int>(p.num_reqs)));
+    for (int item = block - grid; item < p.num_reqs * subs; item += with)
+      form_weights(p, weights, n, item / subs, item % subs, subs);
   }
 }
 
@@ -1568,19 +1617,18 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N, F>, p);
   if (e != cudaSuccess || p.alone) return e;
-  // as many as fit at once: they share the divided units' heads, then the requests,
-  // one turn each (24 requests of up to 2050 slots, 32 heads: 22.6 us, in two turns 3 more)
+  // as many as fit at once: they share the divided units' heads and the requests, one
+  // turn each where that can be (24 requests of up to 2050 slots, 32 heads: in two
+  // turns 3 us more)
   constexpr int kMost = kJoinCtasPerSm * kAttendCtas;
-  const int64_t chunks = p.weights_out == nullptr ? 1 : (p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage;
-  int64_t weight_ctas = kMost / p.num_reqs;
-  weight_ctas = weight_ctas > chunks ? chunks : weight_ctas;
-  weight_ctas = weight_ctas < 1 ? 1 : weight_ctas;
-  const int64_t joins = 4 * static_cast<int64_t>(ctas) * p.group_heads, items = p.num_reqs * weight_ctas;
-  const int64_t work = joins > items ? joins : items;
+  const int64_t pages = (p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage;
+  const int64_t joins = 4 * static_cast<int64_t>(ctas) * p.group_heads;
+  const int64_t work = p.weights_out == nullptr ? (joins > p.num_reqs ? joins : p.num_reqs) : 2 * joins + p.num_reqs * pages;
   cfg.gridDim = dim3(static_cast<unsigned>(work < kMost ? work : kMost));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kvc_attend_join_kernel, p, N, ctas, static_cast<int>(weight_ctas));
+  return p.weights_out == nullptr ? cudaLaunchKernelEx(&cfg, kvc_attend_join_kernel<false>, p, N, ctas)
+                                  : cudaLaunchKernelEx(&cfg, kvc_attend_join_kernel<true>, p, N, ctas);
 }
 
 }  // namespace
