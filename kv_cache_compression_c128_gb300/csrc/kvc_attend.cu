@@ -830,7 +830,7 @@ __device__ void second_role(const AttendParams& p, AttendShared<N, F>& s, int co
 }
 
 // Columns `from` .. `to` - 1 of the four chunks' 4 N, the lanes of a warp.
-template <int N, typename F>
+template <int N, typename F, bool kAlone>
 __device__ __forceinline__ void write_rows(const AttendParams& p, const AttendShared<N, F>& s, const Rows& rows, int from,
                                            int to) {
   constexpr int kWide = N == 16 ? 16 : 32;  // columns at a time
@@ -844,7 +844,7 @@ __device__ __forceinline__ void write_rows(const AttendParams& p, const AttendSh
 #pragma unroll
     for (int j = 0; j < kWide; j += 16) tmem_ld_32x16(tmem + at + j, o + j);
     tmem_wait_ld();
-    if (rows.whole) {
+    if (kAlone || rows.whole) {
       const bool odd = lane & 1;
       uint16_t* const out = p.out + (rows.row0 + b + odd) * kHeadDim + (d & ~1);
 #pragma unroll
@@ -905,7 +905,7 @@ __device__ __forceinline__ void store_combined(const float (&v)[kCount], int lan
 
 // Softmax warps.  Warp w has slots 16 w .. 16 w + 15 of a page: thread t the
 // slots t / 4 and t / 4 + 8 of them, and columns 2 (t % 4) + {0, 1} of each 8.
-template <int N, typename F>
+template <int N, typename F, bool kAlone>
 __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk w) {
   constexpr int kCols = N / 4;  // columns of a thread
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -913,7 +913,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
   const float c = p.scale == 0.f ? 1.f : p.scale * kLog2e;  // scores of scale 0 are zeros
   const int row = warp * 16 + (lane >> 2);
   const int cta = blockIdx.x;
-  int i = 0, at = share_start(s.total, cta, s.ctas);  // (used with equal shares)
+  int i = 0, at = kAlone ? 0 : share_start(s.total, cta, s.ctas);  // (used with equal shares)
   bool ok = true;  // once false, the next vote ends the role
 #pragma unroll 1
   for (int segment = 0; w.left > 0; ++segment) {
@@ -950,7 +950,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
         for (int j = 0; j < 2 * kCols; ++j)
           if (!((j & 2) ? in1 : in0)) x[j] = -INFINITY;
       }
-      if (__builtin_expect(p.scores != nullptr, 0)) {
+      if (!kAlone && __builtin_expect(p.scores != nullptr, 0)) {
         float* dst = p.scores + ((w.req * p.max_pages + w.page + pg) * kSlotsPerPage + row) * p.score_cols +
                      w.group * N + 2 * (lane & 3);
 #pragma unroll
@@ -1046,7 +1046,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
       for (int j = 0; j < kCols; ++j) s.ref[8 * (j >> 1) + 2 * lane + (j & 1)] = ref[j];
     }
     softmax_sync();
-    const bool whole = n == w.pages, bad = s.bad[segment & 7] != 0;
+    const bool whole = kAlone || n == w.pages, bad = s.bad[segment & 7] != 0;
     const int part = 2 * cta + (segment > 0);
     const int heads = heads_of<N>(p, w.group);
     const int64_t row0 = static_cast<int64_t>(w.req) * p.num_heads + w.group * p.group_heads;
@@ -1063,14 +1063,14 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
           total = l * f + exp2_fast(sink - top);
         }
         if (!bad) p.lse[row0 + t] = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
-        if (p.row_stats != nullptr) p.row_stats[row0 + t] = make_float2(top, total == 0.f ? 0.f : 1.f / total);
+        if (!kAlone && p.row_stats != nullptr) p.row_stats[row0 + t] = make_float2(top, total == 0.f ? 0.f : 1.f / total);
         f = total == 0.f ? 0.f : f / total;
       } else {
         p.part_stats[part * N + t] = make_float2(m, l);
       }
       s.factor[t] = f;
     }
-    if (t == 0) {
+    if (!kAlone && t == 0) {
       if (w.page == 0) {  // the unit's first part: where its parts lie
         p.unit_parts[static_cast<int64_t>(w.req) * p.groups + w.group] =
             whole ? make_int2(-1, bad)
@@ -1093,11 +1093,11 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
     if (t == 0) s.bad[segment & 7] = 0;
     tc_fence_after();
     const Rows rows{row0, part, whole && bad ? 0 : heads, whole};
-    if (w.left == n) {  // of the last segment the whole CTA writes the rows
+    if (kAlone || w.left == n) {  // of the last segment the whole CTA writes the rows
       if (t == 0) s.rows = rows;
       return;
     }
-    write_rows<N, F>(p, s, rows, 0, 4 * N);
+    write_rows<N, F, kAlone>(p, s, rows, 0, 4 * N);
     tc_fence_before();
     softmax_sync();  // s.red, s.factor and O are free again
     at += n;
@@ -1151,35 +1151,34 @@ __device__ __forceinline__ void write_empty(const AttendParams& p, int64_t r) {
   if (threadIdx.x < p.num_heads) p.lse[row0 + threadIdx.x] = p.sinks == nullptr ? -INFINITY : p.sinks[threadIdx.x];
 }
 
+// Where a CTA's share lies, in s; all threads.  A unit to each CTA where nothing can
+// be left to join (attend_alone): without a look at the other requests, and with the
+// unit's page ids asked for beside its length.
 template <int N, typename F>
-__global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __grid_constant__ AttendParams p) {
-  extern __shared__ __align__(1024) uint8_t raw_shared[];
-  AttendShared<N, F>& s = *reinterpret_cast<AttendShared<N, F>*>(raw_shared);
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int cta = blockIdx.x;
-  if (warp == kFirstWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
-  if (t == 0) {
-    for (int i = 0; i < 2; ++i) {
-      for (int j = 0; j < 2; ++j) dev::mbar_init(&s.bar.half_full[i][j], 4);
-      for (int j = 0; j < 4; ++j) dev::mbar_init(&s.bar.chunk_empty[i][j], 1);
-      dev::mbar_init(&s.bar.s_full[i], 1);
-    }
-    for (int i = 0; i < weight_places<N, F>(); ++i) dev::mbar_init(&s.bar.p_full[i], kSoftmaxWarps);
-    dev::mbar_init(&s.bar.q_full, 1);
-    dev::mbar_init(&s.bar.q_empty, 1);
-    dev::mbar_init(&s.bar.o_full, 1);
-    for (int i = 0; i < 2; ++i) dev::mbar_init(&s.bar.drain[i], 1);
-    for (int i = 0; i < depth<N, F>() * ring_groups<N, F>(); ++i) {
-      dev::mbar_init(&s.bar.piece_full[0][0] + i, 1);
-      dev::mbar_init(&s.bar.piece_empty[0][0] + i, 1);
-    }
-    for (int i = 0; i < kInfos; ++i) dev::mbar_init(&s.bar.info_full[i], 1);
-    dev::fence_mbar_init();
-    s.abort = 0;
-    for (int i = 0; i < 8; ++i) s.bad[i] = 0;
+__device__ __forceinline__ void take_unit(const AttendParams& p, AttendShared<N, F>& s) {
+  const int cta = blockIdx.x, req = cta / p.groups, t = threadIdx.x;
+  const bool there = req < p.num_reqs;
+  if (there && t < kUndivided && t < p.max_pages) {
+    int32_t id;  // (into the cache that the copying warp then reads it from)
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(id) : "l"(p.page_table + req * p.page_table_row_stride + t));
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (t != 0) return;
+  const int64_t length = there ? p.lengths[req] : 0;
+  if (length < 0 || length > p.max_slots) atomicCAS(p.error, 0u, kErrBadIndex);
+  const int pages = pages_of(p, length);
+  s.start[0] = req;
+  s.start[1] = static_cast<int>(length);
+  s.start[2] = cta % p.groups;
+  s.start[3] = 0;
+  s.total = s.ctas = 0;
+  s.count = pages;
+  s.each = pages;
+  s.rows.heads = 0;
+}
+
+template <int N, typename F>
+__device__ __forceinline__ void find_share(const AttendParams& p, AttendShared<N, F>& s) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, cta = blockIdx.x;
   // Where the share lies: the pages (the host has checked that all fit 31 bits)
   // and the units before each thread's run of requests.  Up to kFewReqs requests
   // every warp finds it for itself, a run of requests a lane.
@@ -1273,6 +1272,44 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     s.rows.heads = 0;
     p.joins[cta] = make_int4(-1, 0, 0, 0);
   }
+}
+
+// kAlone: nothing can be left to join (attend_alone), so that a unit is a CTA's; a
+// kernel of its own, whose code is shorter, and the other's no longer for it (64 x
+// 8192 slots, 64 heads, 8 bits: 118 us, with both in one 125).
+template <int N, typename F, bool kAlone>
+__global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __grid_constant__ AttendParams p) {
+  extern __shared__ __align__(1024) uint8_t raw_shared[];
+  AttendShared<N, F>& s = *reinterpret_cast<AttendShared<N, F>*>(raw_shared);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int cta = blockIdx.x;
+  if (warp == kFirstWarp) tmem_alloc(&s.tmem, tmem_columns<N>());
+  if (t == 0) {
+    for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < 2; ++j) dev::mbar_init(&s.bar.half_full[i][j], 4);
+      for (int j = 0; j < 4; ++j) dev::mbar_init(&s.bar.chunk_empty[i][j], 1);
+      dev::mbar_init(&s.bar.s_full[i], 1);
+    }
+    for (int i = 0; i < weight_places<N, F>(); ++i) dev::mbar_init(&s.bar.p_full[i], kSoftmaxWarps);
+    dev::mbar_init(&s.bar.q_full, 1);
+    dev::mbar_init(&s.bar.q_empty, 1);
+    dev::mbar_init(&s.bar.o_full, 1);
+    for (int i = 0; i < 2; ++i) dev::mbar_init(&s.bar.drain[i], 1);
+    for (int i = 0; i < depth<N, F>() * ring_groups<N, F>(); ++i) {
+      dev::mbar_init(&s.bar.piece_full[0][0] + i, 1);
+      dev::mbar_init(&s.bar.piece_empty[0][0] + i, 1);
+    }
+    for (int i = 0; i < kInfos; ++i) dev::mbar_init(&s.bar.info_full[i], 1);
+    dev::fence_mbar_init();
+    s.abort = 0;
+    for (int i = 0; i < 8; ++i) s.bad[i] = 0;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (kAlone)
+    take_unit(p, s);
+  else
+    find_share(p, s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1287,7 +1324,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
     w.left = count;
     if (warp < kSoftmaxWarps) {
       more_registers<kSoftmaxRegs>();
-      softmax_role<N, F>(p, s, w);
+      softmax_role<N, F, kAlone>(p, s, w);
     } else {
       fewer_registers<kOtherRegs>();
       const int worker = warp - kSoftmaxWarps - (warp > kFirstWarp) - (warp > copy_warp<F>());
@@ -1311,15 +1348,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1) kvc_attend_kernel(const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s.rows.heads > 0) write_rows<N, F>(p, s, s.rows, (warp >> 2) * N, (warp >> 2) * N + N);
-  if (p.alone) {
-#pragma unroll 1
-    for (int r = cta; r < reqs; r += grid)
-      if (p.lengths[r] == 0) write_empty(p, r);
+  if (s.rows.heads > 0) write_rows<N, F, kAlone>(p, s, s.rows, (warp >> 2) * N, (warp >> 2) * N + N);
+  if constexpr (kAlone) {  // (as many CTAs as units, or more)
+    if (cta < p.num_reqs && p.lengths[cta] == 0) write_empty(p, cta);
   }
   if (t == 0 && s.abort) {
     atomicCAS(p.error, 0u, kErrTimeout);
-    p.joins[cta] = make_int4(-2, 0, 0, 0);
+    if constexpr (!kAlone) p.joins[cta] = make_int4(-2, 0, 0, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -1602,7 +1637,8 @@ template <int N, typename F>
 cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   constexpr size_t smem = sizeof(AttendShared<N, F>);
   static_assert(smem <= 232448, "227 KB a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kvc_attend_kernel<N, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = p.alone ? &kvc_attend_kernel<N, F, true> : &kvc_attend_kernel<N, F, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -1615,7 +1651,7 @@ cudaError_t launch_n(const AttendParams& p, int ctas, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kvc_attend_kernel<N, F>, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess || p.alone) return e;
   // as many as fit at once: they share the divided units' heads and the requests, one
   // turn each where that can be (24 requests of up to 2050 slots, 32 heads: in two
