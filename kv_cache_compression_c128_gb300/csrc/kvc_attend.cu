@@ -1130,15 +1130,13 @@ __device__ __forceinline__ Shares aligned_shares(const AttendParams& p, int4* sc
   const int all = __reduce_add_sync(0xFFFFFFFFu, of.own) * p.groups;
   if (lane == 0) scan[warp].x = all;
   __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < kAttendThreads / 32 && least + i <= most; ++i) {
-    of.count = scan[i].x;
-    if (of.count > grid) continue;
-    of.each = least + i;
-    of.finder = i;
-    of.before = warp_inclusive(of.own, lane) - of.own;
-    break;
-  }
+  const int suffices = lane < kAttendThreads / 32 && least + lane <= most ? scan[lane].x : INT_MAX;
+  const uint32_t which = __ballot_sync(0xFFFFFFFFu, suffices <= grid);
+  if (which == 0) return of;
+  of.finder = __ffs(which) - 1;
+  of.each = least + of.finder;
+  of.count = __shfl_sync(0xFFFFFFFFu, suffices, of.finder);
+  of.before = warp_inclusive(of.own, lane) - of.own;
   return of;
 }
 
@@ -1590,7 +1588,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
     if (mine.x >= 0) joins[before] = mine;
     __syncthreads();
     const int heads = divided * p.group_heads;
-    const bool apart = heads >= 2 * grid;  // a head to each 128 threads
+    const bool apart = heads > grid;  // a head to each 128 threads
     const int cuts = 4 * heads <= grid ? 4 : 2 * heads <= grid ? 2 : 1, size = 128 / cuts;
     const int group = t / size, groups = kJoinThreads / size, items = heads * cuts;
     for (int item = apart ? 4 * block + group : block; item < items; item += apart ? 4 * grid : grid) {

@@ -34,9 +34,6 @@ namespace kvc {
 namespace {
 
 constexpr int kWarps = 8;
-// Slots to read up to which a warp has one: with more, the card is full of warps.
-constexpr int64_t kFewRows = 152 * 64;
-
 __device__ __forceinline__ uint32_t round2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -199,7 +196,13 @@ __global__ void __launch_bounds__(kWarps * 32) kvc_store_kernel(const __grid_con
 
 // A warp has kSlots slots, all loads of all of them ahead of the first store.  Where
 // bf16 is asked for, lane l has dims 8 l .. + 7 and 256 + 8 l .. + 7 of each; of fp32
-// values dims 4 l + 128 k .. + 3, k < 4: every store covers one run.
+// values dims 4 l + 128 k .. + 3, k < 4: every store covers one run.  Bound by the
+// bytes: 262144 slots in any order take 60 us in bf16 (6.1 TB/s of what a slot and a
+// row have, and a slot's bytes come in pieces of 64) and 98 in fp32 (6.5 TB/s).
+// Slots of a warp, us, 1 / 2 / 3 / 4: 500 slots, bf16 1.6 / 1.7 / 1.9 / 2.0; 10000
+// 2.9 / 3.4 / 2.9 / 3.8; 40000 11.3 / 10.9 / 10.5 / 11.4; 262144 65.1 / 60.2 / 60.2 /
+// 62.2; fp32 98.1 / 98.7 / 99.4 / 103.4, and one is best at every size.
+constexpr int64_t kFewSlots = 152 * 64;  // as many warps as fit at once
 template <bool kBf16, int kSlots>
 __global__ void __launch_bounds__(kWarps * 32) kvc_dequantize4_kernel(const uint8_t* kv, int64_t num_pages,
                                                                       const int64_t* slots, int64_t num_slots, void* out,
@@ -299,11 +302,11 @@ cudaError_t launch_store(const StoreParams& p, bool four_bits, cudaStream_t stre
 
 cudaError_t launch_dequantize4(const uint8_t* kv, int64_t num_pages, const int64_t* slots, int64_t num_slots, void* out,
                                int out_bf16, uint32_t* err, cudaStream_t stream) {
-  if (num_slots <= kFewRows)
-    return out_bf16 ? launch_rows(kvc_dequantize4_kernel<true, 1>, num_slots, 1, stream, kv, num_pages, slots, num_slots, out, err)
-                    : launch_rows(kvc_dequantize4_kernel<false, 1>, num_slots, 1, stream, kv, num_pages, slots, num_slots, out, err);
-  return out_bf16 ? launch_rows(kvc_dequantize4_kernel<true, 4>, num_slots, 4, stream, kv, num_pages, slots, num_slots, out, err)
-                  : launch_rows(kvc_dequantize4_kernel<false, 4>, num_slots, 4, stream, kv, num_pages, slots, num_slots, out, err);
+  if (!out_bf16)
+    return launch_rows(kvc_dequantize4_kernel<false, 1>, num_slots, 1, stream, kv, num_pages, slots, num_slots, out, err);
+  return num_slots <= kFewSlots
+             ? launch_rows(kvc_dequantize4_kernel<true, 1>, num_slots, 1, stream, kv, num_pages, slots, num_slots, out, err)
+             : launch_rows(kvc_dequantize4_kernel<true, 3>, num_slots, 3, stream, kv, num_pages, slots, num_slots, out, err);
 }
 
 }  // namespace kvc
