@@ -101,15 +101,20 @@ __device__ __forceinline__ uint32_t codes4(const uint4& w, uint32_t byte) {
 }
 
 // 8 codes of 8 bits with the scale 2^e: z 2^-e is exact, and at most 127 in size unless
-// it is infinite.
+// it is infinite (kInfinite: some may be).
+template <bool kInfinite>
 __device__ __forceinline__ uint2 codes8(const uint4& w, int e) {
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
   uint32_t two[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int lo = max(-127, min(127, __float2int_rz(__fmul_rn(dev::bf16_lo(words[i]), inv))));
-    const int hi = max(-127, min(127, __float2int_rz(__fmul_rn(dev::bf16_hi(words[i]), inv))));
+    int lo = __float2int_rz(__fmul_rn(dev::bf16_lo(words[i]), inv));
+    int hi = __float2int_rz(__fmul_rn(dev::bf16_hi(words[i]), inv));
+    if constexpr (kInfinite) {
+      lo = max(-127, min(127, lo));
+      hi = max(-127, min(127, hi));
+    }
     two[i] = __byte_perm(lo, hi, 0x0040);
   }
   return make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410));
@@ -163,12 +168,13 @@ __global__ void __launch_bounds__(kWarps * 32) kvc_store_kernel(const __grid_con
   uint8_t* const scales = base + F::kScaleBase + place * F::kScales;
   reinterpret_cast<uint32_t*>(payload + F::kCodes)[lane] = round2(pair.x, pair.y);
   constexpr int kLanes = F::kFour ? 4 : 8;
-  constexpr uint32_t kMost = F::kFour ? kMost4 : 0x7F80u;
+  // above what a scale holds, infinite or NaN (infinities have the largest 8-bit code)
+  constexpr uint32_t kMost = F::kFour ? kMost4 : 0x7F7Fu;
   uint32_t m = most_of_groups<kLanes>(v, w);
-  // above what a scale holds, or NaN (8 bits: infinities stay as they are)
-  if (__any_sync(0xFFFFFFFFu, (m & 0xFFFFu) > kMost || m >> 16 > kMost)) {
-    v = bring_in(v, kMost);
-    w = bring_in(w, kMost);
+  const bool beyond = __any_sync(0xFFFFFFFFu, (m & 0xFFFFu) > kMost || m >> 16 > kMost);
+  if (beyond) {
+    v = bring_in(v, F::kFour ? kMost : 0x7F80u);
+    w = bring_in(w, F::kFour ? kMost : 0x7F80u);
     m = most_of_groups<kLanes>(v, w);
   }
   const float a = __uint_as_float(m << 16), b = __uint_as_float(m & 0xFFFF0000u);
@@ -183,8 +189,10 @@ __global__ void __launch_bounds__(kWarps * 32) kvc_store_kernel(const __grid_con
     }
   } else {
     const int e0 = dev::scale_exponent(fmaxf(a, 1.0e-4f)), e1 = dev::scale_exponent(fmaxf(b, 1.0e-4f));
-    reinterpret_cast<uint2*>(payload)[lane] = codes8(v, e0);
-    if (lane < 24) reinterpret_cast<uint2*>(payload)[32 + lane] = codes8(w, e1);
+    const uint2 c0 = beyond ? codes8<true>(v, e0) : codes8<false>(v, e0);
+    const uint2 c1 = beyond ? codes8<true>(w, e1) : codes8<false>(w, e1);
+    reinterpret_cast<uint2*>(payload)[lane] = c0;
+    if (lane < 24) reinterpret_cast<uint2*>(payload)[32 + lane] = c1;
     if ((lane & 7) == 0) {
       scales[lane / 8] = static_cast<uint8_t>(e0 + 127);
       scales[4 + lane / 8] = static_cast<uint8_t>(lane < 24 ? e1 + 127 : 0);
