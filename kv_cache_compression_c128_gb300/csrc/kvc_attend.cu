@@ -1081,7 +1081,7 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
         if (w.page + n == w.pages) {  // the unit's last part: this share's joins it
           const int first = s.each > 0 ? cta - w.page / s.each : share_of(s.total, at - w.page, s.ctas);
           const bool at_start = s.each > 0 || share_start(s.total, first, s.ctas) == at - w.page;
-          p.joins[cta] = make_int4(w.req, w.group, 2 * first + !at_start, cta);
+          p.joins[cta] = make_int4(w.req, w.group, 2 * first + !at_start, s.total);
         }
       }
     }
@@ -1268,7 +1268,7 @@ __device__ __forceinline__ void find_share(const AttendParams& p, AttendShared<N
     s.count = count;
     s.each = aligned ? each : 0;
     s.rows.heads = 0;
-    p.joins[cta] = make_int4(-1, 0, 0, 0);
+    p.joins[cta] = make_int4(-1, 0, 0, total);
   }
 }
 
@@ -1473,7 +1473,7 @@ struct WeightsShared {
   int skip;
 };
 __device__ __forceinline__ void form_weights(const AttendParams& p, WeightsShared& s, int n, int r, int sub, int subs) {
-  constexpr int kAhead = 4;  // slots of a thread on their way
+  constexpr int kAhead = 3;  // slots of a thread on their way (4: spilled registers, half a microsecond)
   const int t = threadIdx.x;
   // The heads' references and 1 / sums, by column of the scores: 0 where there is
   // no head or no key.  (Not the log of the sum in their place: it is a number
@@ -1558,8 +1558,8 @@ __device__ __forceinline__ void form_weights(const AttendParams& p, WeightsShare
 // Else it is a CTA's, whose four groups of 128 take a quarter of the parts each,
 // or, where that leaves CTAs without work, 2 or 4 CTAs', each for a part of the
 // dims and with as many more groups.  Where weights are wanted as well, half of the
-// CTAs form them meanwhile: neither needs what the other makes, and both are chains
-// of latencies more than anything else.
+// CTAs or more form them meanwhile: neither needs what the other makes, and both are
+// chains of latencies more than anything else.
 template <bool kWeights>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_kernel(const __grid_constant__ AttendParams p,
                                                                         int n, int ctas) {
@@ -1571,10 +1571,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   // the divided units, in order
-  const int4 mine = t < ctas ? p.joins[t] : make_int4(-1, 0, 0, 0);
+  int4 mine = t < ctas ? p.joins[t] : make_int4(-1, 0, 0, 0);
+  const int pages = kWeights ? p.joins[0].w : 0;  // of all units
   // what a CTA that gave up has not written is not read
   if (__syncthreads_or(mine.x == -2)) return;
   const uint32_t there = __ballot_sync(0xFFFFFFFFu, mine.x >= 0);
+  mine.w = t;
   if (lane == 0) warp_joins[warp] = __popc(there);
   __syncthreads();
   int before = __popc(there & ((1u << lane) - 1)), divided = 0;
@@ -1583,7 +1585,11 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
     divided += warp_joins[i];
   }
   const int block = static_cast<int>(blockIdx.x), all = static_cast<int>(gridDim.x);
-  const int grid = !kWeights ? all : divided == 0 ? 0 : all / 2;  // that join
+  // that join: a third if the scores are more than a third of the parts' bytes, some
+  // ctas + divided parts (100 x up to 2000 slots, 64 heads: 51.1 us, half 62.4; 24 x up
+  // to 2050, 32 heads: 19.9, 18.7)
+  const bool many = 3.f * pages * n > 8.f * (ctas + divided) * p.group_heads;
+  const int grid = !kWeights ? all : divided == 0 ? 0 : many ? all / 3 : all / 2;
   if (block < grid) {
     if (mine.x >= 0) joins[before] = mine;
     __syncthreads();
@@ -1624,8 +1630,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   } else if (block >= grid) {
     __shared__ WeightsShared weights;
     // as many CTAs to a request as there are for all at once, and pages for each
-    const int with = all - grid, pages = static_cast<int>((p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage);
-    const int subs = max(1, min(pages, with / static_cast<int>(p.num_reqs)));
+    const int with = all - grid, longest = static_cast<int>((p.max_slots + kSlotsPerPage - 1) / kSlotsPerPage);
+    const int subs = max(1, min(longest, with / static_cast<int>(p.num_reqs)));
     for (int item = block - grid; item < p.num_reqs * subs; item += with)
       form_weights(p, weights, n, item / subs, item % subs, subs);
   }

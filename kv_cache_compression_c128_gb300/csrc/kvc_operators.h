@@ -104,7 +104,8 @@ struct AttendParams {
   int2* unit_parts;      // [num_reqs * groups]: first part and last CTA; (-1, bad) if whole
   float2* row_stats;     // [num_reqs, num_heads] of undivided units, for the weights: reference (log2) and
                          // 1 / sum (0: no key), or null
-  int4* joins;           // [ctas]: (request, group, first part, last CTA) to join, or (-1, ...)
+  int4* joins;           // [ctas]: (request, group, first part, pages of all units) of a unit whose last
+                         // CTA this is, or (-1, ...); (-2, ...) if it gave up
   long long wait_limit;
   uint32_t* error;
 };
