@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kWarps * 32) kvc_store_kernel(const __grid_con
 // bf16 is asked for, lane l has dims 8 l .. + 7 and 256 + 8 l .. + 7 of each; of fp32
 // values dims 4 l + 128 k .. + 3, k < 4: every store covers one run.  Bound by the
 // bytes: 262144 slots in any order take 60 us in bf16 (6.1 TB/s of what a slot and a
-// row have, and a slot's bytes come in pieces of 64) and 98 in fp32 (6.5 TB/s).
+// row have, and a slot's bytes come in pieces of 64) and 96 in fp32 (6.6 TB/s; 98
+// without stores that are evicted first; in bf16 they are level).
 // Slots of a warp, us, 1 / 2 / 3 / 4: 500 slots, bf16 1.6 / 1.7 / 1.9 / 2.0; 10000
 // 2.9 / 3.4 / 2.9 / 3.8; 40000 11.3 / 10.9 / 10.5 / 11.4; 262144 65.1 / 60.2 / 60.2 /
 // 62.2; fp32 98.1 / 98.7 / 99.4 / 103.4, and one is best at every size.
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__(kWarps * 32) kvc_dequantize4_kernel(const uint
         uint32_t a = fma_bf16x2((half & 0x000F000Fu) | 0x43004300u, s, less);
         uint32_t b = fma_bf16x2((half >> 4 & 0x000F000Fu) | 0x43004300u, s, less);
         if (tails) a = tail[u].x, b = tail[u].y;
-        reinterpret_cast<float4*>(static_cast<float*>(out) + (first + u) * kHeadDim)[32 * k + lane] =
-            make_float4(dev::bf16_lo(a), dev::bf16_hi(a), dev::bf16_lo(b), dev::bf16_hi(b));
+        __stcs(reinterpret_cast<float4*>(static_cast<float*>(out) + (first + u) * kHeadDim) + 32 * k + lane,
+               make_float4(dev::bf16_lo(a), dev::bf16_hi(a), dev::bf16_lo(b), dev::bf16_hi(b)));
       }
     }
   }
