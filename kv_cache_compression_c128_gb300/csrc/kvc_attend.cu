@@ -1372,12 +1372,14 @@ struct Division {
 
 // One head of a divided unit: 4 dims a thread of those at `t`, the sum of parts
 // `from`, `from` + `step`, ...  Every warp forms the parts' weights for itself,
-// in `w`.  Returns the sum; `scale` and `lse` are what finishes it.
+// in `w`.  Returns the sum; what finishes it are the reference (log2) and the sum of
+// the weights.  (Few instructions: 64 requests x 8192 slots have 4096 heads to join,
+// and 450 a warp and head, some 150 of them for parts beyond 32, were most of the
+// joining kernel's time.)
 __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const Division& d, int col, int head, int t,
-                                             int from, int step, float* w, float* scale, float* lse, bool* bad) {
-  const int lane = threadIdx.x & 31, count = d.count();
+                                             int from, int step, float* w, float2* stats, bool* bad) {
+  const int lane = threadIdx.x & 31, count = d.count(), apart = n * (kHeadDim / 4);
   const float4* const parts = reinterpret_cast<const float4*>(p.parts) + col * (kHeadDim / 4) + t;
-  const int64_t apart = static_cast<int64_t>(n) * (kHeadDim / 4);
   const float sink = p.sinks == nullptr ? -INFINITY : p.sinks[head] * kLog2e;
   // all at once, and the first parts with them: one latency, not one for each
   constexpr int kFirst = 2;
@@ -1387,45 +1389,53 @@ __device__ __forceinline__ float4 join_parts(const AttendParams& p, int n, const
     if (from + k * step < count) o[k] = parts[d.part(from + k * step) * apart];
   float2 ml[kStatsPerLane];
   int any = 0;
-#pragma unroll
-  for (int k = 0; k < kStatsPerLane; ++k) {
+  auto read = [&](int k) {
     const int j = lane + 32 * k;
     ml[k] = make_float2(-FLT_MAX, 0.f);
     if (j < count) {
       ml[k] = p.part_stats[d.part(j) * n + col];
       any |= p.part_bad[d.part(j)];
     }
+  };
+  read(0);
+  float top = sink;
+  if (count > 32) {
+#pragma unroll
+    for (int k = 1; k < kStatsPerLane; ++k) read(k);
+#pragma unroll
+    for (int k = 1; k < kStatsPerLane; ++k) top = fmaxf(top, ml[k].x);
   }
-  float top = sink, total = 0.f;
+  top = fmaxf(top, ml[0].x);
 #pragma unroll
-  for (int k = 0; k < kStatsPerLane; ++k) top = fmaxf(top, ml[k].x);
+  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+  const float f = exp2_fast(ml[0].x - top);
+  float total = ml[0].y * f;
+  w[lane] = f;
+  if (count > 32) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-#pragma unroll
-  for (int k = 0; k < kStatsPerLane; ++k) {
-    if (32 * k >= count) break;
-    const float f = exp2_fast(ml[k].x - top);
-    total += ml[k].y * f;
-    w[lane + 32 * k] = f;
+    for (int k = 1; k < kStatsPerLane; ++k) {
+      const float g = exp2_fast(ml[k].x - top);
+      total += ml[k].y * g;
+      w[lane + 32 * k] = g;
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, s);
   if (p.sinks != nullptr) total += exp2_fast(sink - top);
   *bad = __any_sync(0xFFFFFFFFu, any != 0);
-  *scale = total == 0.f ? 0.f : 1.f / total;
-  *lse = total == 0.f ? -INFINITY : (top + log2f(total)) / kLog2e;
+  *stats = make_float2(top, total);
   __syncwarp();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float f, const float4& part) {
-    acc.x += f * part.x;
-    acc.y += f * part.y;
-    acc.z += f * part.z;
-    acc.w += f * part.w;
+  auto add = [&](float g, const float4& part) {
+    acc.x += g * part.x;
+    acc.y += g * part.y;
+    acc.z += g * part.z;
+    acc.w += g * part.w;
   };
 #pragma unroll
   for (int k = 0; k < kFirst; ++k)
     if (from + k * step < count) add(w[from + k * step], o[k]);
-#pragma unroll 4
+#pragma unroll 2
   for (int j = from + kFirst * step; j < count; j += step) add(w[j], parts[d.part(j) * apart]);
   __syncwarp();  // w is free again
   return acc;
@@ -1457,12 +1467,13 @@ __device__ __forceinline__ float2 unit_stats(const AttendParams& p, int n, const
   return make_float2(top, total == 0.f ? 0.f : 1.f / total);
 }
 
-__device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row, int t, float4 v, float f, float lse) {
+__device__ __forceinline__ void store_joined(const AttendParams& p, int64_t row, int t, float4 v, float2 stats) {
+  const float f = stats.y == 0.f ? 0.f : 1.f / stats.y;
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * f, v.y * f);
   const __nv_bfloat162 b = __floats2bfloat162_rn(v.z * f, v.w * f);
   reinterpret_cast<uint2*>(p.out + row * kHeadDim)[t] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (t == 0) p.lse[row] = lse;
+  if (t == 0) p.lse[row] = stats.y == 0.f ? -INFINITY : (stats.x + log2f(stats.y)) / kLog2e;
 }
 
 // The weights of slots [length * sub / subs, length * (sub + 1) / subs) of request r.
@@ -1579,11 +1590,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
   mine.w = t;
   if (lane == 0) warp_joins[warp] = __popc(there);
   __syncthreads();
-  int before = __popc(there & ((1u << lane) - 1)), divided = 0;
-  for (int i = 0; i < kJoinThreads / 32; ++i) {
-    if (i < warp) before += warp_joins[i];
-    divided += warp_joins[i];
-  }
+  const int of_warp = lane < kJoinThreads / 32 ? warp_joins[lane] : 0;
+  const int divided = __reduce_add_sync(0xFFFFFFFFu, of_warp);
+  const int before = __popc(there & ((1u << lane) - 1)) + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of_warp : 0);
   const int block = static_cast<int>(blockIdx.x), all = static_cast<int>(gridDim.x);
   // that join: a third if the scores are more than a third of the parts' bytes, some
   // ctas + divided parts (100 x up to 2000 slots, 64 heads: 51.1 us, half 62.4; 24 x up
@@ -1602,10 +1611,10 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
       const int4 join = joins[unit / p.group_heads];
       const int col = unit % p.group_heads, head = join.y * p.group_heads + col;
       if (head >= p.num_heads) continue;
-      float f, lse;
+      float2 stats;
       bool bad;
       float4 v = join_parts(p, n, Division{join.z, join.w}, col, head, at, apart ? 0 : group, apart ? 1 : groups,
-                            part_weights[warp], &f, &lse, &bad);
+                            part_weights[warp], &stats, &bad);
       if (!apart) {
         sums[t] = v;
         __syncthreads();
@@ -1621,7 +1630,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) kvc_attend_join_
         __syncthreads();
       }
       if (!bad && (apart || group == 0))
-        store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, at, v, f, lse);
+        store_joined(p, static_cast<int64_t>(join.x) * p.num_heads + head, at, v, stats);
     }
   }
   if constexpr (!kWeights) {
