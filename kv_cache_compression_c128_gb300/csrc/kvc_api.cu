@@ -611,7 +611,7 @@ const char* kvc_error_string(kvc_status status) {
 }
 
 const char* kvc_version(void) {
-  return "kvc 0.4.0 sm_103a: cluster route (S=1..16, bf16/fp32 strided state, bulk-copy ring "
+  return "kvc 0.5.0 sm_103a: cluster route (S=1..16, bf16/fp32 strided state, bulk-copy ring "
          "96KiB, st.async merges) + stream-K route";
 }
 

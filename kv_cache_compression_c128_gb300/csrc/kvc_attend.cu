@@ -1,7 +1,7 @@
 // Attention of one new token per request over the packed slots of its pages.
 //
-// Slots n < length_r of request r decode to vectors k_n (exactly; each is the
-// key and the value of every head).  For head h:
+// Slots n < length_r of request r, of 8 bits or of 4, decode to vectors k_n (exactly;
+// each is the key and the value of every head).  For head h:
 //   s_n = scale * q_h . k_n,  L = log(sum_n exp(s_n) + exp(sink_h)),
 //   out_h = sum_n exp(s_n - L) k_n,  lse_h = L,
 // and, where the slots' weights are wanted,
@@ -24,13 +24,13 @@
 // and its products stay in range, so O is rescaled only where a score exceeds m
 // by 32, or at all on a page that holds values beyond 2^64.
 //
-// Warps of a CTA: 0..3 softmax and epilogue, two issue the products, one copies
-// the codes, one the queries, seven decode, one brings the RoPE words.  The codes
-// of a page come by TMA, a piece of 64 slots x 64 bytes for each scale group,
-// through a ring: 24 KB (N 64) or 56 KB stay on their way whatever the decode
-// does.  (Plain loads kept some 14 KB on the way, for the cache that they pass
-// through is what shared memory leaves of it: 193 us on 64 requests x 8192 slots
-// x 64 heads where the ring takes 125.)
+// Warps of a CTA: 0..3 softmax and epilogue, one issues each product (the first's
+// copies the queries too), one copies the codes, seven decode, two bring the RoPE
+// words in turn.  The codes of a page come by TMA, a piece of 64 slots x 64 codes for
+// each 64 dims, through a ring: of 8-bit slots 24 KB (N 64) or 56 KB stay on their way
+// whatever the decode does, of 4-bit ones 14 or 42.  (Plain loads kept some 14 KB on
+// the way, for the cache that they pass through is what shared memory leaves of it:
+// 193 us on 64 requests x 8192 slots x 64 heads, 8 bits, where the ring took 125.)
 //
 // The (request, head group) units are cut into shares of pages, one per CTA: a
 // unit to each where the longest takes hardly more than an equal share; else
@@ -44,15 +44,17 @@
 // What bounds it: a page's products take 1792 cycles at N = 64 and 1380 at 16,
 // all of them operand reads from shared memory at 128 bytes a cycle (measured
 // alone: 32 and 48 cycles for the M 64 and M 128 instruction at N 64, 23.5 and 39
-// at N 16).  The decode's stores and loads of the same memory add some 1000, and a
-// page takes about 4000 in all (2.1 us; 64 requests x 8192 slots x 64 heads: 125
-// us, 2.5 TB/s and 0.55 PFLOP/s): beside the products every other access of
-// shared memory is slow, a barrier's question 250 to 450 cycles.  Hence few
-// questions, one short issuing loop, rolled loops throughout (180 us with straight
-// code in every role, which does not stay in the instruction cache), and no more
-// places than one for each decoding warp.  Small calls are bound by latency: 64
-// slots of one request take 9 us, lengths, page ids, codes, two products and the
-// rows one after the other.
+// at N 16).  The decode's stores and loads of the same memory add some 700 to 1000,
+// and a page takes about 3000 in all; beside the products every other access of
+// shared memory is slow, a barrier's question 150 to 450 cycles.  Hence few
+// questions, short loops, rolled throughout (180 us with straight code in every
+// role, which does not stay in the instruction cache), and no more places than one
+// for each decoding warp.  64 requests x 8192 slots, sinks: 64 heads take 116.5 us of
+// 8-bit slots (306 MB, 2.6 TB/s, 0.59 PFLOP/s) and 106.1 of 4-bit ones (193 MB, 0.65
+// PFLOP/s): half the bytes save little.  Some 80 of these are pages; the rest are
+// the way to the first scores (6), rows and parts (8), and the joining kernel (10).
+// Small calls are bound by latency: 64 slots of one request take 8 us, length, page
+// ids, codes, two products and the rows one after the other.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
