@@ -133,9 +133,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def _build_call() -> None:
     """Compile csrc/kvc_call.cpp, the operators' calls as the interpreter's own functions.
-    Without the interpreter's or torch's headers the calls go through ctypes."""
-    import torch
-
+    Without torch, or its or the interpreter's headers, calls go through ctypes."""
+    try:
+        import torch
+    except ImportError:
+        return
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"), cuda]
