@@ -390,7 +390,8 @@ struct Walk {
 
 // Start of CTA c's share of `total` pages among `ctas`.
 __device__ __forceinline__ int share_start(int total, int c, int ctas) {
-  return static_cast<int>(static_cast<long long>(total) * c / ctas);
+  const int each = total / ctas, rest = total - each * ctas;  // (rest * c fits: at most 152 CTAs)
+  return each * c + rest * c / ctas;
 }
 
 // The CTA whose share holds page `at`.
@@ -1113,20 +1114,21 @@ __device__ void softmax_role(const AttendParams& p, AttendShared<N, F>& s, Walk 
 // 32 requests of up to 4000 slots take 33.7 us with equal shares and 25.8 with
 // these, 96 of up to 1500 35.6 and 28.2 (64 heads); 32 of up to 4000 at 16 heads
 // 24.3 and 21.0.  Every warp tries a number; `own` and `before` are the finder's
-// lanes'.  The search takes 1 us.
+// lanes'.  (Every whole division here is some 150 cycles of the way to the first page.)
 struct Shares {
   int each, count, finder, own, before;
 };
 template <int N>
-__device__ __forceinline__ Shares aligned_shares(const AttendParams& p, int4* scan, int lo, int hi, int total, int units,
-                                              int shortest, int grid) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, least = (total + grid - 1) / grid;
+__device__ __forceinline__ Shares aligned_shares(const AttendParams& p, int4* scan, int lo, int hi, int total, int equal,
+                                              int units, int shortest, int grid) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, least = equal + (equal * grid < total);
   Shares of = {0, 0, 0, 0, 0};
   // pages that it is worth: more for N = 64's longer end, and where a share could hold several short units
-  const int several = min(least / __reduce_min_sync(0xFFFFFFFFu, shortest), 2);
-  const int most = total / grid + (N == 64 ? 4 + 4 * several : 2);
+  shortest = __reduce_min_sync(0xFFFFFFFFu, shortest);
+  const int several = (least >= shortest) + (least >= 2 * shortest);
+  const int most = equal + (N == 64 ? 4 + 4 * several : 2);
   // a unit's last share is half empty on average: not tried where that is too much
-  if (total / most + units / 2 > grid) return of;
+  if (total >= static_cast<long long>(grid + 1 - units / 2) * most) return of;
 #pragma unroll 1
   for (int r = lo; r < hi; ++r) of.own += (pages_of(p, p.lengths[r]) + least + warp - 1) / (least + warp);
   const int all = __reduce_add_sync(0xFFFFFFFFu, of.own) * p.groups;
@@ -1229,9 +1231,10 @@ __device__ __forceinline__ void find_share(const AttendParams& p, AttendShared<N
   // A unit to each CTA, if the longest takes no more than kUndivided pages over
   // an equal share: no parts, nothing to join.
   int each = longest, own = mine_units, shares = units, finder = 0;
-  bool aligned = units <= grid && longest <= total / grid + kUndivided;
+  const int equal = total / grid;
+  bool aligned = units <= grid && longest <= equal + kUndivided;
   if (!aligned && few && units <= grid) {
-    const Shares found = aligned_shares<N>(p, s.scan, lo, hi, total, units, shortest, grid);
+    const Shares found = aligned_shares<N>(p, s.scan, lo, hi, total, equal, units, shortest, grid);
     aligned = found.each > 0;
     if (aligned) {
       each = found.each;
@@ -1255,10 +1258,12 @@ __device__ __forceinline__ void find_share(const AttendParams& p, AttendShared<N
       const int length = p.lengths[r], pages = pages_of(p, length);
       const int of_unit = aligned ? (pages + each - 1) / each : pages, size = of_unit * p.groups;
       if (off < size) {
+        int group = 0;
+        for (; off >= of_unit; off -= of_unit) ++group;  // of two at most
         s.start[0] = r;
         s.start[1] = length;
-        s.start[2] = off / of_unit;
-        s.start[3] = off % of_unit * (aligned ? each : 1);
+        s.start[2] = group;
+        s.start[3] = off * (aligned ? each : 1);
         break;
       }
       off -= size;
