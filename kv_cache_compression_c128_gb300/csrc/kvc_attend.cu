@@ -118,7 +118,8 @@ constexpr float kRescaleAbove = 32.f;                   // log2
 // can have) of them times 2^32 stay in range.  On a large page the reference
 // follows the maximum, so that no value is multiplied by more than 1.
 constexpr uint32_t kLargeScale = 184;                   // 128 x 2^(184 - 127) = 2^64
-constexpr int kJoinThreads = kAttendThreads, kJoinCtasPerSm = 2;
+constexpr int kJoinThreads = kAttendThreads, kLogJoinThreads = 9, kJoinCtasPerSm = 2;
+static_assert(kJoinThreads == 1 << kLogJoinThreads, "");
 constexpr int kStatsPerLane = (kAttendCtas + 31) / 32;  // of a unit's parts
 
 // Groups of a page whose codes come through the ring, one warp and depth()
@@ -1498,8 +1499,11 @@ __device__ __forceinline__ void form_weights(const AttendParams& p, WeightsShare
   // of the scores' size, and what its rounding loses would be a factor of every
   // weight, 2 % at scores of 1e5.)
   // A column to each kJoinThreads / score_cols threads (4 .. 32), which share its parts.
-  const int with = kJoinThreads / static_cast<int>(p.score_cols), col = t / with, first = t % with;
-  const int unit = col / n, c = col % n, head = unit * p.group_heads + c;
+  // (All these are powers of two: shifts, not divisions on the way to the first load.)
+  const int log_cols = 31 - __clz(static_cast<int>(p.score_cols)), log_with = kLogJoinThreads - log_cols;
+  const int with = 1 << log_with, col = t >> log_with, first = t & (with - 1);
+  const int unit = n == p.score_cols ? 0 : col >> (log_cols - 1), c = col & (n - 1);  // (two units at most)
+  const int head = unit * p.group_heads + c;
   const bool is_head = c < p.group_heads && head < p.num_heads;
   const int64_t length = p.lengths[r];
   int2 parts = make_int2(-1, 0);
@@ -1513,20 +1517,22 @@ __device__ __forceinline__ void form_weights(const AttendParams& p, WeightsShare
     if (sub == 0) write_empty(p, r);
     return;
   }
-  const int begin = static_cast<int>(length * sub / subs), end = static_cast<int>(length * (sub + 1) / subs);
+  const int each = static_cast<int>(length) / subs, rest = static_cast<int>(length) - each * subs;
+  const int begin = each * sub + (rest * sub) / subs, end = each * (sub + 1) + (rest * (sub + 1)) / subs;
   if (begin == end) return;
   // 4 columns a thread, `lanes` threads a slot
-  const int lanes = static_cast<int>(p.score_cols) / 4, step = kJoinThreads / lanes;
+  const int lanes = 1 << (log_cols - 2), step = kJoinThreads >> (log_cols - 2);
+  const int row = t >> (log_cols - 2), at = t & (lanes - 1);
   const float* const weights_in = p.weights_in == nullptr ? nullptr : p.weights_in + r * p.weights_in_row_stride;
   float* const weights_out = p.weights_out + r * p.weights_out_row_stride;
   const float4* const scores =
-      reinterpret_cast<const float4*>(p.scores + r * p.max_pages * kSlotsPerPage * p.score_cols) + t % lanes;
+      reinterpret_cast<const float4*>(p.scores + r * p.max_pages * kSlotsPerPage * p.score_cols) + at;
   float4 x[kAhead];
   float old[kAhead];
   auto fetch = [&](int from) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int slot = from + k * step + t / lanes;
+      const int slot = from + k * step + row;
       old[k] = 0.f;
       if (slot < end) {
         x[k] = scores[static_cast<int64_t>(slot) * lanes];
@@ -1552,18 +1558,18 @@ __device__ __forceinline__ void form_weights(const AttendParams& p, WeightsShare
   }
   __syncthreads();
   if (!s.skip) {
-    const float4 m = *reinterpret_cast<const float4*>(s.tops + 4 * (t % lanes));
-    const float4 f = *reinterpret_cast<const float4*>(s.shares + 4 * (t % lanes));
+    const float4 m = *reinterpret_cast<const float4*>(s.tops + 4 * at);
+    const float4 f = *reinterpret_cast<const float4*>(s.shares + 4 * at);
     for (int from = begin; from < end; from += kAhead * step) {  // a warp stays together
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int slot = from + k * step + t / lanes;
+        const int slot = from + k * step + row;
         float sum = 0.f;
         if (slot < end)
           sum = (f.x == 0.f ? 0.f : exp2_fast(x[k].x - m.x) * f.x) + (f.y == 0.f ? 0.f : exp2_fast(x[k].y - m.y) * f.y) +
                 (f.z == 0.f ? 0.f : exp2_fast(x[k].z - m.z) * f.z) + (f.w == 0.f ? 0.f : exp2_fast(x[k].w - m.w) * f.w);
         for (int d = lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (slot < end && t % lanes == 0) weights_out[slot] = old[k] + sum;
+        if (slot < end && at == 0) weights_out[slot] = old[k] + sum;
       }
       fetch(from + kAhead * step);
     }
