@@ -49,9 +49,9 @@
 // shared memory is slow, a barrier's question 150 to 450 cycles.  Hence few
 // questions, short loops, rolled throughout (180 us with straight code in every
 // role, which does not stay in the instruction cache), and no more places than one
-// for each decoding warp.  64 requests x 8192 slots, sinks: 64 heads take 116.5 us of
-// 8-bit slots (306 MB, 2.6 TB/s, 0.59 PFLOP/s) and 106.1 of 4-bit ones (193 MB, 0.65
-// PFLOP/s): half the bytes save little.  Some 80 of these are pages; the rest are
+// for each decoding warp.  64 requests x 8192 slots, sinks: 64 heads take 117 to
+// 118 us of 8-bit slots (306 MB, 2.6 TB/s, 0.58 PFLOP/s) and 104.8 of 4-bit ones (193 MB,
+// 0.66 PFLOP/s): fewer bytes save little.  Some 80 of these are pages; the rest are
 // the way to the first scores (6), rows and parts (8), and the joining kernel (10).
 // Small calls are bound by latency: 64 slots of one request take 8 us, length, page
 // ids, codes, two products and the rows one after the other.
@@ -1155,17 +1155,13 @@ __device__ __forceinline__ void write_empty(const AttendParams& p, int64_t r) {
 }
 
 // Where a CTA's share lies, in s; all threads.  A unit to each CTA where nothing can
-// be left to join (attend_alone): without a look at the other requests, and with the
-// unit's page ids asked for beside its length.
+// be left to join (attend_alone): without a look at the other requests.  (Page ids asked
+// for here, beside the length, change nothing: 1 x 64 slots 8.0 us with and without.)
 template <int N, typename F>
 __device__ __forceinline__ void take_unit(const AttendParams& p, AttendShared<N, F>& s) {
-  const int cta = blockIdx.x, req = cta / p.groups, t = threadIdx.x;
+  if (threadIdx.x != 0) return;
+  const int cta = blockIdx.x, req = cta / p.groups;
   const bool there = req < p.num_reqs;
-  if (there && t < kUndivided && t < p.max_pages) {
-    int32_t id;  // (into the cache that the copying warp then reads it from)
-    asm volatile("ld.global.s32 %0, [%1];" : "=r"(id) : "l"(p.page_table + req * p.page_table_row_stride + t));
-  }
-  if (t != 0) return;
   const int64_t length = there ? p.lengths[req] : 0;
   if (length < 0 || length > p.max_slots) atomicCAS(p.error, 0u, kErrBadIndex);
   const int pages = pages_of(p, length);

@@ -157,7 +157,8 @@ struct EvictParams {
 
 // Whether no lengths at all can leave anything to the joining kernel: there are
 // CTAs for all units, none long enough to be divided, and no weights to form.
-// (One request of 64 slots, 64 heads: 9.1 us, with both kernels 10.7; 8 of 128: 9.9, 11.3.)
+// (One request of 64 slots, 64 heads: 8.0 us, 8 of 128: 8.9.  With both kernels, before other
+// steps that shortened either way, 10.7 instead of 9.1, and 11.3 instead of 9.9.)
 bool attend_alone(const AttendParams& p, int ctas);
 cudaError_t launch_attend(const AttendParams& p, int columns, int ctas, cudaStream_t stream);
 cudaError_t launch_join(const JoinParams& p, cudaStream_t stream);

@@ -34,6 +34,7 @@ namespace kvc {
 namespace {
 
 constexpr int kWarps = 8;
+
 __device__ __forceinline__ uint32_t round2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
