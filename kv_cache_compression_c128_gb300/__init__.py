@@ -895,7 +895,7 @@ _known_axes = {None: (1, None)}  # of what `axes` was found right for: (axes tha
 
 def _axes(axes):
     """(axes that positions have at least, the 32 bytes of a C call)"""
-    pairs = bytes(axes)
+    pairs = bytes(list(axes))  # (bytes(32), and those of an array of 4 numbers of 8 bytes, are 32 zeros)
     if len(pairs) != 32:
         raise ValueError("axes must name an axis of positions for each of the 32 pairs")
     known = (max(pairs) + 1, pairs)

@@ -102,6 +102,22 @@ def test_wrappers_refuse_cpu_tensors(kvc):
         kvc.attend(torch.zeros((1, 8, 512), dtype=torch.bfloat16), kv, torch.zeros((1, 1), dtype=torch.int32), torch.ones(1, dtype=torch.int32))
 
 
+def test_axes_are_32_numbers_whatever_holds_them(kvc):
+    names = [0, 2, 1, 1] * 8
+    want = (3, bytes(names))
+    for held in (names, tuple(names), bytes(names), bytearray(names), iter(names), torch.tensor(names)):
+        assert kvc._axes(held) == want
+    for dtype in (np.uint8, np.int32, np.int64, ">i2"):
+        assert kvc._axes(np.array(names, dtype)) == want
+    # neither a number of axes nor 32 bytes of fewer numbers
+    for bad in (32, None, [0.0] * 32, "0" * 32):
+        with pytest.raises(TypeError):
+            kvc._axes(bad)
+    for bad in (np.zeros(4, np.int64), np.zeros(32 * 8, np.uint8), names[:31], [-1] * 32, [256] * 32):
+        with pytest.raises(ValueError):
+            kvc._axes(bad)
+
+
 def test_a_code_is_within_half_a_scale_and_uses_all_seven():
     rng = np.random.default_rng(1)
     x = (rng.standard_normal((300, 512)) * 10.0 ** rng.uniform(-3, 4, (300, 1))).astype(np.float32)
