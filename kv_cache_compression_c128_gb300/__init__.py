@@ -552,7 +552,8 @@ def kvc_evict_format(kv_cache, kv_format, num_kv_pages, page_table, num_reqs, ma
 def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
     """Read slots of a packed kv_cache back as [len(slots), 512] vectors
     (torch.float32 or torch.bfloat16) on the cache's device.  Pages of 23552
-    bytes hold 4-bit slots, others 8-bit ones."""
+    bytes hold 4-bit slots, pages of 37376 8-bit ones.  `out`, if given, is a
+    contiguous tensor of that dtype with room for len(slots) * 512 values."""
     torch = _torch or _load_torch()
     dtype = torch.float32 if dtype is None else dtype
     if out is not None and stream is None and _quick is not None and isinstance(out, torch.Tensor) and out.dtype == dtype:
@@ -575,7 +576,10 @@ def dequantize(kv_cache, slots, dtype=None, out=None, stream=None):
         _check(out, "out", dtype, kv_cache.device)
     shape = kv_cache.shape
     four = len(shape) == 2 and shape[1] == KV4_PAGE_BYTES
-    if four and out is not None and out.numel() < M * HEAD_DIM:
+    # (of 8-bit slots also pages in several dimensions: [num_pages, 64, 584])
+    if not shape or kv_cache.numel() != shape[0] * (KV4_PAGE_BYTES if four else KV_PAGE_BYTES):
+        raise ValueError(f"kv_cache must be [num_pages, {KV_PAGE_BYTES}] uint8, or [num_pages, {KV4_PAGE_BYTES}] of 4-bit slots")
+    if out is not None and out.numel() < M * HEAD_DIM:
         raise ValueError("out must hold len(slots) * 512 values")
 
     def call(raw):
