@@ -747,6 +747,17 @@ def compress_layers(state_caches, token_to_req, positions, boundary_token_indice
                         ("kv_slot_mapping", kv_slot_mapping, torch.int64)):
         _check(t, name, dt, dev)
     _check(block_table, "block_table", torch.int32, dev, contiguous=False)
+    if s0.shape[1] < block_size:
+        raise ValueError("state caches must have block_size rows a block")
+    if block_table.dim() != 2 or cos_sin_cache.dim() < 1 or cos_sin_cache.numel() < 64 * cos_sin_cache.shape[0]:
+        raise ValueError("block_table must be 2-D and cos_sin_cache [P, 64]")
+    if any(w.numel() < HEAD_DIM for w in rms_norm_weights):
+        raise ValueError("rms_norm_weights must have 512 elements each")
+    kv_shape = kv_caches[0].shape  # (pages of 4-bit slots are shorter than what is written)
+    if not kv_shape or kv_caches[0].numel() != kv_shape[0] * KV_PAGE_BYTES:
+        raise ValueError(f"kv_caches must be [num_pages, {KV_PAGE_BYTES}] uint8")
+    if token_to_req.numel() < positions.numel():
+        raise ValueError("token_to_req and positions must have one entry per token")
     N = boundary_token_indices.numel()
     if y_out is not None:
         _check(y_out, "y_out", torch.float32, dev)
