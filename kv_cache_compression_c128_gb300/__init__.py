@@ -12,6 +12,7 @@ from a KernelGen Optimization" (KernelGen Challenge 8 write-up), section
 from __future__ import annotations
 
 import ctypes
+import hashlib
 import importlib.machinery
 import importlib.util
 import os
@@ -27,7 +28,6 @@ _CSRC = os.path.join(_HERE, "csrc")
 _INCLUDE = os.path.join(_ROOT, "include")
 _LIB_DIR = os.path.join(_HERE, "_lib")
 LIB_PATH = os.path.join(_LIB_DIR, "libkvc.so")
-_CALL_PATH = os.path.join(_LIB_DIR, "_kvc_call.so")
 _SOURCES = ["kvc_cluster.cu", "kvc_streamk.cu", "kvc_reader.cu", "kvc_api.cu", "kvc_static.cu",
             "kvc_selftest.cu", "kvc_attend.cu", "kvc_join.cu", "kvc_evict.cu", "kvc_operators.cu",
             "kvc_store.cu", "kvc_rotate.cu"]
@@ -98,9 +98,10 @@ def _stale() -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/*.cu for sm_103a into _lib/libkvc.so (in-tree)."""
-    if not force and not _stale():
-        return LIB_PATH
     os.makedirs(_LIB_DIR, exist_ok=True)
+    if not force and not _stale():
+        _build_call()
+        return LIB_PATH
     nvcc = _nvcc()
     common = ARCH_FLAGS + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                            "-I", _INCLUDE]
@@ -117,7 +118,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return r.stderr
 
     with ThreadPoolExecutor(len(_SOURCES) + 1) as ex:
-        calls = ex.submit(_build_call)
+        calls = ex.submit(_build_call, force)
         logs = list(ex.map(compile_one, zip(_SOURCES, objs)))
         calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -131,30 +132,55 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB_PATH
 
 
-def _build_call() -> None:
-    """Compile csrc/kvc_call.cpp, the operators' calls as the interpreter's own functions.
-    Without torch, or its or the interpreter's headers, calls go through ctypes."""
+def _call_path(torch_dir):
+    """Where kvc_call.cpp's module lies that was built for this interpreter, the torch in
+    `torch_dir` and the entry points of these sources; None if these cannot be told.  It
+    reads tensors and passes arguments as the headers lay them out that it was built with:
+    one built beside others has another name, and is not loaded."""
+    tag = hashlib.sha256(str(sysconfig.get_config_var("SOABI")).encode())
     try:
-        import torch
-    except ImportError:
+        for path in (os.path.join(torch_dir, "version.py"), os.path.join(_CSRC, "kvc_call.cpp"),
+                     os.path.join(_INCLUDE, "kvc.h")):
+            with open(path, "rb") as f:
+                tag.update(hashlib.sha256(f.read()).digest())
+        for name in ("libc10.so", "libtorch_python.so"):
+            tag.update(b"%d " % os.path.getsize(os.path.join(torch_dir, "lib", name)))
+    except OSError:
+        return None
+    return os.path.join(_LIB_DIR, f"_kvc_call.{tag.hexdigest()[:16]}.so")
+
+
+def _build_call(force: bool = False) -> None:
+    """Compile csrc/kvc_call.cpp, the operators' calls as the interpreter's own functions,
+    unless it is there, and remove what was built beside other sources, another torch or
+    interpreter.  Without torch, or its or the interpreter's headers, calls go through ctypes."""
+    spec = importlib.util.find_spec("torch")
+    root = "" if spec is None or spec.origin is None else os.path.dirname(spec.origin)
+    path = _call_path(root)
+    for name in os.listdir(_LIB_DIR):
+        old = os.path.join(_LIB_DIR, name)
+        if name.startswith("_kvc_call.") and name.endswith(".so") and (force or old != path):
+            os.remove(old)
+    if path is None or os.path.exists(path):
         return
-    root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"), cuda]
     needed = ["Python.h", os.path.join("torch", "csrc", "autograd", "python_variable.h"), "cuda_runtime.h"]
     if not all(os.path.exists(os.path.join(d, f)) for d, f in zip(includes, needed)):
-        if os.path.exists(_CALL_PATH):
-            os.remove(_CALL_PATH)
+        return
+    try:
+        import torch
+    except ImportError:
         return
     libs = os.path.join(root, "lib")
-    tmp = _CALL_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     cmd += [f"-I{d}" for d in includes] + [os.path.join(_CSRC, "kvc_call.cpp"), "-o", tmp, "-L" + libs]
     cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + libs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for kvc_call.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, _CALL_PATH)
+    os.replace(tmp, path)
 
 
 # ---- loading -----------------------------------------------------------------
@@ -251,12 +277,13 @@ def lib():
 def _load_quick():
     """kvc_call.cpp's functions, where they were built (torch is loaded)."""
     global _quick
-    if _quick is None and os.path.exists(LIB_PATH) and os.path.exists(_CALL_PATH):
+    path = _call_path(os.path.dirname(_torch.__file__))
+    if _quick is None and path is not None and os.path.exists(LIB_PATH) and os.path.exists(path):
         try:
-            loader = importlib.machinery.ExtensionFileLoader("_kvc_call", _CALL_PATH)
+            loader = importlib.machinery.ExtensionFileLoader("_kvc_call", path)
             call = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvc_call", loader))
             loader.exec_module(call)
-        except ImportError:  # built beside another torch
+        except ImportError:  # (a library that it needs is gone)
             return
         L = lib()
         call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
