@@ -16,9 +16,11 @@ import hashlib
 import importlib.machinery
 import importlib.util
 import os
+import shutil
 import subprocess
 import sysconfig
 import threading
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from typing import Optional
 
@@ -120,13 +122,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(len(_SOURCES) + 1) as ex:
         calls = ex.submit(_build_call, force)
         logs = list(ex.map(compile_one, zip(_SOURCES, objs)))
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        r = subprocess.run([nvcc, "-shared"] + ARCH_FLAGS + objs + ["-o", tmp],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB_PATH)
         calls.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, "-shared"] + ARCH_FLAGS + objs + ["-o", tmp],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
     if verbose:
         print("".join(logs))
     return LIB_PATH
@@ -150,37 +152,58 @@ def _call_path(torch_dir):
     return os.path.join(_LIB_DIR, f"_kvc_call.{tag.hexdigest()[:16]}.so")
 
 
+def _call_command(root, out):
+    """The compiler's command that makes kvc_call.cpp's module of the torch in `root`; None
+    without a compiler, torch with CUDA, or a header or library of theirs."""
+    libs = os.path.join(root, "lib")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"), cuda]
+    needed = [os.path.join(includes[0], "Python.h"), os.path.join(cuda, "cuda_runtime.h"),
+              os.path.join(includes[1], "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(includes[1], "c10", "cuda", "impl", "cuda_cmake_macros.h")]
+    linked = ["c10", "c10_cuda", "torch_cpu", "torch_python"]
+    needed += [os.path.join(libs, f"lib{name}.so") for name in linked]
+    if shutil.which("g++") is None or not all(map(os.path.exists, needed)):
+        return None
+    try:
+        import torch
+    except (ImportError, OSError):
+        return None
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    cmd += [f"-I{d}" for d in includes] + [os.path.join(_CSRC, "kvc_call.cpp"), "-o", out, "-L" + libs]
+    return cmd + [f"-l{name}" for name in linked] + ["-Wl,-rpath," + libs]
+
+
 def _build_call(force: bool = False) -> None:
     """Compile csrc/kvc_call.cpp, the operators' calls as the interpreter's own functions,
     unless it is there, and remove what was built beside other sources, another torch or
-    interpreter.  Without torch, or its or the interpreter's headers, calls go through ctypes."""
+    interpreter.  Where that cannot be done, calls go through ctypes; a compiler that fails
+    is not asked again for the same sources and torch (but with force)."""
     spec = importlib.util.find_spec("torch")
     root = "" if spec is None or spec.origin is None else os.path.dirname(spec.origin)
     path = _call_path(root)
-    for name in os.listdir(_LIB_DIR):
-        old = os.path.join(_LIB_DIR, name)
-        if name.startswith("_kvc_call.") and name.endswith(".so") and (force or old != path):
-            os.remove(old)
-    if path is None or os.path.exists(path):
-        return
-    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-    includes = [sysconfig.get_paths()["include"], os.path.join(root, "include"), cuda]
-    needed = ["Python.h", os.path.join("torch", "csrc", "autograd", "python_variable.h"), "cuda_runtime.h"]
-    if not all(os.path.exists(os.path.join(d, f)) for d, f in zip(includes, needed)):
-        return
+    failed = f"{path}.failed"
     try:
-        import torch
-    except ImportError:
-        return
-    libs = os.path.join(root, "lib")
-    tmp = path + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
-    cmd += [f"-I{d}" for d in includes] + [os.path.join(_CSRC, "kvc_call.cpp"), "-o", tmp, "-L" + libs]
-    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + libs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for kvc_call.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, path)
+        for name in os.listdir(_LIB_DIR):
+            old = os.path.join(_LIB_DIR, name)
+            if name.startswith("_kvc_call.") and name.endswith((".so", ".failed")) and (force or old not in (path, failed)):
+                os.remove(old)
+        if path is None or os.path.exists(path) or os.path.exists(failed):
+            return
+        tmp = path + f".tmp{os.getpid()}"
+        cmd = _call_command(root, tmp)
+        if cmd is None:
+            return
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, path)
+            return
+        said = f"{r.stdout}\n{r.stderr}"
+        with open(failed, "w") as f:
+            f.write(said)
+    except OSError as e:
+        said = str(e)
+    warnings.warn(f"kvc_call.cpp was not compiled, calls go through ctypes:\n{said}", RuntimeWarning)
 
 
 # ---- loading -----------------------------------------------------------------

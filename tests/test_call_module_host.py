@@ -1,5 +1,6 @@
 """The module of the operators' calls: a module that was built beside another torch,
-interpreter or library is not loaded, and does not stay."""
+interpreter or library is not loaded, and does not stay; the library is built whether or
+not the module can be."""
 import os
 import shutil
 import subprocess
@@ -128,3 +129,54 @@ def test_the_module_here_refuses_in_words():
     with pytest.raises(ValueError, match="no CPU path"):
         kvc.dequantize(torch.zeros((2, kvc.KV_PAGE_BYTES), dtype=torch.uint8), torch.zeros(3, dtype=torch.int64),
                        torch.float32, out=torch.zeros((3, 512)))
+
+
+@pytest.mark.parametrize("how", ["fails", "no compiler", "nothing to run"])
+def test_the_library_is_built_without_the_module(place, monkeypatch, how):
+    ran = []
+
+    def run(cmd, **_):
+        ran.append(cmd[0])
+        if cmd[0] == "g++":
+            if how == "nothing to run":
+                raise FileNotFoundError("g++")
+            return subprocess.CompletedProcess(cmd, 1, "", "cannot find -lc10_cuda")
+        open(cmd[cmd.index("-o") + 1], "wb").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(kvc.subprocess, "run", run)
+    if how == "no compiler":
+        monkeypatch.setattr(shutil, "which", lambda name: None)
+    (place / "libkvc.so").unlink()
+    if how == "no compiler":
+        assert kvc.build() == kvc.LIB_PATH
+    else:
+        with pytest.warns(RuntimeWarning, match="calls go through ctypes"):
+            assert kvc.build() == kvc.LIB_PATH
+    assert os.path.exists(kvc.LIB_PATH) and not [f for f in _modules(place) if f.endswith(".so")]
+    asked = ran.count("g++")
+    assert asked == (how != "no compiler")
+    if how == "fails":  # not asked again, until something changes
+        kvc.build()
+        assert ran.count("g++") == asked
+        with pytest.warns(RuntimeWarning, match="c10_cuda"):
+            kvc.build(force=True)
+        assert ran.count("g++") == asked + 1
+
+
+@pytest.mark.parametrize("gone", ["lib/libc10_cuda.so", "include/c10/cuda/impl/cuda_cmake_macros.h", "lib/libtorch_cpu.so"])
+def test_no_compiler_is_asked_beside_a_torch_without_cuda(place, compiled, monkeypatch, gone):
+    there = os.path.exists
+    monkeypatch.setattr(kvc.os.path, "exists", lambda path: path != os.path.join(TORCH, *gone.split("/")) and there(path))
+    kvc.build()
+    assert not compiled and not _modules(place)
+
+
+def test_a_place_that_cannot_be_written_keeps_its_library(place, compiled, monkeypatch):
+    def remove(path):
+        raise PermissionError(path)
+
+    (place / "_kvc_call.so").write_bytes(b"")
+    monkeypatch.setattr(kvc.os, "remove", remove)
+    with pytest.warns(RuntimeWarning):
+        assert kvc.build() == kvc.LIB_PATH
