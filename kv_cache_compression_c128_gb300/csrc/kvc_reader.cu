@@ -14,6 +14,10 @@
 // Large calls (more slot pairs than fit on the device at once): one warp per
 // slot on a persistent grid, 4 (fp32 output) or 2 (bf16) slots per warp in
 // flight, every load and store coalesced.  584 bytes read and 1 or 2 KiB written per slot.
+//
+// Slots and their indices are read with ordinary loads, not the read-only path's: a
+// kernel here may be resident while the one ahead of it on the stream, which releases its
+// dependents at its start, still writes them, so they are not read-only for its lifetime.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -80,7 +84,7 @@ struct Piece {
   bool ok;         // the slot is read (non-negative and on a page)
 };
 
-__device__ __forceinline__ Piece load_piece(const uint8_t* __restrict__ kv, int64_t num_pages,
+__device__ __forceinline__ Piece load_piece(const uint8_t* kv, int64_t num_pages,
                                             int64_t slot, int d0, int t, uint32_t* err) {
   Piece pc{0u, make_uint2(0u, 0u), 0u, false};
   if (slot < 0) return pc;
@@ -92,10 +96,10 @@ __device__ __forceinline__ Piece load_piece(const uint8_t* __restrict__ kv, int6
   const uint8_t* pg = kv + page * kPageBytes;
   const uint8_t* payload = pg + off * kTokenStride;
   if (d0 < kNopeDim) {
-    pc.codes = __ldg(reinterpret_cast<const uint32_t*>(payload + d0));
-    pc.b = __ldg(pg + kScaleBase + off * kScaleDim + d0 / kGroup);
+    pc.codes = *reinterpret_cast<const uint32_t*>(payload + d0);
+    pc.b = pg[kScaleBase + off * kScaleDim + d0 / kGroup];
   } else {
-    pc.raw = __ldg(reinterpret_cast<const uint2*>(payload + kNopeDim + 2 * (d0 - kNopeDim)));
+    pc.raw = *reinterpret_cast<const uint2*>(payload + kNopeDim + 2 * (d0 - kNopeDim));
   }
   pc.ok = true;
   return pc;
@@ -132,8 +136,8 @@ __device__ __forceinline__ void store_piece(const Piece& pc, int d0, int t, int6
 // slot pairs): one slot per 128-thread lane.
 template <int kUnroll>
 __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_kernel(
-    const uint8_t* __restrict__ kv, int64_t num_pages, const int64_t* __restrict__ slots,
-    int64_t num_slots, void* __restrict__ out, int out_bf16, uint32_t* err) {
+    const uint8_t* kv, int64_t num_pages, const int64_t* slots,
+    int64_t num_slots, void* out, int out_bf16, uint32_t* err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane_slot = threadIdx.x / kThreadsPerSlot;
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_kernel(
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t m = base + u * width;
-      sl[u] = m < num_slots ? __ldg(slots + m) : -1;
+      sl[u] = m < num_slots ? slots[m] : -1;
     }
     Piece pc[kUnroll];
 #pragma unroll
@@ -173,8 +177,8 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_kernel(
 // that are not read back soon.
 template <int kUnroll, bool kStream>
 __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_warp_kernel(
-    const uint8_t* __restrict__ kv, int64_t num_pages, const int64_t* __restrict__ slots,
-    int64_t num_slots, void* __restrict__ out, int out_bf16, uint32_t* err) {
+    const uint8_t* kv, int64_t num_pages, const int64_t* slots,
+    int64_t num_slots, void* out, int out_bf16, uint32_t* err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kWarps = kReaderThreads / 32;
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_warp_kernel(
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t m = base + u * width;
-      sl[u] = m < num_slots ? __ldg(slots + m) : -1;
+      sl[u] = m < num_slots ? slots[m] : -1;
     }
     uint32_t codes[kUnroll][4];
     uint2 scale[kUnroll], rope[kUnroll];
@@ -206,14 +210,14 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_warp_kernel(
       }
       const uint8_t* pg = kv + page * kPageBytes;
       const uint8_t* payload = pg + off * kTokenStride;
-      scale[u] = __ldg(reinterpret_cast<const uint2*>(pg + kScaleBase + off * kScaleDim));
+      scale[u] = *reinterpret_cast<const uint2*>(pg + kScaleBase + off * kScaleDim);
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        codes[u][k] = __ldg(reinterpret_cast<const uint32_t*>(payload + 4 * lane + 128 * k));
+        codes[u][k] = *reinterpret_cast<const uint32_t*>(payload + 4 * lane + 128 * k);
       if (!rope_lane)
-        codes[u][3] = __ldg(reinterpret_cast<const uint32_t*>(payload + 4 * lane + 384));
+        codes[u][3] = *reinterpret_cast<const uint32_t*>(payload + 4 * lane + 384);
       else
-        rope[u] = __ldg(reinterpret_cast<const uint2*>(payload + kNopeDim + 8 * (lane - 16)));
+        rope[u] = *reinterpret_cast<const uint2*>(payload + kNopeDim + 8 * (lane - 16));
       ok[u] = true;
     }
 #pragma unroll
@@ -269,8 +273,8 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_warp_kernel(
 // 4-dims-per-lane layout.  Same values, bit for bit.
 template <int kUnroll>
 __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_wide16_kernel(
-    const uint8_t* __restrict__ kv, int64_t num_pages, const int64_t* __restrict__ slots,
-    int64_t num_slots, uint16_t* __restrict__ out, uint32_t* err) {
+    const uint8_t* kv, int64_t num_pages, const int64_t* slots,
+    int64_t num_slots, uint16_t* out, uint32_t* err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kWarps = kReaderThreads / 32;
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_wide16_kernel(
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t m = base + u * width;
-      sl[u] = m < num_slots ? __ldg(slots + m) : -1;
+      sl[u] = m < num_slots ? slots[m] : -1;
     }
     uint2 codes[kUnroll][2], scale[kUnroll];
     uint4 rope[kUnroll];
@@ -301,12 +305,12 @@ __global__ void __launch_bounds__(kReaderThreads) kvc_dequant_wide16_kernel(
       }
       const uint8_t* pg = kv + page * kPageBytes;
       const uint8_t* payload = pg + off * kTokenStride;
-      scale[u] = __ldg(reinterpret_cast<const uint2*>(pg + kScaleBase + off * kScaleDim));
-      codes[u][0] = __ldg(reinterpret_cast<const uint2*>(payload + 8 * lane));
+      scale[u] = *reinterpret_cast<const uint2*>(pg + kScaleBase + off * kScaleDim);
+      codes[u][0] = *reinterpret_cast<const uint2*>(payload + 8 * lane);
       if (!rope_lane)
-        codes[u][1] = __ldg(reinterpret_cast<const uint2*>(payload + 256 + 8 * lane));
+        codes[u][1] = *reinterpret_cast<const uint2*>(payload + 256 + 8 * lane);
       else
-        rope[u] = __ldg(reinterpret_cast<const uint4*>(payload + kNopeDim + 16 * (lane - 24)));
+        rope[u] = *reinterpret_cast<const uint4*>(payload + kNopeDim + 16 * (lane - 24));
       ok[u] = true;
     }
 #pragma unroll
