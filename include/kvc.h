@@ -365,7 +365,8 @@ kvc_status kvc_store(const void* x, int32_t x_dtype, int64_t x_row_stride, int64
  * x, out       bf16 or fp32 (dtype): row (t, h) of 64 elements at t *
  *              token_stride + h * head_stride (elements; multiples of 16 bytes,
  *              >= 0), 16-byte aligned.  The rows of out do not overlap; out may be
- *              x itself, at the same strides.
+ *              x itself, at the same strides, and shares no byte of a row with
+ *              x's rows else (KVC_ERR_INVALID_ARG).
  * positions    int64, entry (t, axis) at t * positions_token_stride + axis *
  *              positions_axis_stride (>= 0).
  * num_axes     1 .. 4.

@@ -1056,8 +1056,8 @@ def rotate(x, positions, cos_sin_cache, *, axes=None, inverse: bool = False, out
 
     `inverse` turns by the opposite angles: attention's rows back, whose last 64
     dims are sums of rotated ones, and the gradient with respect to x from the
-    one with respect to the result.  Returns `out`, which may be x itself (a new
-    contiguous tensor if None).  A position outside the table leaves its token's
+    one with respect to the result.  Returns `out`, which may be x itself, and whose
+    rows share no memory with x's else (a new contiguous tensor if None).  A position outside the table leaves its token's
     rows of out as they were and raises the device error word.  No gradient is
     recorded.
     """

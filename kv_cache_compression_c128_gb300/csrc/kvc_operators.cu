@@ -12,6 +12,7 @@
 #include "../../include/kvc.h"
 #include "kvc_internal.h"
 #include "kvc_operators.h"
+#include "kvc_overlap.h"
 
 namespace {
 
@@ -420,6 +421,12 @@ kvc_status kvc_rotate(const void* x, int32_t dtype, int64_t x_token_stride, int6
       !heads_apart(num_tokens, out_token_stride, num_heads, out_head_stride))
     return KVC_ERR_INVALID_ARG;
   if (num_tokens > INT32_MAX) return KVC_ERR_UNSUPPORTED;  // (a launch has no more CTAs)
+  // in place, or apart: else rows would be read that others have been turned into
+  const bool in_place = x == out && (num_tokens == 1 || x_token_stride == out_token_stride) &&
+                        (num_heads == 1 || x_head_stride == out_head_stride);
+  if (!in_place && kvc::rows_meet(x, {x_token_stride, x_head_stride}, out, {out_token_stride, out_head_stride}, num_tokens, num_heads,
+                                  kvc::kRopeDim, p.f32 ? 4 : 2))
+    return KVC_ERR_INVALID_ARG;
   int sms = 0;
   long long wait_limit = 0;
   const kvc_status st = kvc::operator_device(&sms, &p.error, &wait_limit);
