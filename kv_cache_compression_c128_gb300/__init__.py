@@ -11,6 +11,7 @@ from a KernelGen Optimization" (KernelGen Challenge 8 write-up), section
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import hashlib
 import importlib.machinery
@@ -187,7 +188,8 @@ def _build_call(force: bool = False) -> None:
         for name in os.listdir(_LIB_DIR):
             old = os.path.join(_LIB_DIR, name)
             if name.startswith("_kvc_call.") and name.endswith((".so", ".failed")) and (force or old not in (path, failed)):
-                os.remove(old)
+                with contextlib.suppress(FileNotFoundError):  # (another process was quicker)
+                    os.remove(old)
         if path is None or os.path.exists(path) or os.path.exists(failed):
             return
         tmp = path + f".tmp{os.getpid()}"

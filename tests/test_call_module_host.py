@@ -180,3 +180,13 @@ def test_a_place_that_cannot_be_written_keeps_its_library(place, compiled, monke
     monkeypatch.setattr(kvc.os, "remove", remove)
     with pytest.warns(RuntimeWarning):
         assert kvc.build() == kvc.LIB_PATH
+
+
+def test_two_processes_that_remove_the_same_file(place, compiled, monkeypatch):
+    def remove(path):
+        raise FileNotFoundError(path)
+
+    (place / "_kvc_call.so").write_bytes(b"")
+    monkeypatch.setattr(kvc.os, "remove", remove)
+    kvc.build()
+    assert os.path.exists(kvc._call_path(TORCH)) and len(compiled) == 1
