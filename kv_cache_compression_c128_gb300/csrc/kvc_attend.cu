@@ -50,7 +50,7 @@
 // questions, short loops, rolled throughout (180 us with straight code in every
 // role, which does not stay in the instruction cache), and no more places than one
 // for each decoding warp.  64 requests x 8192 slots, sinks: 64 heads take 117 to
-// 118 us of 8-bit slots (306 MB, 2.6 TB/s, 0.58 PFLOP/s) and 104.8 of 4-bit ones (193 MB,
+// 118 us of 8-bit slots (306 MB, 2.6 TB/s, 0.58 PFLOP/s) and 105 of 4-bit ones (193 MB,
 // 0.66 PFLOP/s): fewer bytes save little.  Some 80 of these are pages; the rest are
 // the way to the first scores (6), rows and parts (8), and the joining kernel (10).
 // Small calls are bound by latency: 64 slots of one request take 8 us, length, page

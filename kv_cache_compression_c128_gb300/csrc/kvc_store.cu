@@ -12,11 +12,13 @@
 // A warp has a row: lane l dims 8 l .. + 7, 256 + 8 l .. + 7 and pair l of the rotated
 // ones, so that every load and store covers one run of the row, a scale group is 4 or
 // 8 lanes, and each lane asks for one angle.  Large calls are bound by the rows in and
-// the slots out: 65537 fp32 rows to 8-bit slots take 25.8 us (99 % of the copy
-// bandwidth), to 4-bit ones turned to one axis 26.9 (97 %); bf16 rows to 4 bits with
-// three axes 19.1 (85 %), which is near what its instructions take to issue.  (Two rows
-// a warp: 29.8, 30.1, 21.7.  Codes by division, angles by the eight lanes of the
-// rotated dims: 340 instructions a row, 26.7 us for the last.)
+// the slots out: 65537 fp32 rows to 8-bit slots in order take 26.7 us (96 % of the copy
+// bandwidth), to 4-bit ones turned to one axis 27.5 (95 %); bf16 rows to 4 bits with
+// three axes 18.9 (86 %), which is near what its instructions take to issue, to 8 bits
+// as they are 19.0 (82 %); three inputs in turn, replayed.  (Two rows a warp, in a run that
+// took 25.8, 26.9 and 19.1 for the first three: 29.8, 30.1, 21.7.  Codes by division,
+// angles by the eight lanes of the rotated dims: 340 instructions a row, 26.7 us for the
+// third.)
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
